@@ -4,7 +4,9 @@
  * The library implements the data-parallel hot path of one decode step over a paged KV
  * cache: the append of each request's new K/V, the attention of each request's single
  * query token over its whole cached history, and the gather of one request's scattered
- * KV blocks into a contiguous buffer for transfer.
+ * KV blocks into a contiguous buffer for transfer. For the step that comes before it, the
+ * new tokens of prompts, prompt chunks or drafts, it holds the attention of a chunk over the
+ * same cache and the block tables and slots built on the GPU from the requests' lengths.
  *
  * Conventions shared by every entry point:
  *  - Every pointer argument is a DEVICE pointer unless its comment says "host". The caller
@@ -72,6 +74,8 @@ typedef enum {
 #define PDA_DEVERR_BLOCK_ID 0x2    /* a block id needed by a request is outside [0, num_blocks) */
 #define PDA_DEVERR_SLOT 0x4        /* slot_mapping[b] >= num_blocks * block_size */
 #define PDA_DEVERR_TIMEOUT 0x8     /* a pipeline wait passed its time limit; results invalid */
+#define PDA_DEVERR_QUERY 0x10      /* query_lens / query_start negative, decreasing or beyond T */
+#define PDA_DEVERR_NO_BLOCKS 0x20  /* free_count out of range, or too few free blocks */
 
 /* Bytes of the fixed device scratch behind pda_paged_decode_attention_noalloc. */
 #define PDA_NOALLOC_SCRATCH_BYTES (8u << 20)
@@ -453,6 +457,140 @@ pda_status pda_kv_unpack_block_scales_batched(const void* const* ins,
                                               void* k_scales, void* v_scales, int H_kv, int D,
                                               int block_size, int num_blocks,
                                               int32_t* error_word, cudaStream_t stream);
+
+/*
+ * pda_kv_assign_blocks -- grow and shrink every request's block table to its length, taking
+ * blocks from a free list and giving them back, on the GPU.
+ *
+ * Blocks are handed out as tokens arrive (page "From PagedAttention to Prefill-Decode
+ * disaggregation", sec. 2.2 step 3); the pages give no free list. Here it is a stack:
+ * free_list[0 .. free_count) holds the ids of the free blocks, the last one on top. With
+ * need_b = ceil(context_lens[b] / block_size):
+ *  - a row that holds more than it needs gives back entries [need_b, blocks_held[b]) of its
+ *    table; all rows' entries are pushed in order of b, then of the entry;
+ *  - after that, a row that holds fewer gets entries [blocks_held[b], need_b), popped one at
+ *    a time in the same order. The first row whose blocks are not all there, and every later
+ *    row that grows, get none (PDA_DEVERR_NO_BLOCKS); their counts stay.
+ *
+ *  block_tables   [B, max_blocks_per_seq] int32, updated in place. Entries given back are
+ *                 left in the table, behind the row's new end.
+ *  blocks_held    [B] int32: entries of each row in use; blocks_held_out [B] receives the
+ *                 new counts. The two may be the same buffer.
+ *  free_list      [num_blocks] int32, updated in place; entries above the new count are
+ *                 unspecified but in place (popped entries are not cleared).
+ *  free_count     [1] int32; free_count_out [1] receives the new count; may be the same.
+ *  context_lens   [B] int32: the length each row must cover; 0 gives every block back.
+ *  shared_blocks  [B] int32 or NULL: the row's first shared_blocks[b] entries belong to
+ *                 somebody else (a prefix that several rows share) and are never given back.
+ *                 No other block may be in two rows, or it is given back twice.
+ *  A row with context_lens < 0 or beyond max_blocks_per_seq * block_size, or with blocks_held
+ *  outside [0, max_blocks_per_seq], is left as it is (PDA_DEVERR_CONTEXT_LEN). free_count
+ *  outside [0, num_blocks] (PDA_DEVERR_NO_BLOCKS), or more blocks given back than the list
+ *  holds (PDA_DEVERR_BLOCK_ID), leaves everything as it is. An id out of range that is moved
+ *  sets PDA_DEVERR_BLOCK_ID. Buffers not named as shareable must not overlap.
+ *  B <= 8192 and B * max_blocks_per_seq < 2^31, else PDA_ERR_UNSUPPORTED. B == 0 copies the
+ *  count.
+ */
+pda_status pda_kv_assign_blocks(int32_t* block_tables, const int32_t* blocks_held,
+                                int32_t* blocks_held_out, int32_t* free_list,
+                                const int32_t* free_count, int32_t* free_count_out,
+                                const int32_t* context_lens, const int32_t* shared_blocks, int B,
+                                int max_blocks_per_seq, int block_size, int num_blocks,
+                                int32_t* error_word, cudaStream_t stream);
+
+/*
+ * pda_kv_build_slots -- the cache slot of every new token, and where each request's tokens
+ * start, from the requests' lengths, on the GPU.
+ *
+ * The slot that pda_kv_append takes comes from the block table (page "From PagedAttention to
+ * Prefill-Decode disaggregation", sec. 2.2 step 3). Request b brings n = query_lens[b] new
+ * tokens, the last of its L = context_lens[b]; they are rows query_start[b] ..
+ * query_start[b + 1) of the step's tokens. Token i is at position p = L - n + i:
+ *      slot_mapping[query_start[b] + i] = block_tables[b][p / block_size] * block_size
+ *                                         + p % block_size.
+ *
+ *  slot_mapping   [N] int32, written whole: rows behind the last token get -1 (padding).
+ *  query_start    [B + 1] int32, written: exclusive prefix sum of query_lens, clipped at N.
+ *  query_lens     [B] int32; context_lens [B] int32; block_tables [B, max_blocks_per_seq].
+ *  More than N tokens, or a negative query_lens (taken as 0), sets PDA_DEVERR_QUERY.
+ *  L < 0, L beyond the table, or 0 < L < n gives the request's tokens -1 and sets
+ *  PDA_DEVERR_CONTEXT_LEN; L == 0 gives -1 without an error (a padded row). A block id out
+ *  of range gives -1 and PDA_DEVERR_BLOCK_ID. Outputs must not overlap inputs.
+ *  B <= 8192, N <= 2^30, B * max_blocks_per_seq < 2^31, else PDA_ERR_UNSUPPORTED.
+ */
+pda_status pda_kv_build_slots(int32_t* slot_mapping, int32_t* query_start,
+                              const int32_t* query_lens, const int32_t* context_lens,
+                              const int32_t* block_tables, int N, int B, int max_blocks_per_seq,
+                              int block_size, int num_blocks, int32_t* error_word,
+                              cudaStream_t stream);
+
+/*
+ * pda_chunk_attention_workspace_size -- bytes of device workspace pda_paged_chunk_attention
+ * (or _fp8, with PDA_FP8_E4M3) needs on the current device for these sizes. The bound does
+ * not depend on the lengths. Written to *bytes (host).
+ */
+pda_status pda_chunk_attention_workspace_size(int B, int T, int H, int H_kv, int D,
+                                              int block_size, pda_dtype kv_dtype, int sm_cap,
+                                              size_t* bytes);
+
+/*
+ * pda_paged_chunk_attention -- every new token of each request attends over the request's
+ * cached history up to and including itself.
+ *
+ * The attention of a prompt, of a chunk of a long prompt (the pages' chunked prefill), of
+ * the rest of a prompt behind a shared prefix (page "From PagedAttention to Prefill-Decode
+ * disaggregation", sec. 2.3) or of drafted tokens, after their K and V have been appended
+ * (pda_kv_append takes any number of tokens). Request b has n = query_start[b + 1] -
+ * query_start[b] new tokens, the last of its L = context_lens[b]. For token i, at position
+ * p = L - n + i, and head h with kv-head k = h / (H / H_kv):
+ *      s_t = scale * q . K_t[k],  t <= p
+ *      out = sum_t softmax(s)_t * V_t[k].
+ * n == 1 is pda_paged_decode_attention's row.
+ *
+ *  out, q         [T, H, D] in q_dtype: the step's tokens, request after request. Rows
+ *                 outside [query_start[0], query_start[B]) are neither computed nor written.
+ *  query_start    [B + 1] int32 (device), non-decreasing, within [0, T].
+ *  context_lens   [B] int32 (device). L == 0 gives zero rows (a padded request). L < 0,
+ *                 L > max_context_len, L > max_blocks_per_seq * block_size or 0 < L < n
+ *                 gives NaN rows and PDA_DEVERR_CONTEXT_LEN.
+ *  A request whose pair of query_start is decreasing or outside [0, T] is left out
+ *  (PDA_DEVERR_QUERY). A block id out of range gives NaN in the rows that see the block and
+ *  PDA_DEVERR_BLOCK_ID.
+ *  What the cache holds behind a row's position (later tokens, rows behind L, unused blocks)
+ *  does not reach that row's output, NaN and infinities included.
+ *  q_dtype must equal kv_dtype (PDA_F32, PDA_BF16 or PDA_F16); out has the same type.
+ *  fp32 is computed in fp32; bf16 and fp16 on the tensor cores with fp32 accumulation and
+ *  softmax, the probabilities rounded to the cache's type.
+ *  workspace      device scratch of at least pda_chunk_attention_workspace_size(...) bytes,
+ *                 256-byte aligned, not shared by calls that may run concurrently; its
+ *                 content before and after a call means nothing.
+ *  The other arguments, the supported sizes (D, block_size, H / H_kv, B) and alignment are
+ *  those of pda_paged_decode_attention; T * H < 2^31.
+ */
+pda_status pda_paged_chunk_attention(void* out, const void* q, const void* k_cache,
+                                     const void* v_cache, const int32_t* block_tables,
+                                     int max_blocks_per_seq, const int32_t* context_lens,
+                                     const int32_t* query_start, int max_context_len, int B,
+                                     int T, int H, int H_kv, int D, int block_size,
+                                     int num_blocks, float scale, pda_dtype q_dtype,
+                                     pda_dtype kv_dtype, int sm_cap, void* workspace,
+                                     size_t workspace_bytes, int32_t* error_word,
+                                     cudaStream_t stream);
+
+/*
+ * pda_paged_chunk_attention_fp8 -- pda_paged_chunk_attention over an FP8 E4M3 cache: stored
+ * code c of K means decode(c) * k_scale, of V decode(c) * v_scale (finite per-tensor scales).
+ * Codes are widened exactly; q and out are PDA_BF16, and the products run as for a bf16 cache.
+ */
+pda_status pda_paged_chunk_attention_fp8(void* out, const void* q, const void* k_cache,
+                                         const void* v_cache, const int32_t* block_tables,
+                                         int max_blocks_per_seq, const int32_t* context_lens,
+                                         const int32_t* query_start, int max_context_len, int B,
+                                         int T, int H, int H_kv, int D, int block_size,
+                                         int num_blocks, float scale, float k_scale,
+                                         float v_scale, pda_dtype q_dtype, int sm_cap,
+                                         void* workspace, size_t workspace_bytes,
+                                         int32_t* error_word, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,7 @@ from . import build_lib
  PDA_ERR_TOO_LARGE) = range(6)
 PDA_F32, PDA_BF16, PDA_FP8_E4M3, PDA_NVFP4, PDA_F16 = 0, 1, 2, 3, 4
 PDA_DEVERR_CONTEXT_LEN, PDA_DEVERR_BLOCK_ID, PDA_DEVERR_SLOT, PDA_DEVERR_TIMEOUT = 1, 2, 4, 8
+PDA_DEVERR_QUERY, PDA_DEVERR_NO_BLOCKS = 0x10, 0x20
 PDA_PACK_MAX_BATCH = 64
 PDA_PACK_MAX_LAYERS = 256
 PDA_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -30,7 +31,9 @@ EXPORTED = [
     "pda_kv_unpack_blocks", "pda_kv_unpack_blocks_batched", "pda_paged_decode_attention_fp8",
     "pda_paged_decode_attention_nvfp4", "pda_kv_pack_layers", "pda_kv_unpack_layers",
     "pda_kv_append_block_scales", "pda_kv_pack_block_scales_batched",
-    "pda_kv_unpack_block_scales_batched",
+    "pda_kv_unpack_block_scales_batched", "pda_kv_assign_blocks", "pda_kv_build_slots",
+    "pda_chunk_attention_workspace_size", "pda_paged_chunk_attention",
+    "pda_paged_chunk_attention_fp8",
 ]
 
 _lock = threading.Lock()
@@ -100,6 +103,23 @@ def load():
         lib.pda_kv_pack_block_scales_batched.restype = I
         lib.pda_kv_unpack_block_scales_batched.argtypes = [P, P, P, I, P, P, I, I, I, I, P, P]
         lib.pda_kv_unpack_block_scales_batched.restype = I
+        # tables, held, held_out, free list, count, count_out, lens, shared, B, max_blocks, bs,
+        # NB, error_word, stream
+        lib.pda_kv_assign_blocks.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, P, P]
+        lib.pda_kv_assign_blocks.restype = I
+        lib.pda_kv_build_slots.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P]
+        lib.pda_kv_build_slots.restype = I
+        lib.pda_chunk_attention_workspace_size.argtypes = [I, I, I, I, I, I, I, I,
+                                                           ctypes.POINTER(SZ)]
+        lib.pda_chunk_attention_workspace_size.restype = I
+        # out, q, k, v, tables, max_blocks, lens, query_start, max_context_len, B, T, H, H_kv,
+        # D, bs, NB, scale(s), dtypes, sm_cap, workspace, bytes, error_word, stream
+        lib.pda_paged_chunk_attention.argtypes = [P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I,
+                                                  F, I, I, I, P, SZ, P, P]
+        lib.pda_paged_chunk_attention.restype = I
+        lib.pda_paged_chunk_attention_fp8.argtypes = [P, P, P, P, P, I, P, P, I, I, I, I, I, I,
+                                                      I, I, F, F, F, I, I, P, SZ, P, P]
+        lib.pda_paged_chunk_attention_fp8.restype = I
         _lib = lib
         return lib
 
@@ -114,7 +134,9 @@ class PdaDeviceError(RuntimeError):
     NAMES = {PDA_DEVERR_CONTEXT_LEN: "context length out of range",
              PDA_DEVERR_BLOCK_ID: "block id out of range",
              PDA_DEVERR_SLOT: "slot out of range",
-             PDA_DEVERR_TIMEOUT: "pipeline wait timed out"}
+             PDA_DEVERR_TIMEOUT: "pipeline wait timed out",
+             PDA_DEVERR_QUERY: "query lengths out of range",
+             PDA_DEVERR_NO_BLOCKS: "too few free blocks"}
 
     def __init__(self, bits: int):
         self.bits = bits
@@ -436,3 +458,159 @@ def kv_unpack_layers(packed, k_caches, v_caches, block_table_row, context_len: i
                                        int(context_len), H_kv, D, bs, NB, _dtype(k_caches[0]),
                                        _ptr(error_word), _stream(stream)),
            "pda_kv_unpack_layers")
+
+
+# ---------------------------------------------------------------- a step of new tokens
+def _require(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+class _on:
+    """Launches on the tensors' own device: checks that all of them (None skipped) live there,
+    makes it current for the call if it is not, and holds the stream to launch on."""
+
+    def __init__(self, stream, *tensors):
+        dev = tensors[0].device
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise ValueError(f"tensors on {t.device} and {dev}: all must share one device")
+        _require(dev.type == "cuda", "tensor must live on a CUDA device")
+        self.device = dev
+        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
+        self.raw = ctypes.c_void_p(self.stream.cuda_stream)
+        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _int32(shape, **tensors):
+    for name, t in tensors.items():
+        _require(t.dtype == torch.int32 and t.shape == shape,
+                 f"{name} must be int32 of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+
+
+def kv_assign_blocks(block_tables, blocks_held, free_list, free_count, context_lens,
+                     block_size: int, blocks_held_out=None, free_count_out=None,
+                     shared_blocks=None, error_word=None, stream=None):
+    """Grow and shrink the rows of ``block_tables`` to ``context_lens`` tokens, taking blocks
+    off the top of the stack ``free_list[:free_count]`` and giving them back to it, in place
+    (``blocks_held`` and ``free_count`` too, unless other outputs are given for them)."""
+    _require(block_tables.dim() == 2 and free_list.dim() == 1,
+             "block_tables must be [B, max_blocks] and free_list [num_blocks]")
+    B, max_blocks = block_tables.shape
+    held_out = blocks_held if blocks_held_out is None else blocks_held_out
+    count_out = free_count if free_count_out is None else free_count_out
+    _int32((B, max_blocks), block_tables=block_tables)
+    _int32((B,), blocks_held=blocks_held, blocks_held_out=held_out, context_lens=context_lens)
+    if shared_blocks is not None:
+        _int32((B,), shared_blocks=shared_blocks)
+    _int32((1,), free_count=free_count, free_count_out=count_out)
+    _int32(free_list.shape, free_list=free_list)
+    with _on(stream, block_tables, blocks_held, held_out, free_list, free_count, count_out,
+             context_lens, shared_blocks, error_word) as on:
+        _check(load().pda_kv_assign_blocks(
+            _ptr(block_tables), _ptr(blocks_held), _ptr(held_out), _ptr(free_list),
+            _ptr(free_count), _ptr(count_out), _ptr(context_lens), _ptr(shared_blocks), B,
+            max_blocks, int(block_size), free_list.shape[0], _ptr(error_word), on.raw),
+            "pda_kv_assign_blocks")
+    return block_tables
+
+
+def kv_build_slots(slot_mapping, query_start, query_lens, context_lens, block_tables,
+                   block_size: int, num_blocks: int, error_word=None, stream=None):
+    """Fill ``slot_mapping`` ([N] int32, for ``kv_append``) and ``query_start`` ([B + 1], for
+    ``paged_chunk_attention``) from ``query_lens`` new tokens of ``context_lens`` per request;
+    rows of ``slot_mapping`` behind the last token get -1."""
+    _require(block_tables.dim() == 2 and slot_mapping.dim() == 1,
+             "block_tables must be [B, max_blocks] and slot_mapping [N]")
+    B, max_blocks = block_tables.shape
+    _int32((B, max_blocks), block_tables=block_tables)
+    _int32((B,), query_lens=query_lens, context_lens=context_lens)
+    _int32((B + 1,), query_start=query_start)
+    _int32(slot_mapping.shape, slot_mapping=slot_mapping)
+    with _on(stream, query_start, slot_mapping, query_lens, context_lens, block_tables,
+             error_word) as on:
+        _check(load().pda_kv_build_slots(
+            _ptr(slot_mapping), _ptr(query_start), _ptr(query_lens), _ptr(context_lens),
+            _ptr(block_tables), slot_mapping.shape[0], B, max_blocks, int(block_size),
+            int(num_blocks), _ptr(error_word), on.raw), "pda_kv_build_slots")
+    return slot_mapping
+
+
+def chunk_attention_workspace_size(B, T, H, H_kv, D, block_size=16, kv_dtype=torch.bfloat16,
+                                   sm_cap=0) -> int:
+    n = ctypes.c_size_t(0)
+    dt = {torch.bfloat16: PDA_BF16, torch.float32: PDA_F32, torch.float16: PDA_F16,
+          torch.uint8: PDA_FP8_E4M3, torch.float8_e4m3fn: PDA_FP8_E4M3}[kv_dtype]
+    _check(load().pda_chunk_attention_workspace_size(B, T, H, H_kv, D, block_size, dt, sm_cap,
+                                                     ctypes.byref(n)),
+           "pda_chunk_attention_workspace_size")
+    return n.value
+
+
+def alloc_chunk_workspace(B, T, H, H_kv, D, block_size=16, kv_dtype=torch.bfloat16, sm_cap=0,
+                          device=None) -> torch.Tensor:
+    """Workspace for one chunk-attention call (torch.uint8 / float8_e4m3fn: an FP8 cache)."""
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        n = chunk_attention_workspace_size(B, T, H, H_kv, D, block_size, kv_dtype, sm_cap)
+        return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _chunk(fn, what, scales, out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+           max_context_len, sm_cap, workspace, error_word, stream, dtypes):
+    _require(q.dim() == 3 and k_cache.dim() == 4 and block_tables.dim() == 2,
+             "q must be [T, H, D], the caches [NB, bs, H_kv, D], block_tables [B, max_blocks]")
+    T, H, D = q.shape
+    NB, bs, H_kv, D2 = k_cache.shape
+    B, max_blocks = block_tables.shape
+    _require(D == D2 and v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype,
+             "q, k_cache and v_cache must agree in head size, shape and type")
+    _require(out.shape == q.shape and out.dtype == q.dtype, "out must be like q")
+    _int32((B, max_blocks), block_tables=block_tables)
+    _int32((B,), context_lens=context_lens)
+    _int32((B + 1,), query_start=query_start)
+    with _on(stream, q, out, k_cache, v_cache, block_tables, context_lens, query_start,
+             workspace, error_word) as on:
+        if workspace is None:  # from the launching stream's pool: reused there only
+            with torch.cuda.stream(on.stream):
+                workspace = alloc_chunk_workspace(B, T, H, H_kv, D, bs, k_cache.dtype, sm_cap,
+                                                  on.device)
+        _check(fn(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                  max_blocks, _ptr(context_lens), _ptr(query_start), int(max_context_len), B, T,
+                  H, H_kv, D, bs, NB, *scales, *dtypes, int(sm_cap), _ptr(workspace),
+                  workspace.numel() * workspace.element_size(), _ptr(error_word), on.raw), what)
+    return out
+
+
+def paged_chunk_attention(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                          max_context_len: int, scale: float, sm_cap: int = 0, workspace=None,
+                          error_word=None, stream=None):
+    """Attention of each request's new tokens (rows ``query_start[b]:query_start[b + 1]`` of
+    ``q`` [T, H, D], the last of its ``context_lens[b]``) over its paged history up to and
+    including themselves."""
+    return _chunk(load().pda_paged_chunk_attention, "pda_paged_chunk_attention",
+                  (float(scale),), out, q, k_cache, v_cache, block_tables, context_lens,
+                  query_start, max_context_len, sm_cap, workspace, error_word, stream,
+                  (_dtype(q), _dtype(k_cache)))
+
+
+def paged_chunk_attention_fp8(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                              max_context_len: int, scale: float, k_scale: float,
+                              v_scale: float, sm_cap: int = 0, workspace=None, error_word=None,
+                              stream=None):
+    """``paged_chunk_attention`` over an FP8 E4M3 cache: stored code c of K means
+    decode(c) * k_scale."""
+    _require(_dtype(k_cache) == PDA_FP8_E4M3, "the caches must hold FP8 E4M3 codes")
+    return _chunk(load().pda_paged_chunk_attention_fp8, "pda_paged_chunk_attention_fp8",
+                  (float(scale), float(k_scale), float(v_scale)), out, q, k_cache, v_cache,
+                  block_tables, context_lens, query_start, max_context_len, sm_cap, workspace,
+                  error_word, stream, (_dtype(q),))
