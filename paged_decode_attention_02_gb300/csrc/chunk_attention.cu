@@ -7,35 +7,19 @@
 // maximum and sum in fp32.
 #include <math.h>
 
+#include "chunk_internal.h"
 #include "pda_device.cuh"
-#include "pda_internal.h"
 
 namespace pda {
 namespace {
 
 constexpr int kChunkMaxBatch = 8192;
 
-struct ChunkParams {
-  void* out;
-  const void* q;
-  const void* k_cache;
-  const void* v_cache;
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  const int32_t* query_start;
-  int32_t* error_word;
-  float scale_log2;  // softmax scale times log2 e (and the cache's K scale)
-  float v_scale;
-  int B, T, H, H_kv, G, max_blocks, max_context_len, block_size, num_blocks;
-};
-
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(fp8e4m3 x) { return e4m3_to_f32(x.bits); }
 __device__ __forceinline__ void from_f32(float* p, float x) { *p = x; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f32(__half* p, float x) { *p = __float2half_rn(x); }
 
 template <typename KV, typename Q, int D>
 __global__ void __launch_bounds__(256) chunk_rows_kernel(const ChunkParams p) {
@@ -119,6 +103,11 @@ void launch_rows(const ChunkParams& p, int D, cudaStream_t stream) {
     chunk_rows_kernel<KV, Q, 64><<<grid, 256, 0, stream>>>(p);
 }
 
+size_t workspace_for(pda_dtype kv_dtype, int D, int sms) {
+  const size_t n = kv_dtype == PDA_BF16 || kv_dtype == PDA_F16 ? chunk_tc_workspace(sms, D) : 0;
+  return n < 256 ? 256 : n;
+}
+
 // The launch behind both public entry points.
 pda_status launch_chunk(void* out, const void* q, const void* k_cache, const void* v_cache,
                         const int32_t* block_tables, int max_blocks_per_seq,
@@ -143,20 +132,22 @@ pda_status launch_chunk(void* out, const void* q, const void* k_cache, const voi
   if (static_cast<long long>(num_blocks) * block_size >= (1ll << 31) ||
       static_cast<long long>(B) * max_blocks_per_seq >= (1ll << 31))
     return PDA_ERR_UNSUPPORTED;
-  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < 256)
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PDA_ERR_WORKSPACE;
+  int dev, sms;
+  const pda_status dst = current_device_sms(&dev, &sms);
+  if (dst != PDA_OK) return dst;
+  if (sm_cap > 0 && sm_cap < sms) sms = sm_cap;
+  if (workspace_bytes < workspace_for(kv_dtype, D, sms)) return PDA_ERR_WORKSPACE;
   const ChunkParams p{out,     q,      k_cache,   v_cache,
                       block_tables, context_lens, query_start, error_word,
                       scale * k_scale * 1.4426950408889634f,
                       v_scale, B,      T,         H,
                       H_kv,    H / H_kv, max_blocks_per_seq, max_context_len,
                       block_size, num_blocks};
-  if (kv_dtype == PDA_BF16)
-    launch_rows<__nv_bfloat16, __nv_bfloat16>(p, D, stream);
-  else if (kv_dtype == PDA_F16)
-    launch_rows<__half, __half>(p, D, stream);
-  else if (kv_dtype == PDA_F32)
+  if (kv_dtype == PDA_BF16 || kv_dtype == PDA_F16)
+    return launch_chunk_tc(p, D, kv_dtype, dev, sms, workspace, stream);
+  if (kv_dtype == PDA_F32)
     launch_rows<float, float>(p, D, stream);
   else
     launch_rows<fp8e4m3, __nv_bfloat16>(p, D, stream);
@@ -174,7 +165,10 @@ extern "C" pda_status pda_chunk_attention_workspace_size(int B, int T, int H, in
   if (bytes == nullptr) return PDA_ERR_INVALID_ARG;
   const pda_status st = check_shape(B, T, H, H_kv, D, block_size, kv_dtype, sm_cap);
   if (st != PDA_OK) return st;
-  *bytes = 256;
+  int dev, sms;
+  const pda_status dst = current_device_sms(&dev, &sms);
+  if (dst != PDA_OK) return dst;
+  *bytes = workspace_for(kv_dtype, D, sm_cap > 0 && sm_cap < sms ? sm_cap : sms);
   return PDA_OK;
 }
 

@@ -1,0 +1,961 @@
+// chunk_attention_tc.cu -- chunk attention over 16-bit caches on the tcgen05 tensor cores.
+//
+// Mathematics. With packed rows R = token * G + head (the G query heads of a kv-head share its
+// keys), S = Q K^T per 128 rows x 128 keys, softmax with a running maximum m and sum l,
+// O += P V. m is a reference, not the exact maximum: it only moves when a row's scores pass
+// it by 2^8, and then O and l are rescaled; the result O / l does not depend on it. Scores,
+// m, l and O stay in fp32; the probabilities are rounded to the operands' 16-bit type for the
+// P V product (the matrix instruction takes no wider operand with 16-bit V).
+//
+// One block per SM walks a contiguous range of the launch's units (chunk_plan.h). Warps:
+//   0-3, 4-7  softmax of row group 0 and 1 (a thread per row: TMEM lane = row)
+//   8         plans the block's pieces, publishes them, and loads Q, K and V with TMA
+//   9         issues the matrix instructions
+//   10, 11    clean the V tiles at the diagonal and the end (see below)
+// An item of more than 128 rows gives each group 128 rows; both read every K and V tile. An
+// item of fewer gives both groups the same rows and alternate tiles, merged at the end, so
+// that one group's softmax still runs under the other's products.
+// TMEM: S0 | S1 | O0 | O1, 128 columns each; P overwrites the first 64 columns of its S.
+//
+// V tiles that reach past what some row may see (the diagonal ones) multiply zero
+// probabilities with later tokens' V, or with whatever lies behind the last token; 0 * NaN
+// would reach the output. Warps 10 and 11 zero the rows behind the end, replace non-finite
+// values by zeros and note their rows, and the epilogue adds those values back to the rows
+// that do see them.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "chunk_internal.h"
+#include "chunk_plan.h"
+#include "tcgen05.cuh"
+
+namespace pda {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kDescs = 4;
+constexpr int kMinPieceTiles = 6;   // a cut item's pieces are at least this long
+constexpr int kMinWorkerUnits = 4;  // a worker's range is at least this long
+constexpr float kRaise = 8.f;       // the reference maximum moves by at least 2^8
+
+// One piece of work: key tiles [ja, jb) of an item.
+struct Desc {
+  int valid;
+  int row0;     // the item's first token: row of q and out
+  int tokens;   // tokens of the item
+  int pos0;     // position of the first
+  int kh;
+  int ja, jb;
+  int tiles0, tiles1;  // key tiles of row groups 0 and 1
+  int single;   // both groups hold the same 128 rows
+  int jc;       // first tile that some row does not see whole
+  int end;      // keys any row sees
+  int slot;     // partial-result slot, -1: the whole item
+  int bad_from; // position of the first block with an id out of range
+  long long table;  // the request's row in block_tables
+  unsigned nonfinite[3][4];  // V rows of tiles jc .. jc + 2 that hold a NaN or infinity
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kChunkKeys * D * 2;  // bytes of a K, V or Q tile
+  static constexpr int kHalf = kChunkKeys * 128;    // of its 64-element half
+  // K and V ring apart: every V tile passes through the cleaning warps, K tiles do not
+  static constexpr int kK = D == 128 ? 3 : 5;
+  static constexpr int kV = D == 128 ? 2 : 5;
+};
+
+// One box of a 3-D tensor map into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* tm, int c0, int c1, int c2,
+                                        uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+      : "memory");
+}
+
+struct Misc {
+  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5], clean[5];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], merge_ready, merge_done, done;
+  uint64_t desc_full[kDescs], desc_empty[kDescs];
+  Desc desc[kDescs];
+  float2 ml[128];
+  uint32_t tmem;
+};
+
+template <int D>
+constexpr size_t smem_bytes() {
+  return 1024 + static_cast<size_t>(Cfg<D>::kK + Cfg<D>::kV + 2) * Cfg<D>::kTile + sizeof(Misc);
+}
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "227 KB a block");
+
+// ---------------------------------------------------------------- plan
+// Units of the requests [0, c * per) for every c, built by all threads of the block.
+struct Plan {
+  long long* prefix;  // kPlanChunks + 1 entries in shared memory
+  int per, workers;
+  long long units;
+};
+constexpr int kPlanChunks = 256;
+
+struct Where {
+  int b, kh, i;
+  long long start;  // unit
+  ChunkReq r;
+};
+
+// A request with work to do; n = 0 for one without (empty, padded or in error).
+__device__ __forceinline__ ChunkReq chunk_req(const ChunkParams& p, int b, int lt) {
+  const int q0 = p.query_start[b], q1 = p.query_start[b + 1], L = p.context_lens[b];
+  const bool ok = q0 >= 0 && q1 <= p.T && q0 < q1 && L >= q1 - q0 && L <= p.max_context_len &&
+                  L <= static_cast<long long>(p.max_blocks) * p.block_size;
+  return ChunkReq{ok ? q1 - q0 : 0, ok ? L : 0, lt};
+}
+
+__device__ __forceinline__ Plan make_plan(const ChunkParams& p, int lt, int workers,
+                                          long long* prefix) {
+  Plan pl;
+  pl.prefix = prefix;
+  pl.per = (p.B + kPlanChunks - 1) / kPlanChunks;
+  const int c = threadIdx.x, lane = c & 31;
+  long long x = 0;
+  if (c < kPlanChunks)
+    for (int b = c * pl.per; b < min(p.B, (c + 1) * pl.per); ++b)
+      x += chunk_req(p, b, lt).units();
+  x *= p.H_kv;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(kFullMask, x, o);
+    if (lane >= o) x += y;
+  }
+  if (c < kPlanChunks) prefix[c + 1] = x;
+  __syncthreads();
+  long long before = 0;
+  if (c < kPlanChunks)
+    for (int w = 0; w < (c >> 5); ++w) before += prefix[32 * w + 32];
+  __syncthreads();
+  if (c < kPlanChunks) prefix[c + 1] = x + before;
+  if (c == 0) prefix[0] = 0;
+  __syncthreads();
+  pl.units = prefix[kPlanChunks];
+  pl.workers = chunk_workers(pl.units, workers, kMinWorkerUnits);
+  return pl;
+}
+
+// The item that holds unit u < units.
+__device__ __forceinline__ Where locate(const ChunkParams& p, const Plan& pl, int lt,
+                                        long long u) {
+  int lo = 0, hi = kPlanChunks - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (pl.prefix[mid + 1] > u)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  long long at = pl.prefix[lo];
+  int b = lo * pl.per;
+  ChunkReq r = chunk_req(p, b, lt);
+  long long one = r.units();
+  while (at + one * p.H_kv <= u) {
+    at += one * p.H_kv;
+    r = chunk_req(p, ++b, lt);
+    one = r.units();
+  }
+  const int kh = static_cast<int>((u - at) / one);
+  at += kh * one;
+  const int i = r.item_of(u - at);
+  return Where{b, kh, i, at + r.units_before(i), r};
+}
+
+// The cut before worker c, snapped; *w: the item it falls into (for a cut below `units`).
+__device__ __forceinline__ long long cut_of(const ChunkParams& p, const Plan& pl, int lt, int c,
+                                            Where* w) {
+  const long long u = chunk_cut(pl.units, pl.workers, c);
+  if (u >= pl.units) return pl.units;
+  *w = locate(p, pl, lt, u);
+  return chunk_snap(u, w->start, w->r.tiles(w->i), kMinPieceTiles);
+}
+
+// ---------------------------------------------------------------- the block's pipeline
+// A wait of a whole warp: false for all lanes if it ran out for any.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(kFullMask, mbar_wait_bounded(bar, parity));
+}
+
+struct Groups {
+  int n0, n1;  // steps of each group
+};
+__device__ __forceinline__ Groups groups_of(const Desc& d) {
+  const int nt = d.jb - d.ja;
+  if (d.single) return Groups{(nt + 1) >> 1, nt >> 1};
+  return Groups{max(0, min(d.jb, d.tiles0) - d.ja), max(0, min(d.jb, d.tiles1) - d.ja)};
+}
+
+__device__ __forceinline__ bool nonfinite16(uint32_t w, uint32_t exp_mask, uint32_t exp_one) {
+  // per half: (exponent bits) + 1 carries into the sign place when they are all ones
+  return (((w & exp_mask) + exp_one) & 0x80008000u) != 0;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const ChunkParams p, int g_shift,
+                    float* partial) {
+  using C = Cfg<D>;
+  constexpr int NK = C::kK, NV = C::kV;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char* ks = smem;
+  unsigned char* vs = ks + NK * C::kTile;
+  unsigned char* qs = vs + NV * C::kTile;
+  Misc& ms = *reinterpret_cast<Misc*>(qs + 2 * C::kTile);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int lt = kItemRowsLog2 - g_shift;
+
+  // the merge kernel may start its own prologue as soon as blocks leave
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    for (int i = 0; i < 5; ++i) {
+      mbar_init(&ms.k_full[i], 1);
+      mbar_init(&ms.k_empty[i], 1);
+      mbar_init(&ms.v_full[i], 1);
+      mbar_init(&ms.v_empty[i], 1);
+      mbar_init(&ms.clean[i], 2);
+    }
+    mbar_init(&ms.q_full, 1);
+    mbar_init(&ms.q_empty, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&ms.s_full[g], 1);
+      mbar_init(&ms.p_full[g], 128);
+      mbar_init(&ms.o_full[g], 1);
+    }
+    mbar_init(&ms.merge_ready, 128);
+    mbar_init(&ms.merge_done, 128);
+    mbar_init(&ms.done, 1);
+    for (int i = 0; i < kDescs; ++i) {
+      mbar_init(&ms.desc_full[i], 1);
+      mbar_init(&ms.desc_empty[i], 1 + 2 + 8);  // matrix warp, cleaners, softmax warps
+    }
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&ms.tmem, 512);
+    tmem_relinquish();
+  }
+  const Plan pl = make_plan(p, lt, gridDim.x, reinterpret_cast<long long*>(ks));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem;
+
+  // requests without work whose rows are written all the same: padded (zeros) or in error (NaN)
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int q0 = p.query_start[b], q1 = p.query_start[b + 1], L = p.context_lens[b];
+    if (q0 == q1 && q0 >= 0 && q1 <= p.T) continue;
+    if (q0 < 0 || q1 > p.T || q0 > q1) {
+      if (tid == 0) atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
+      continue;
+    }
+    if (chunk_req(p, b, lt).n > 0) continue;
+    if (L != 0 && tid == 0) atomic_or_error(p.error_word, PDA_DEVERR_CONTEXT_LEN);
+    const uint32_t w = L == 0 ? 0u : 0x7fff7fffu;  // a NaN in either type
+    uint4* rows = reinterpret_cast<uint4*>(p.out) + static_cast<size_t>(q0) * p.H * (D / 8);
+    const long long vecs = static_cast<long long>(q1 - q0) * p.H * (D / 8);
+    for (long long i = tid; i < vecs; i += kThreads) rows[i] = make_uint4(w, w, w, w);
+  }
+
+  bool timed_out = false;
+  if (warp == 8) {
+    // ================================================================ plan and load
+    Where w{};
+    Where w_end{};
+    const bool mine = static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0;
+    long long u = 0, u_end = 0;
+    if (mine) {
+      u_end = cut_of(p, pl, lt, blockIdx.x + 1, &w_end);
+      u = cut_of(p, pl, lt, blockIdx.x, &w);
+      if (u < u_end && u >= w.start + w.r.tiles(w.i) + 1) w = locate(p, pl, lt, u);
+    }
+    __syncwarp();
+    fence_proxy_async_smem();  // the plan's shared memory becomes load stages
+    int item = 0;
+    unsigned loads = 0;  // tiles loaded so far, of K and of V
+    const int bs = p.block_size;
+    const int nbt = bs >= kChunkKeys ? 1 : kChunkKeys / bs;  // blocks of a tile
+    const int box_rows = bs >= kChunkKeys ? kChunkKeys : bs;
+    const int tiles_per_group = 32 / nbt;
+    while (u < u_end && !timed_out) {
+      const ChunkReq r = w.r;
+      const int tiles = r.tiles(w.i);
+      const long long end = w.start + tiles + 1;
+      const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
+      const int ja = u == w.start ? 0 : static_cast<int>(u - w.start - 1);
+      const int jb = u_end >= end ? tiles : static_cast<int>(u_end - w.start - 1);
+      const int slot = item % kDescs;
+      Desc& d = ms.desc[slot];
+      if (!warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
+        timed_out = true;
+        break;
+      }
+      const int pos0 = r.L - r.n + tok0;
+      const int half = 128 >> g_shift;  // tokens of a row group
+      const bool single = tokens <= half;
+      const int kv_end = pos0 + tokens;
+      const long long table = static_cast<long long>(w.b) * p.max_blocks;
+      const int row0 = p.query_start[w.b] + tok0;
+      if (lane == 0) {
+        d.valid = 1;
+        d.row0 = row0;
+        d.tokens = tokens;
+        d.pos0 = pos0;
+        d.kh = w.kh;
+        d.ja = ja;
+        d.jb = jb;
+        d.tiles0 = single ? tiles : ((pos0 + half - 1) >> 7) + 1;
+        d.tiles1 = tiles;
+        d.single = single;
+        d.jc = (pos0 + 1) >> 7;
+        d.end = kv_end;
+        d.slot = ja == 0 && jb == tiles ? -1 : static_cast<int>(blockIdx.x) * 2 + (ja == 0 ? 1 : 0);
+        d.bad_from = 0x7fffffff;
+        d.table = table;
+        for (int k = 0; k < 12; ++k) d.nonfinite[k >> 2][k & 3] = 0;
+        mbar_arrive(&ms.desc_full[slot]);
+      }
+      __syncwarp();
+      // Q
+      if (!warp_wait(&ms.q_empty, (item & 1) ^ 1)) {
+        timed_out = true;
+        break;
+      }
+      const int q_tiles = single ? 1 : 2;
+      if (lane == 0) mbar_arrive_expect_tx(&ms.q_full, q_tiles * C::kTile);
+      __syncwarp();
+      if (lane < q_tiles * C::kHalves) {
+        const int g = lane / C::kHalves, h = lane % C::kHalves;
+        tma_box(qs + g * C::kTile + h * C::kHalf, &tm_q, 64 * h, w.kh << g_shift,
+                   row0 + g * half, &ms.q_full);
+      }
+      // K and V
+      const int nt = jb - ja;
+      const int pairs = single ? (nt + 1) >> 1 : nt;
+      int group = -1, ids = 0, next_ids = 0;
+      auto fetch = [&](int gr) {  // the ids of tiles ja + gr * tiles_per_group + ..
+        const int t = gr * tiles_per_group + lane / nbt;
+        const int blk = bs >= kChunkKeys ? static_cast<int>((static_cast<long long>(ja + t) * kChunkKeys) / bs)
+                                         : (ja + t) * nbt + lane % nbt;
+        const bool used = t < nt && static_cast<long long>(blk) * bs < kv_end;
+        return used ? p.block_tables[table + blk] : 0;
+      };
+      next_ids = fetch(0);
+      for (int s = 0; s < pairs && !timed_out; ++s) {
+        const int first = single ? 2 * s : s, count = single ? min(2, nt - first) : 1;
+        if (first / tiles_per_group != group) {
+          group = first / tiles_per_group;
+          ids = next_ids;
+          const int t = group * tiles_per_group + lane / nbt;
+          const int blk = bs >= kChunkKeys ? static_cast<int>((static_cast<long long>(ja + t) * kChunkKeys) / bs)
+                                           : (ja + t) * nbt + lane % nbt;
+          const bool used = t < nt && static_cast<long long>(blk) * bs < kv_end;
+          if (used && (ids < 0 || ids >= p.num_blocks)) {
+            // the rows that see the block become NaN in the epilogue; any block stands in
+            atomicMin(&d.bad_from, max(blk * bs, (ja + t) * kChunkKeys));
+            atomic_or_error(p.error_word, PDA_DEVERR_BLOCK_ID);
+            ids = 0;
+          }
+          __threadfence_block();
+          __syncwarp();
+          next_ids = fetch(group + 1);
+        }
+        for (int x = 0; x < 2 * count; ++x) {
+          const bool is_v = x >= count;
+          const int t = first + (is_v ? x - count : x);
+          const unsigned at = loads + t;
+          const int st = is_v ? at % NV : at % NK;
+          const unsigned turn = is_v ? at / NV : at / NK;
+          uint64_t* full = is_v ? &ms.v_full[st] : &ms.k_full[st];
+          if (!warp_wait(is_v ? &ms.v_empty[st] : &ms.k_empty[st], (turn & 1) ^ 1)) {
+            timed_out = true;
+            break;
+          }
+          const int key0 = (ja + t) * kChunkKeys;
+          const int boxes = min(nbt, (kv_end - key0 + box_rows - 1) / box_rows);
+          if (lane == 0)
+            mbar_arrive_expect_tx(full, boxes * C::kHalves * box_rows * 128);
+          __syncwarp();
+          const int blk = lane / C::kHalves, h = lane % C::kHalves;
+          const int id = __shfl_sync(kFullMask, ids, ((t - group * tiles_per_group) * nbt + blk) & 31);
+          if (blk < boxes) {
+            const int row = id * bs + (bs > kChunkKeys ? key0 % bs : 0);
+            tma_box((is_v ? vs : ks) + st * C::kTile + h * C::kHalf + blk * box_rows * 128,
+                        is_v ? &tm_v : &tm_k, 64 * h, w.kh, row, full);
+          }
+        }
+      }
+      loads += nt;
+      ++item;
+      // the next item
+      u = end;
+      if (u < u_end) {
+        w.start = end;
+        if (w.i + 1 < r.items()) {
+          ++w.i;
+        } else {
+          w.i = 0;
+          if (++w.kh == p.H_kv) {
+            w.kh = 0;
+            do {
+              w.r = chunk_req(p, ++w.b, lt);
+            } while (w.r.n == 0);
+          }
+        }
+      }
+    }
+    if (!timed_out) {
+      const int slot = item % kDescs;
+      if (warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
+        if (lane == 0) {
+          ms.desc[slot].valid = 0;
+          mbar_arrive(&ms.desc_full[slot]);
+        }
+      } else {
+        timed_out = true;
+      }
+    }
+    if (timed_out) {
+      // copies in flight land before the block may leave: wait for the last one of each stage
+      for (int st = 0; st < 2 * 5; ++st) {
+        uint64_t* full = st < 5 ? &ms.k_full[st] : &ms.v_full[st - 5];
+        warp_wait(full, 0);
+        warp_wait(full, 1);
+      }
+      warp_wait(&ms.q_full, 0);
+      warp_wait(&ms.q_full, 1);
+    }
+  } else if (warp == 9) {
+    // ================================================================ matrix instructions
+    if (lane == 0) {
+      const bool negate = p.scale_log2 < 0.f;  // S is compared and scaled by |scale|
+      const uint32_t id_qk = mma_idesc(kBf16, kChunkKeys, negate, false);
+      const uint32_t id_pv = mma_idesc(kBf16, D, false, true);
+      const uint32_t k0 = smem_addr(ks), v0 = smem_addr(vs), q0 = smem_addr(qs);
+      unsigned loads = 0, p_phase = 0;
+      for (int item = 0; !timed_out; ++item) {
+        const int slot = item % kDescs;
+        if (!mbar_wait_bounded(&ms.desc_full[slot], (item / kDescs) & 1)) {
+          timed_out = true;
+          break;
+        }
+        const Desc& d = ms.desc[slot];
+        if (!d.valid) break;
+        const Groups gr = groups_of(d);
+        const int nt = d.jb - d.ja, ja = d.ja, kv_end = d.end;
+        const bool single = d.single != 0;
+        const int last_g = gr.n1 >= gr.n0 ? 1 : 0, steps = max(gr.n0, gr.n1);
+        if (!mbar_wait_bounded(&ms.q_full, item & 1)) {
+          timed_out = true;
+          break;
+        }
+        tc_fence_after();
+        auto qk = [&](int g, int s) {
+          const int t = single ? 2 * s + g : s;
+          const unsigned at = loads + t;
+          const int st = at % NK;
+          if (!mbar_wait_bounded(&ms.k_full[st], (at / NK) & 1)) return false;
+          tc_fence_after();
+          const uint32_t a = q0 + (single ? 0 : g * C::kTile), b = k0 + st * C::kTile;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * C::kHalf + (k & 3) * 32;
+            mma_f16_ss(tmem + g * 128, smem_desc_sw128(a + off, 16, 1024),
+                       smem_desc_sw128(b + off, 16, 1024), id_qk, k > 0);
+          }
+          mma_commit(&ms.s_full[g]);
+          if (single || g == 1) mma_commit(&ms.k_empty[st]);
+          if (g == last_g && s == steps - 1) mma_commit(&ms.q_empty);
+          return true;
+        };
+        auto pv = [&](int g, int s, bool last) {
+          const int t = single ? 2 * s + g : s;
+          const unsigned at = loads + t;
+          const int st = at % NV;
+          if (!mbar_wait_bounded(&ms.v_full[st], (at / NV) & 1)) return false;
+          if (!mbar_wait_bounded(&ms.clean[st], (at / NV) & 1)) return false;
+          if (!mbar_wait_bounded(&ms.p_full[g], (p_phase >> g) & 1)) return false;
+          p_phase ^= 1u << g;
+          tc_fence_after();
+          const uint32_t b = v0 + st * C::kTile;
+          const int ksteps = (min(kChunkKeys, kv_end - (ja + t) * kChunkKeys) + 15) >> 4;
+          for (int k = 0; k < ksteps; ++k)
+            mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * k,
+                       smem_desc_sw128(b + k * 2048, C::kHalf, 1024), id_pv, s > 0 || k > 0);
+          if (single || g == 1) mma_commit(&ms.v_empty[st]);
+          if (last) mma_commit(&ms.o_full[g]);
+          return true;
+        };
+        bool ok = true;
+        if (gr.n0 > 0) ok = qk(0, 0);
+        if (ok && gr.n1 > 0) ok = qk(1, 0);
+        for (int s = 0; ok && s < steps; ++s) {
+          if (s < gr.n0) {
+            ok = pv(0, s, s + 1 == gr.n0);
+            if (ok && s + 1 < gr.n0) ok = qk(0, s + 1);
+          }
+          if (ok && s < gr.n1) {
+            ok = pv(1, s, s + 1 == gr.n1);
+            if (ok && s + 1 < gr.n1) ok = qk(1, s + 1);
+          }
+        }
+        if (!ok) {
+          timed_out = true;
+          break;
+        }
+        loads += nt;
+        mbar_arrive(&ms.desc_empty[slot]);
+      }
+      // nothing of this thread's is in flight when the block gives its TMEM back
+      mma_commit(&ms.done);
+      if (!mbar_wait_bounded(&ms.done, 0)) timed_out = true;
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ================================================================ clean V tiles
+    const int half = warp - 10;
+    unsigned loads = 0;
+    for (int item = 0; !timed_out; ++item) {
+      const int slot = item % kDescs;
+      if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
+        timed_out = true;
+        break;
+      }
+      Desc& d = ms.desc[slot];
+      if (!d.valid) break;
+      const int ja = d.ja, nt = d.jb - ja, jc = d.jc, kv_end = d.end;
+      for (int t = 0; t < nt; ++t) {
+        const unsigned at = loads + t;
+        const int st = at % NV;
+        if (!warp_wait(&ms.v_full[st], (at / NV) & 1)) {
+          timed_out = true;
+          break;
+        }
+        if (ja + t < jc) {  // every row sees every key
+          if (lane == 0) mbar_arrive(&ms.clean[st]);
+          continue;
+        }
+        const int keys = min(kChunkKeys, kv_end - (ja + t) * kChunkKeys);
+        const int rows = (keys + 15) & ~15;  // what the products read
+        constexpr uint32_t kMask = kBf16 ? 0x7f807f80u : 0x7c007c00u;
+        constexpr uint32_t kOne = kBf16 ? 0x00800080u : 0x04000400u;
+        // a lane takes one 16-byte chunk of every fourth row
+        for (int r = half * 4 + (lane >> 3); r < rows; r += 8) {
+          for (int h = 0; h < C::kHalves; ++h) {
+            uint4* at16 = reinterpret_cast<uint4*>(vs + st * C::kTile + h * C::kHalf + r * 128) +
+                          ((lane & 7) ^ (r & 7));
+            if (r >= keys) {
+              *at16 = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 v = *at16;
+            if (nonfinite16(v.x, kMask, kOne) || nonfinite16(v.y, kMask, kOne) ||
+                nonfinite16(v.z, kMask, kOne) || nonfinite16(v.w, kMask, kOne)) {
+              uint32_t* e = &v.x;
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t hit = ((e[k] & kMask) + kOne) & 0x80008000u;
+                e[k] &= ~((hit >> 15) * 0xffffu);
+              }
+              *at16 = v;
+              atomicOr(&d.nonfinite[ja + t - jc][r >> 5], 1u << (r & 31));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.clean[st]);
+      }
+      loads += nt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
+    }
+  } else {
+    // ================================================================ softmax and output
+    const int g = warp >> 2;
+    const int row = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4) << 16
+    const uint32_t tS = tmem + lanes + g * 128, tO = tmem + lanes + 256 + g * 128;
+    const float sl = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    // fp16 probabilities are kept 2^4 higher (the factor cancels in O / l): with the
+    // reference up to 2^8 below the maximum they stay below 2^13, and fewer are subnormal
+    const float lift = kBf16 ? 0.f : 4.f;
+    unsigned s_phase = 0, o_phase = 0, m_phase = 0;
+    for (int item = 0; !timed_out; ++item) {
+      const int slot = item % kDescs;
+      if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
+        timed_out = true;
+        break;
+      }
+      const Desc& d = ms.desc[slot];
+      if (!d.valid) break;
+      const Groups gr = groups_of(d);
+      const int steps = g == 0 ? gr.n0 : gr.n1;
+      const bool single = d.single != 0;
+      const int ja = d.ja;
+      const int packed = single ? row : g * 128 + row;
+      const int tok = packed >> g_shift;
+      const int pos = d.pos0 + min(tok, d.tokens - 1);  // this row's position
+      const int first_pos = d.pos0 + ((single ? 0 : g * 128) >> g_shift);
+      float m = -INFINITY, l = 0.f;
+      for (int s = 0; s < steps; ++s) {
+        if (!warp_wait(&ms.s_full[g], s_phase)) {
+          timed_out = true;
+          break;
+        }
+        s_phase ^= 1;
+        tc_fence_after();
+        const int key0 = (ja + (single ? 2 * s + g : s)) * kChunkKeys;
+        float x[kChunkKeys];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld32(x + 32 * k, tS + 32 * k);
+        tmem_wait_ld();
+        if (key0 + kChunkKeys - 1 > first_pos) {
+          const int seen = pos - key0;
+#pragma unroll
+          for (int k = 0; k < kChunkKeys; ++k)
+            if (k > seen) x[k] = -INFINITY;
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int k = 4; k < kChunkKeys; k += 4) {
+          mx[0] = fmaxf(mx[0], x[k]);
+          mx[1] = fmaxf(mx[1], x[k + 1]);
+          mx[2] = fmaxf(mx[2], x[k + 2]);
+          mx[3] = fmaxf(mx[3], x[k + 3]);
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (s == 0) {
+          m = top;
+        } else {
+          const bool raise = top > m && (top - m) * sl > kRaise;
+          if (__any_sync(kFullMask, raise)) {
+            const float c = raise ? ex2((m - top) * sl) : 1.f;
+            if (raise) m = top;
+            l *= c;
+            // the product of the step before is complete: its successor's scores are
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+              float o[32];
+              tmem_ld32(o, tO + k);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= c;
+              tmem_st32(tO + k, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : lift - m * sl;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kChunkKeys; k += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float a = ex2(fmaf(x[k + e], sl, ref)), b = ex2(fmaf(x[k + e + 1], sl, ref));
+            sum[e & 2] += a;
+            sum[(e & 2) + 1] += b;
+            pk[e / 2] = pack2<kBf16>(a, b);
+          }
+          tmem_st16(tS + k / 2, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&ms.p_full[g]);
+      }
+      if (timed_out) break;
+      // ---- the piece's rows
+      if (steps > 0) {
+        if (!warp_wait(&ms.o_full[g], o_phase)) {
+          timed_out = true;
+          break;
+        }
+        o_phase ^= 1;
+        tc_fence_after();
+      }
+      float m1 = -INFINITY, l1 = 0.f;  // group 1's, where the groups share their rows
+      const bool other = single && gr.n1 > 0;
+      if (other) {
+        if (g == 1) {
+          ms.ml[row] = make_float2(m, l);
+          tc_fence_before();
+          mbar_arrive(&ms.merge_ready);
+          if (!warp_wait(&ms.merge_done, m_phase)) {
+            timed_out = true;
+            break;
+          }
+        } else {
+          if (!warp_wait(&ms.merge_ready, m_phase)) {
+            timed_out = true;
+            break;
+          }
+          tc_fence_after();
+          const float2 v = ms.ml[row];
+          m1 = v.x;
+          l1 = v.y;
+        }
+        m_phase ^= 1;
+      }
+      if (g == 0 || !single) {
+        const float top = fmaxf(m, m1);
+        const float c0 = m == -INFINITY ? 0.f : ex2((m - top) * sl);
+        const float c1 = m1 == -INFINITY ? 0.f : ex2((m1 - top) * sl);
+        l = l * c0 + (other ? l1 * c1 : 0.f);
+        const bool dead = pos >= d.bad_from;
+        const bool write = tok < d.tokens;
+        const int part = d.slot;
+        bool odd = false;
+        if (d.jb > d.jc)
+          for (int k = 0; k < 12; ++k) odd |= d.nonfinite[k >> 2][k & 3] != 0;
+        const float inv = dead ? NAN : part >= 0 ? 1.f : p.v_scale / l;
+        const size_t at =
+            (static_cast<size_t>(d.row0 + tok) * p.H + (d.kh << g_shift) + (packed & ((1 << g_shift) - 1))) * D;
+        float* po = partial + (static_cast<size_t>(max(part, 0)) * 256 + packed) * (D + 4);
+        if (write && part >= 0) {
+          po[D] = steps > 0 && top != -INFINITY ? top * sl : -INFINITY;
+          po[D + 1] = dead ? NAN : l;
+        }
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+          float o[32];
+          if (steps > 0) {
+            tmem_ld32(o, tO + k);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= c0;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (other) {
+            float o1[32];
+            tmem_ld32(o1, tO + 128 + k);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], c1, o[e]);
+          }
+          if (odd) {  // non-finite V values, for the rows that see them
+            for (int y = 0; y < 128 * 3; ++y) {
+              if (!((d.nonfinite[y >> 7][(y >> 5) & 3] >> (y & 31)) & 1)) continue;
+              const int key = d.jc * kChunkKeys + y;
+              const int id = p.block_tables[d.table + key / p.block_size];
+              if (id < 0 || id >= p.num_blocks) continue;
+              const uint16_t* v =
+                  static_cast<const uint16_t*>(p.v_cache) +
+                  ((static_cast<size_t>(id) * p.block_size + key % p.block_size) * p.H_kv + d.kh) * D + k;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float f = kBf16 ? __uint_as_float(static_cast<uint32_t>(v[e]) << 16)
+                                      : __half2float(__ushort_as_half(v[e]));
+                if (!isfinite(f) && key <= pos) o[e] += f;
+              }
+            }
+          }
+          if (write && part >= 0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(po + k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else if (write) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + k);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              dst[e / 8] = make_uint4(pack2<kBf16>(o[e] * inv, o[e + 1] * inv),
+                                      pack2<kBf16>(o[e + 2] * inv, o[e + 3] * inv),
+                                      pack2<kBf16>(o[e + 4] * inv, o[e + 5] * inv),
+                                      pack2<kBf16>(o[e + 6] * inv, o[e + 7] * inv));
+          }
+          __syncwarp();
+        }
+        if (other) {
+          tc_fence_before();
+          mbar_arrive(&ms.merge_done);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
+    }
+  }
+  if (timed_out) atomic_or_error(p.error_word, PDA_DEVERR_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- merge of cut items
+// Block x handles the item that cut x + 1 falls into, if that is the first cut inside it:
+// piece i of a row holds (m_i, l_i, O_i); with M = max m_i the row is
+// sum O_i 2^(m_i - M) / sum l_i 2^(m_i - M). A warp takes a row at a time.
+constexpr int kMergeRows = 32;  // rows of a block
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(256)
+    chunk_merge_kernel(const ChunkParams p, int g_shift, const float* partial, int grid) {
+  __shared__ long long prefix[kPlanChunks + 1];
+  const int lt = kItemRowsLog2 - g_shift;
+  const Plan pl = make_plan(p, lt, grid, prefix);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
+  const int c = blockIdx.x + 1;
+  if (c >= pl.workers) return;
+  Where w, before;
+  const long long s = cut_of(p, pl, lt, c, &w);
+  const int tiles = w.r.tiles(w.i);
+  const long long end = w.start + tiles + 1;
+  if (s <= w.start || s >= end || cut_of(p, pl, lt, c - 1, &before) > w.start) return;
+  int pieces = 2;  // worker c - 1's, and one for each cut inside the item
+  for (; c + pieces - 1 < pl.workers; ++pieces) {
+    const long long u = chunk_cut(pl.units, pl.workers, c + pieces - 1);
+    if (u >= end || chunk_snap(u, w.start, tiles, kMinPieceTiles) >= end) break;
+  }
+  const int tok0 = w.i << lt, tokens = min(1 << lt, w.r.n - tok0);
+  const int rows = tokens << g_shift;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int V = D / 32;
+  const size_t row0 = static_cast<size_t>(p.query_start[w.b]) + tok0;
+  for (int r = blockIdx.y * kMergeRows + warp; r < min(rows, (static_cast<int>(blockIdx.y) + 1) * kMergeRows); r += 8) {
+    auto piece = [&](int i) {
+      const int slot = i == 0 ? 2 * (c - 1) + 1 : 2 * (c + i - 1);
+      return partial + (static_cast<size_t>(slot) * 256 + r) * (D + 4);
+    };
+    float M = -INFINITY;
+    for (int i = lane; i < pieces; i += 32) M = fmaxf(M, piece(i)[D]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+    float l = 0.f, acc[V] = {};
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+      const float* at = piece(i);
+      const float mi = at[D];
+      const float wgt = mi == -INFINITY ? 0.f : ex2(mi - M);
+      l = fmaf(wgt, at[D + 1], l);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(wgt, at[lane * V + e], acc[e]);
+    }
+    const float inv = p.v_scale / l;
+    const size_t at = ((row0 + (r >> g_shift)) * p.H + (w.kh << g_shift) + (r & ((1 << g_shift) - 1))) * D + lane * V;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+    for (int e = 0; e < V; e += 2) out[e / 2] = pack2<kBf16>(acc[e] * inv, acc[e + 1] * inv);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+// A map over 16-bit rows [rows, heads, D] whose boxes are 64 elements of `box_heads` heads of
+// `box_rows` rows, written with the 128-byte swizzle.
+pda_status encode_heads(CUtensorMap* tm, const void* base, long long rows, int heads, int D,
+                        bool bf16, int box_heads, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
+                                 static_cast<cuuint64_t>(heads) * D * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads),
+                             static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t one[3] = {1u, 1u, 1u};
+  const CUresult r = g_encode(
+      tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+      const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B,
+      D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PDA_OK : PDA_ERR_INVALID_ARG;
+}
+
+template <int D, bool kBf16>
+pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaStream_t stream) {
+  static std::atomic<bool> raised[64];
+  if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(chunk_tc_kernel<D, kBf16>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem_bytes<D>())) != cudaSuccess)
+      return PDA_ERR_CUDA;
+    if (dev < 64) raised[dev].store(true, std::memory_order_release);
+  }
+  int g_shift = 0;
+  while ((1 << g_shift) < p.G) ++g_shift;
+  CUtensorMap tq, tk, tv;
+  const long long rows = static_cast<long long>(p.num_blocks) * p.block_size;
+  const int box = p.block_size < kChunkKeys ? p.block_size : kChunkKeys;
+  pda_status st = encode_heads(&tq, p.q, p.T, p.H, D, kBf16, p.G, 128 >> g_shift);
+  if (st == PDA_OK) st = encode_heads(&tk, p.k_cache, rows, p.H_kv, D, kBf16, 1, box);
+  if (st == PDA_OK) st = encode_heads(&tv, p.v_cache, rows, p.H_kv, D, kBf16, 1, box);
+  if (st != PDA_OK) return st;
+  // no more blocks than the host's bound on the units can keep busy
+  const long long cap = static_cast<long long>(p.max_blocks) * p.block_size;
+  const long long keys = p.max_context_len < cap ? p.max_context_len : cap;
+  const int tiles = static_cast<int>((keys + kChunkKeys - 1) / kChunkKeys);
+  const int lt = kItemRowsLog2 - g_shift;
+  const long long items = ((static_cast<long long>(p.T) >> lt) + p.B) * p.H_kv;
+  const int grid = chunk_workers(items * (tiles + 1), sms, kMinWorkerUnits);
+  chunk_tc_kernel<D, kBf16><<<grid, kThreads, smem_bytes<D>(), stream>>>(tq, tk, tv, p, g_shift,
+                                                                         partial);
+  if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+  if (grid == 1 || tiles < 2 * kMinPieceTiles) return PDA_OK;  // no item is cut
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid - 1), 256 / kMergeRows);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D, kBf16>, p, g_shift,
+                            static_cast<const float*>(partial), grid) == cudaSuccess
+             ? PDA_OK
+             : PDA_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t chunk_tc_workspace(int sms, int D) {
+  return static_cast<size_t>(sms) * 2 * 256 * (D + 4) * sizeof(float);
+}
+
+pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int dev, int sms,
+                           void* workspace, cudaStream_t stream) {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (g_encode == nullptr) return PDA_ERR_CUDA;
+  float* partial = static_cast<float*>(workspace);
+  if (kv_dtype == PDA_BF16)
+    return D == 128 ? launch<128, true>(p, dev, sms, partial, stream)
+                    : launch<64, true>(p, dev, sms, partial, stream);
+  return D == 128 ? launch<128, false>(p, dev, sms, partial, stream)
+                  : launch<64, false>(p, dev, sms, partial, stream);
+}
+
+}  // namespace pda

@@ -1,0 +1,29 @@
+// chunk_internal.h -- what the translation units of chunk attention share.
+#pragma once
+
+#include "pda_internal.h"
+
+namespace pda {
+
+struct ChunkParams {
+  void* out;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start;
+  int32_t* error_word;
+  float scale_log2;  // softmax scale times log2 e (and the cache's K scale)
+  float v_scale;
+  int B, T, H, H_kv, G, max_blocks, max_context_len, block_size, num_blocks;
+};
+
+// Workspace bytes of the tensor-core kernel on `sms` SMs.
+size_t chunk_tc_workspace(int sms, int D);
+
+// 16-bit caches on the tensor cores.
+pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int dev, int sms,
+                           void* workspace, cudaStream_t stream);
+
+}  // namespace pda
