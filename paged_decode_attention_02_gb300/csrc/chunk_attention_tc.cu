@@ -9,9 +9,11 @@
 //
 // One block per SM walks a contiguous range of the launch's units (chunk_plan.h). Warps:
 //   0-3, 4-7  softmax of row group 0 and 1 (a thread per row: TMEM lane = row)
-//   8         plans the block's pieces, publishes them, and loads Q, K and V with TMA
+//   8         plans the block's pieces, publishes them, and loads Q and K with TMA
 //   9         issues the matrix instructions
-//   10, 11    clean the V tiles at the diagonal and the end (see below)
+//   10        loads V with TMA
+//   12-15     clean the V tiles at the diagonal and the end (see below)
+// The softmax warps take the registers that the others give back (setmaxnreg).
 // An item of more than 128 rows gives each group 128 rows; both read every K and V tile. An
 // item of fewer gives both groups the same rows and alternate tiles, merged at the end, so
 // that one group's softmax still runs under the other's products.
@@ -19,7 +21,7 @@
 //
 // V tiles that reach past what some row may see (the diagonal ones) multiply zero
 // probabilities with later tokens' V, or with whatever lies behind the last token; 0 * NaN
-// would reach the output. Warps 10 and 11 zero the rows behind the end, replace non-finite
+// would reach the output. Warps 12 to 15 zero the rows behind the end, replace non-finite
 // values by zeros and note their rows, and the epilogue adds those values back to the rows
 // that do see them.
 #include <cudaTypedefs.h>
@@ -34,7 +36,9 @@
 namespace pda {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;  // 2 x 128 of each: what 512 x 128 give
+constexpr int kCleaners = 4;
 constexpr int kDescs = 4;
 constexpr int kMinPieceTiles = 6;   // a cut item's pieces are at least this long
 constexpr int kMinWorkerUnits = 4;  // a worker's range is at least this long
@@ -68,13 +72,23 @@ struct Cfg {
   static constexpr int kV = D == 128 ? 2 : 5;
 };
 
-// One box of a 3-D tensor map into shared memory, completing on `bar`.
+// One box of a tensor map into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* tm, int c0, int c1, int c2,
                                         uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_box4(void* dst, const CUtensorMap* tm, int c0, int c1, int c2,
+                                         int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "r"(smem_addr(bar))
       : "memory");
 }
 
@@ -187,6 +201,63 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(kFullMask, mbar_wait_bounded(bar, parity));
 }
 
+// The ids of a piece's blocks, 32 at a time: lane l holds that of block l % nbt of tile
+// l / nbt of the current group of tiles, the next group's already under way.
+struct BlockIds {
+  const int32_t* table;
+  int bs, nbt, per_group;  // block size, blocks of a tile, tiles of a group
+  int ja, nt, end, num_blocks;
+  int group, ids, next;
+
+  __device__ __forceinline__ int block_of(int gr, bool* used) const {
+    const int lane = threadIdx.x & 31, t = gr * per_group + lane / nbt;
+    const long long key = static_cast<long long>(ja + t) * kChunkKeys + (lane % nbt) * bs;
+    *used = t < nt && key < end;
+    return *used ? static_cast<int>(key / bs) : 0;
+  }
+  __device__ __forceinline__ int fetch(int gr) const {
+    bool used;
+    const int blk = block_of(gr, &used);
+    return used ? table[blk] : 0;
+  }
+  __device__ __forceinline__ void start(const ChunkParams& p, const Desc& d) {
+    bs = p.block_size;
+    nbt = bs >= kChunkKeys ? 1 : kChunkKeys / bs;
+    per_group = 32 / nbt;
+    table = p.block_tables + d.table;
+    ja = d.ja;
+    nt = d.jb - d.ja;
+    end = d.end;
+    num_blocks = p.num_blocks;
+    group = -1;
+    next = fetch(0);
+  }
+  // Makes tile t's group current; *bad_from falls to the first key of a block whose id is out
+  // of range (any block stands in: the rows that see it become NaN).
+  __device__ __forceinline__ void advance(int t, int* bad_from, int32_t* error_word) {
+    if (t / per_group == group) return;
+    group = t / per_group;
+    ids = next;
+    if (ids < 0 || ids >= num_blocks) {
+      if (bad_from != nullptr) {
+        bool used;
+        const int blk = block_of(group, &used);
+        atomicMin(bad_from, max(blk * bs, (ja + group * per_group + (threadIdx.x & 31) / nbt) * kChunkKeys));
+        atomic_or_error(error_word, PDA_DEVERR_BLOCK_ID);
+        __threadfence_block();
+      }
+      ids = 0;
+    }
+    __syncwarp();
+    next = fetch(group + 1);
+  }
+  // Cache row of block `blk` of tile t (all lanes call).
+  __device__ __forceinline__ int row(int t, int blk) const {
+    const int id = __shfl_sync(kFullMask, ids, ((t - group * per_group) * nbt + blk) & 31);
+    return id * bs + (bs > kChunkKeys ? ((ja + t) * kChunkKeys) % bs : 0);
+  }
+};
+
 struct Groups {
   int n0, n1;  // steps of each group
 };
@@ -199,6 +270,12 @@ __device__ __forceinline__ Groups groups_of(const Desc& d) {
 __device__ __forceinline__ bool nonfinite16(uint32_t w, uint32_t exp_mask, uint32_t exp_one) {
   // per half: (exponent bits) + 1 carries into the sign place when they are all ones
   return (((w & exp_mask) + exp_one) & 0x80008000u) != 0;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 template <bool kBf16>
@@ -237,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ms.k_empty[i], 1);
       mbar_init(&ms.v_full[i], 1);
       mbar_init(&ms.v_empty[i], 1);
-      mbar_init(&ms.clean[i], 2);
+      mbar_init(&ms.clean[i], kCleaners);
     }
     mbar_init(&ms.q_full, 1);
     mbar_init(&ms.q_empty, 1);
@@ -251,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ms.done, 1);
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(&ms.desc_full[i], 1);
-      mbar_init(&ms.desc_empty[i], 1 + 2 + 8);  // matrix warp, cleaners, softmax warps
+      mbar_init(&ms.desc_empty[i], 1 + 1 + kCleaners + 8);  // all that read it
     }
     fence_mbar_init();
   }
@@ -282,319 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   bool timed_out = false;
-  if (warp == 8) {
-    // ================================================================ plan and load
-    Where w{};
-    Where w_end{};
-    const bool mine = static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0;
-    long long u = 0, u_end = 0;
-    if (mine) {
-      u_end = cut_of(p, pl, lt, blockIdx.x + 1, &w_end);
-      u = cut_of(p, pl, lt, blockIdx.x, &w);
-      if (u < u_end && u >= w.start + w.r.tiles(w.i) + 1) w = locate(p, pl, lt, u);
-    }
-    __syncwarp();
-    fence_proxy_async_smem();  // the plan's shared memory becomes load stages
-    int item = 0;
-    unsigned loads = 0;  // tiles loaded so far, of K and of V
-    const int bs = p.block_size;
-    const int nbt = bs >= kChunkKeys ? 1 : kChunkKeys / bs;  // blocks of a tile
-    const int box_rows = bs >= kChunkKeys ? kChunkKeys : bs;
-    const int tiles_per_group = 32 / nbt;
-    while (u < u_end && !timed_out) {
-      const ChunkReq r = w.r;
-      const int tiles = r.tiles(w.i);
-      const long long end = w.start + tiles + 1;
-      const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
-      const int ja = u == w.start ? 0 : static_cast<int>(u - w.start - 1);
-      const int jb = u_end >= end ? tiles : static_cast<int>(u_end - w.start - 1);
-      const int slot = item % kDescs;
-      Desc& d = ms.desc[slot];
-      if (!warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
-        timed_out = true;
-        break;
-      }
-      const int pos0 = r.L - r.n + tok0;
-      const int half = 128 >> g_shift;  // tokens of a row group
-      const bool single = tokens <= half;
-      const int kv_end = pos0 + tokens;
-      const long long table = static_cast<long long>(w.b) * p.max_blocks;
-      const int row0 = p.query_start[w.b] + tok0;
-      if (lane == 0) {
-        d.valid = 1;
-        d.row0 = row0;
-        d.tokens = tokens;
-        d.pos0 = pos0;
-        d.kh = w.kh;
-        d.ja = ja;
-        d.jb = jb;
-        d.tiles0 = single ? tiles : ((pos0 + half - 1) >> 7) + 1;
-        d.tiles1 = tiles;
-        d.single = single;
-        d.jc = (pos0 + 1) >> 7;
-        d.end = kv_end;
-        d.slot = ja == 0 && jb == tiles ? -1 : static_cast<int>(blockIdx.x) * 2 + (ja == 0 ? 1 : 0);
-        d.bad_from = 0x7fffffff;
-        d.table = table;
-        for (int k = 0; k < 12; ++k) d.nonfinite[k >> 2][k & 3] = 0;
-        mbar_arrive(&ms.desc_full[slot]);
-      }
-      __syncwarp();
-      // Q
-      if (!warp_wait(&ms.q_empty, (item & 1) ^ 1)) {
-        timed_out = true;
-        break;
-      }
-      const int q_tiles = single ? 1 : 2;
-      if (lane == 0) mbar_arrive_expect_tx(&ms.q_full, q_tiles * C::kTile);
-      __syncwarp();
-      if (lane < q_tiles * C::kHalves) {
-        const int g = lane / C::kHalves, h = lane % C::kHalves;
-        tma_box(qs + g * C::kTile + h * C::kHalf, &tm_q, 64 * h, w.kh << g_shift,
-                   row0 + g * half, &ms.q_full);
-      }
-      // K and V
-      const int nt = jb - ja;
-      const int pairs = single ? (nt + 1) >> 1 : nt;
-      int group = -1, ids = 0, next_ids = 0;
-      auto fetch = [&](int gr) {  // the ids of tiles ja + gr * tiles_per_group + ..
-        const int t = gr * tiles_per_group + lane / nbt;
-        const int blk = bs >= kChunkKeys ? static_cast<int>((static_cast<long long>(ja + t) * kChunkKeys) / bs)
-                                         : (ja + t) * nbt + lane % nbt;
-        const bool used = t < nt && static_cast<long long>(blk) * bs < kv_end;
-        return used ? p.block_tables[table + blk] : 0;
-      };
-      next_ids = fetch(0);
-      for (int s = 0; s < pairs && !timed_out; ++s) {
-        const int first = single ? 2 * s : s, count = single ? min(2, nt - first) : 1;
-        if (first / tiles_per_group != group) {
-          group = first / tiles_per_group;
-          ids = next_ids;
-          const int t = group * tiles_per_group + lane / nbt;
-          const int blk = bs >= kChunkKeys ? static_cast<int>((static_cast<long long>(ja + t) * kChunkKeys) / bs)
-                                           : (ja + t) * nbt + lane % nbt;
-          const bool used = t < nt && static_cast<long long>(blk) * bs < kv_end;
-          if (used && (ids < 0 || ids >= p.num_blocks)) {
-            // the rows that see the block become NaN in the epilogue; any block stands in
-            atomicMin(&d.bad_from, max(blk * bs, (ja + t) * kChunkKeys));
-            atomic_or_error(p.error_word, PDA_DEVERR_BLOCK_ID);
-            ids = 0;
-          }
-          __threadfence_block();
-          __syncwarp();
-          next_ids = fetch(group + 1);
-        }
-        for (int x = 0; x < 2 * count; ++x) {
-          const bool is_v = x >= count;
-          const int t = first + (is_v ? x - count : x);
-          const unsigned at = loads + t;
-          const int st = is_v ? at % NV : at % NK;
-          const unsigned turn = is_v ? at / NV : at / NK;
-          uint64_t* full = is_v ? &ms.v_full[st] : &ms.k_full[st];
-          if (!warp_wait(is_v ? &ms.v_empty[st] : &ms.k_empty[st], (turn & 1) ^ 1)) {
-            timed_out = true;
-            break;
-          }
-          const int key0 = (ja + t) * kChunkKeys;
-          const int boxes = min(nbt, (kv_end - key0 + box_rows - 1) / box_rows);
-          if (lane == 0)
-            mbar_arrive_expect_tx(full, boxes * C::kHalves * box_rows * 128);
-          __syncwarp();
-          const int blk = lane / C::kHalves, h = lane % C::kHalves;
-          const int id = __shfl_sync(kFullMask, ids, ((t - group * tiles_per_group) * nbt + blk) & 31);
-          if (blk < boxes) {
-            const int row = id * bs + (bs > kChunkKeys ? key0 % bs : 0);
-            tma_box((is_v ? vs : ks) + st * C::kTile + h * C::kHalf + blk * box_rows * 128,
-                        is_v ? &tm_v : &tm_k, 64 * h, w.kh, row, full);
-          }
-        }
-      }
-      loads += nt;
-      ++item;
-      // the next item
-      u = end;
-      if (u < u_end) {
-        w.start = end;
-        if (w.i + 1 < r.items()) {
-          ++w.i;
-        } else {
-          w.i = 0;
-          if (++w.kh == p.H_kv) {
-            w.kh = 0;
-            do {
-              w.r = chunk_req(p, ++w.b, lt);
-            } while (w.r.n == 0);
-          }
-        }
-      }
-    }
-    if (!timed_out) {
-      const int slot = item % kDescs;
-      if (warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
-        if (lane == 0) {
-          ms.desc[slot].valid = 0;
-          mbar_arrive(&ms.desc_full[slot]);
-        }
-      } else {
-        timed_out = true;
-      }
-    }
-    if (timed_out) {
-      // copies in flight land before the block may leave: wait for the last one of each stage
-      for (int st = 0; st < 2 * 5; ++st) {
-        uint64_t* full = st < 5 ? &ms.k_full[st] : &ms.v_full[st - 5];
-        warp_wait(full, 0);
-        warp_wait(full, 1);
-      }
-      warp_wait(&ms.q_full, 0);
-      warp_wait(&ms.q_full, 1);
-    }
-  } else if (warp == 9) {
-    // ================================================================ matrix instructions
-    if (lane == 0) {
-      const bool negate = p.scale_log2 < 0.f;  // S is compared and scaled by |scale|
-      const uint32_t id_qk = mma_idesc(kBf16, kChunkKeys, negate, false);
-      const uint32_t id_pv = mma_idesc(kBf16, D, false, true);
-      const uint32_t k0 = smem_addr(ks), v0 = smem_addr(vs), q0 = smem_addr(qs);
-      unsigned loads = 0, p_phase = 0;
-      for (int item = 0; !timed_out; ++item) {
-        const int slot = item % kDescs;
-        if (!mbar_wait_bounded(&ms.desc_full[slot], (item / kDescs) & 1)) {
-          timed_out = true;
-          break;
-        }
-        const Desc& d = ms.desc[slot];
-        if (!d.valid) break;
-        const Groups gr = groups_of(d);
-        const int nt = d.jb - d.ja, ja = d.ja, kv_end = d.end;
-        const bool single = d.single != 0;
-        const int last_g = gr.n1 >= gr.n0 ? 1 : 0, steps = max(gr.n0, gr.n1);
-        if (!mbar_wait_bounded(&ms.q_full, item & 1)) {
-          timed_out = true;
-          break;
-        }
-        tc_fence_after();
-        auto qk = [&](int g, int s) {
-          const int t = single ? 2 * s + g : s;
-          const unsigned at = loads + t;
-          const int st = at % NK;
-          if (!mbar_wait_bounded(&ms.k_full[st], (at / NK) & 1)) return false;
-          tc_fence_after();
-          const uint32_t a = q0 + (single ? 0 : g * C::kTile), b = k0 + st * C::kTile;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * C::kHalf + (k & 3) * 32;
-            mma_f16_ss(tmem + g * 128, smem_desc_sw128(a + off, 16, 1024),
-                       smem_desc_sw128(b + off, 16, 1024), id_qk, k > 0);
-          }
-          mma_commit(&ms.s_full[g]);
-          if (single || g == 1) mma_commit(&ms.k_empty[st]);
-          if (g == last_g && s == steps - 1) mma_commit(&ms.q_empty);
-          return true;
-        };
-        auto pv = [&](int g, int s, bool last) {
-          const int t = single ? 2 * s + g : s;
-          const unsigned at = loads + t;
-          const int st = at % NV;
-          if (!mbar_wait_bounded(&ms.v_full[st], (at / NV) & 1)) return false;
-          if (!mbar_wait_bounded(&ms.clean[st], (at / NV) & 1)) return false;
-          if (!mbar_wait_bounded(&ms.p_full[g], (p_phase >> g) & 1)) return false;
-          p_phase ^= 1u << g;
-          tc_fence_after();
-          const uint32_t b = v0 + st * C::kTile;
-          const int ksteps = (min(kChunkKeys, kv_end - (ja + t) * kChunkKeys) + 15) >> 4;
-          for (int k = 0; k < ksteps; ++k)
-            mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * k,
-                       smem_desc_sw128(b + k * 2048, C::kHalf, 1024), id_pv, s > 0 || k > 0);
-          if (single || g == 1) mma_commit(&ms.v_empty[st]);
-          if (last) mma_commit(&ms.o_full[g]);
-          return true;
-        };
-        bool ok = true;
-        if (gr.n0 > 0) ok = qk(0, 0);
-        if (ok && gr.n1 > 0) ok = qk(1, 0);
-        for (int s = 0; ok && s < steps; ++s) {
-          if (s < gr.n0) {
-            ok = pv(0, s, s + 1 == gr.n0);
-            if (ok && s + 1 < gr.n0) ok = qk(0, s + 1);
-          }
-          if (ok && s < gr.n1) {
-            ok = pv(1, s, s + 1 == gr.n1);
-            if (ok && s + 1 < gr.n1) ok = qk(1, s + 1);
-          }
-        }
-        if (!ok) {
-          timed_out = true;
-          break;
-        }
-        loads += nt;
-        mbar_arrive(&ms.desc_empty[slot]);
-      }
-      // nothing of this thread's is in flight when the block gives its TMEM back
-      mma_commit(&ms.done);
-      if (!mbar_wait_bounded(&ms.done, 0)) timed_out = true;
-    }
-    __syncwarp();
-  } else if (warp >= 10) {
-    // ================================================================ clean V tiles
-    const int half = warp - 10;
-    unsigned loads = 0;
-    for (int item = 0; !timed_out; ++item) {
-      const int slot = item % kDescs;
-      if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
-        timed_out = true;
-        break;
-      }
-      Desc& d = ms.desc[slot];
-      if (!d.valid) break;
-      const int ja = d.ja, nt = d.jb - ja, jc = d.jc, kv_end = d.end;
-      for (int t = 0; t < nt; ++t) {
-        const unsigned at = loads + t;
-        const int st = at % NV;
-        if (!warp_wait(&ms.v_full[st], (at / NV) & 1)) {
-          timed_out = true;
-          break;
-        }
-        if (ja + t < jc) {  // every row sees every key
-          if (lane == 0) mbar_arrive(&ms.clean[st]);
-          continue;
-        }
-        const int keys = min(kChunkKeys, kv_end - (ja + t) * kChunkKeys);
-        const int rows = (keys + 15) & ~15;  // what the products read
-        constexpr uint32_t kMask = kBf16 ? 0x7f807f80u : 0x7c007c00u;
-        constexpr uint32_t kOne = kBf16 ? 0x00800080u : 0x04000400u;
-        // a lane takes one 16-byte chunk of every fourth row
-        for (int r = half * 4 + (lane >> 3); r < rows; r += 8) {
-          for (int h = 0; h < C::kHalves; ++h) {
-            uint4* at16 = reinterpret_cast<uint4*>(vs + st * C::kTile + h * C::kHalf + r * 128) +
-                          ((lane & 7) ^ (r & 7));
-            if (r >= keys) {
-              *at16 = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 v = *at16;
-            if (nonfinite16(v.x, kMask, kOne) || nonfinite16(v.y, kMask, kOne) ||
-                nonfinite16(v.z, kMask, kOne) || nonfinite16(v.w, kMask, kOne)) {
-              uint32_t* e = &v.x;
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t hit = ((e[k] & kMask) + kOne) & 0x80008000u;
-                e[k] &= ~((hit >> 15) * 0xffffu);
-              }
-              *at16 = v;
-              atomicOr(&d.nonfinite[ja + t - jc][r >> 5], 1u << (r & 31));
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        __threadfence_block();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.clean[st]);
-      }
-      loads += nt;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
-    }
-  } else {
+  if (warp < 8) {
+    reg_inc<kSoftmaxRegs>();
     // ================================================================ softmax and output
     const int g = warp >> 2;
     const int row = tid & 127;
@@ -642,12 +408,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int k = 4; k < kChunkKeys; k += 4) {
-          mx[0] = fmaxf(mx[0], x[k]);
-          mx[1] = fmaxf(mx[1], x[k + 1]);
-          mx[2] = fmaxf(mx[2], x[k + 2]);
-          mx[3] = fmaxf(mx[3], x[k + 3]);
-        }
+        for (int k = 4; k + 4 < kChunkKeys; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[k + 2 * e], x[k + 2 * e + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[kChunkKeys - 4 + e]);
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (s == 0) {
           m = top;
@@ -670,20 +435,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.f : lift - m * sl;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 sl2 = make_float2(sl, sl), ref2 = make_float2(ref, ref);
+        float2 sum[2] = {};
 #pragma unroll
         for (int k = 0; k < kChunkKeys; k += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float a = ex2(fmaf(x[k + e], sl, ref)), b = ex2(fmaf(x[k + e + 1], sl, ref));
-            sum[e & 2] += a;
-            sum[(e & 2) + 1] += b;
-            pk[e / 2] = pack2<kBf16>(a, b);
+            float2 a = __ffma2_rn(make_float2(x[k + e], x[k + e + 1]), sl2, ref2);
+            a.x = ex2(a.x);
+            a.y = ex2(a.y);
+            sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], a);
+            pk[e / 2] = pack2<kBf16>(a.x, a.y);
           }
           tmem_st16(tS + k / 2, pk);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&ms.p_full[g]);
@@ -799,6 +566,347 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
     }
+  } else {
+    reg_dec<kOtherRegs>();
+  if (warp == 8) {
+    // ================================================================ plan, load Q and K
+    Where w{};
+    Where w_end{};
+    const bool mine = static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0;
+    long long u = 0, u_end = 0;
+    if (mine) {
+      u_end = cut_of(p, pl, lt, blockIdx.x + 1, &w_end);
+      u = cut_of(p, pl, lt, blockIdx.x, &w);
+      if (u < u_end && u >= w.start + w.r.tiles(w.i) + 1) w = locate(p, pl, lt, u);
+    }
+    __syncwarp();
+    fence_proxy_async_smem();  // the plan's shared memory becomes load stages
+    int item = 0;
+    int k_at = 0, k_turn = 0;
+    while (u < u_end && !timed_out) {
+      const ChunkReq r = w.r;
+      const int tiles = r.tiles(w.i);
+      const long long end = w.start + tiles + 1;
+      const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
+      const int ja = u == w.start ? 0 : static_cast<int>(u - w.start - 1);
+      const int jb = u_end >= end ? tiles : static_cast<int>(u_end - w.start - 1);
+      const int slot = item % kDescs;
+      Desc& d = ms.desc[slot];
+      if (!warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
+        timed_out = true;
+        break;
+      }
+      const int pos0 = r.L - r.n + tok0;
+      const int half = 128 >> g_shift;  // tokens of a row group
+      const bool single = tokens <= half;
+      const int kv_end = pos0 + tokens;
+      const long long table = static_cast<long long>(w.b) * p.max_blocks;
+      const int row0 = p.query_start[w.b] + tok0;
+      if (lane == 0) {
+        d.valid = 1;
+        d.row0 = row0;
+        d.tokens = tokens;
+        d.pos0 = pos0;
+        d.kh = w.kh;
+        d.ja = ja;
+        d.jb = jb;
+        d.tiles0 = single ? tiles : ((pos0 + half - 1) >> 7) + 1;
+        d.tiles1 = tiles;
+        d.single = single;
+        d.jc = (pos0 + 1) >> 7;
+        d.end = kv_end;
+        d.slot = ja == 0 && jb == tiles ? -1 : static_cast<int>(blockIdx.x) * 2 + (ja == 0 ? 1 : 0);
+        d.bad_from = 0x7fffffff;
+        d.table = table;
+        for (int k = 0; k < 12; ++k) d.nonfinite[k >> 2][k & 3] = 0;
+        mbar_arrive(&ms.desc_full[slot]);
+      }
+      __syncwarp();
+      // Q
+      if (!warp_wait(&ms.q_empty, (item & 1) ^ 1)) {
+        timed_out = true;
+        break;
+      }
+      const int q_tiles = single ? 1 : 2;
+      if (lane == 0) mbar_arrive_expect_tx(&ms.q_full, q_tiles * C::kTile);
+      __syncwarp();
+      if (lane < q_tiles * C::kHalves) {
+        const int g = lane / C::kHalves, h = lane % C::kHalves;
+        tma_box(qs + g * C::kTile + h * C::kHalf, &tm_q, 64 * h, w.kh << g_shift,
+                   row0 + g * half, &ms.q_full);
+      }
+      // K: a box of 64 elements of a block's rows (128 at most) for each half of a row
+      const int nt = jb - ja;
+      const int box_rows = min(p.block_size, kChunkKeys);
+      BlockIds ids;
+      ids.start(p, d);
+      for (int t = 0; t < nt; ++t) {
+        ids.advance(t, &d.bad_from, p.error_word);
+        if (!warp_wait(&ms.k_empty[k_at], k_turn ^ 1)) {
+          timed_out = true;
+          break;
+        }
+        const int boxes = min(ids.nbt, (kv_end - (ja + t) * kChunkKeys + box_rows - 1) / box_rows);
+        if (lane == 0)
+          mbar_arrive_expect_tx(&ms.k_full[k_at], boxes * C::kHalves * box_rows * 128);
+        __syncwarp();
+        const int blk = lane / C::kHalves, h = lane % C::kHalves;
+        const int row = ids.row(t, blk);
+        if (blk < boxes)
+          tma_box(ks + k_at * C::kTile + h * C::kHalf + blk * box_rows * 128, &tm_k, 64 * h, w.kh,
+                  row, &ms.k_full[k_at]);
+        if (++k_at == NK) {
+          k_at = 0;
+          k_turn ^= 1;
+        }
+      }
+      ++item;
+      // the next item
+      u = end;
+      if (u < u_end) {
+        w.start = end;
+        if (w.i + 1 < r.items()) {
+          ++w.i;
+        } else {
+          w.i = 0;
+          if (++w.kh == p.H_kv) {
+            w.kh = 0;
+            do {
+              w.r = chunk_req(p, ++w.b, lt);
+            } while (w.r.n == 0);
+          }
+        }
+      }
+    }
+    if (!timed_out) {
+      const int slot = item % kDescs;
+      if (warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
+        if (lane == 0) {
+          ms.desc[slot].valid = 0;
+          mbar_arrive(&ms.desc_full[slot]);
+        }
+      } else {
+        timed_out = true;
+      }
+    }
+    if (timed_out) {
+      // copies in flight land before the block may leave
+      for (int st = 0; st < 5; ++st)
+        for (int turn = 0; turn < 2; ++turn) warp_wait(&ms.k_full[st], turn);
+      warp_wait(&ms.q_full, 0);
+      warp_wait(&ms.q_full, 1);
+    }
+  } else if (warp == 9) {
+    // ================================================================ matrix instructions
+    // The whole warp walks the steps, so that descriptors stay in uniform registers; one
+    // elected lane issues.
+    const bool leader = elect_one();
+    const bool negate = p.scale_log2 < 0.f;  // S is compared and scaled by |scale|
+    const uint32_t id_qk = mma_idesc(kBf16, kChunkKeys, negate, false);
+    const uint32_t id_pv = mma_idesc(kBf16, D, false, true);
+    const uint64_t dk0 = smem_desc_sw128(smem_addr(ks), 16, 1024);
+    const uint64_t dq0 = smem_desc_sw128(smem_addr(qs), 16, 1024);
+    const int box_rows = min(p.block_size, kChunkKeys);
+    const uint64_t dv0 = smem_desc_sw128(smem_addr(vs), box_rows * 128, 1024);
+    // 16 rows further down: in the same box, or in the next one (whose halves are in between)
+    const int box_log2 = 31 - __clz(box_rows);
+    int k_at = 0, k_turn = 0, v_at = 0, v_turn = 0;  // stage and parity of the next K, V tile
+    unsigned p_phase = 0;
+    for (int item = 0; !timed_out; ++item) {
+      const int slot = item % kDescs;
+      if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
+        timed_out = true;
+        break;
+      }
+      const Desc& d = ms.desc[slot];
+      if (!__shfl_sync(kFullMask, d.valid, 0)) break;
+      const Groups grp = groups_of(d);
+      const int n0 = __shfl_sync(kFullMask, grp.n0, 0), n1 = __shfl_sync(kFullMask, grp.n1, 0);
+      const bool single = __shfl_sync(kFullMask, d.single, 0) != 0;
+      // keys the rows may see from the piece's first tile on
+      const int keys = __shfl_sync(kFullMask, d.end - d.ja * kChunkKeys, 0);
+      const int steps = max(n0, n1), last_g = n1 >= n0 ? 1 : 0;
+      if (!warp_wait(&ms.q_full, item & 1)) {
+        timed_out = true;
+        break;
+      }
+      tc_fence_after();
+      // A tile is used by both groups, the second releasing it, or (single) by one.
+      auto qk = [&](int g, int s) {
+        if (!warp_wait(&ms.k_full[k_at], k_turn)) return false;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t a = dq0 + (single ? 0 : g * (C::kTile >> 4)), b = dk0 + k_at * (C::kTile >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
+            mma_f16_ss(tmem + g * 128, a + off, b + off, id_qk, k > 0);
+          }
+          mma_commit(&ms.s_full[g]);
+          if (single || g == 1) mma_commit(&ms.k_empty[k_at]);
+          if (g == last_g && s == steps - 1) mma_commit(&ms.q_empty);
+        }
+        __syncwarp();
+        if (single || g == 1) {
+          if (++k_at == NK) {
+            k_at = 0;
+            k_turn ^= 1;
+          }
+        }
+        return true;
+      };
+      auto pv = [&](int g, int s, bool last) {
+        if (!warp_wait(&ms.v_full[v_at], v_turn) || !warp_wait(&ms.clean[v_at], v_turn) ||
+            !warp_wait(&ms.p_full[g], (p_phase >> g) & 1))
+          return false;
+        p_phase ^= 1u << g;
+        tc_fence_after();
+        const int left = keys - (single ? 2 * s + g : s) * kChunkKeys;
+        if (leader) {
+          const uint64_t b = dv0 + v_at * (C::kTile >> 4);
+#pragma unroll
+          for (int k = 0; k < kChunkKeys / 16; ++k)
+            if (16 * k < left)
+              mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * k,
+                         b + ((((16 * k) >> box_log2) << box_log2) * (D * 2) + ((16 * k) & (box_rows - 1)) * 128) / 16,
+                         id_pv, s > 0 || k > 0);
+          if (single || g == 1) mma_commit(&ms.v_empty[v_at]);
+          if (last) mma_commit(&ms.o_full[g]);
+        }
+        __syncwarp();
+        if (single || g == 1) {
+          if (++v_at == NV) {
+            v_at = 0;
+            v_turn ^= 1;
+          }
+        }
+        return true;
+      };
+      bool ok = true;
+      if (n0 > 0) ok = qk(0, 0);
+      if (ok && n1 > 0) ok = qk(1, 0);
+      for (int s = 0; ok && s < steps; ++s) {
+        if (s < n0) {
+          ok = pv(0, s, s + 1 == n0);
+          if (ok && s + 1 < n0) ok = qk(0, s + 1);
+        }
+        if (ok && s < n1) {
+          ok = pv(1, s, s + 1 == n1);
+          if (ok && s + 1 < n1) ok = qk(1, s + 1);
+        }
+      }
+      if (!ok) {
+        timed_out = true;
+        break;
+      }
+      if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
+    }
+    // nothing of this warp's is in flight when the block gives its TMEM back
+    if (leader) mma_commit(&ms.done);
+    if (!warp_wait(&ms.done, 0)) timed_out = true;
+  } else if (warp == 10) {
+    // ================================================================ load V
+    // A block's rows (128 at most) come as one box, both halves of its rows one behind the
+    // other: the P V product takes 16 rows of one block at a time, so blocks need not join.
+    int v_at = 0, v_turn = 0;
+    for (int item = 0; !timed_out; ++item) {
+      const int slot = item % kDescs;
+      if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
+        timed_out = true;
+        break;
+      }
+      const Desc& d = ms.desc[slot];
+      if (!d.valid) break;
+      const int box_rows = min(p.block_size, kChunkKeys);
+      const int kh = d.kh;
+      BlockIds ids;
+      ids.start(p, d);
+      for (int t = 0; t < ids.nt; ++t) {
+        ids.advance(t, nullptr, nullptr);
+        if (!warp_wait(&ms.v_empty[v_at], v_turn ^ 1)) {
+          timed_out = true;
+          break;
+        }
+        const int boxes = min(ids.nbt, (ids.end - (ids.ja + t) * kChunkKeys + box_rows - 1) / box_rows);
+        if (lane == 0)
+          mbar_arrive_expect_tx(&ms.v_full[v_at], boxes * box_rows * D * 2);
+        __syncwarp();
+        const int row = ids.row(t, lane);
+        if (lane < boxes)
+          tma_box4(vs + v_at * C::kTile + lane * box_rows * D * 2, &tm_v, 0, row, 0, kh,
+                   &ms.v_full[v_at]);
+        if (++v_at == NV) {
+          v_at = 0;
+          v_turn ^= 1;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
+    }
+    if (timed_out)
+      for (int st = 0; st < 5; ++st)
+        for (int turn = 0; turn < 2; ++turn) warp_wait(&ms.v_full[st], turn);
+  } else if (warp >= 12) {
+    // ================================================================ clean V tiles
+    const int part = warp - 12;
+    const int box_rows = min(p.block_size, kChunkKeys);
+    unsigned loads = 0;
+    for (int item = 0; !timed_out; ++item) {
+      const int slot = item % kDescs;
+      if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
+        timed_out = true;
+        break;
+      }
+      Desc& d = ms.desc[slot];
+      if (!d.valid) break;
+      const int ja = d.ja, nt = d.jb - ja, jc = d.jc, kv_end = d.end;
+      for (int t = 0; t < nt; ++t) {
+        const unsigned at = loads + t;
+        const int st = at % NV;
+        if (!warp_wait(&ms.v_full[st], (at / NV) & 1)) {
+          timed_out = true;
+          break;
+        }
+        if (ja + t < jc) {  // every row sees every key
+          if (lane == 0) mbar_arrive(&ms.clean[st]);
+          continue;
+        }
+        const int keys = min(kChunkKeys, kv_end - (ja + t) * kChunkKeys);
+        const int rows = (keys + 15) & ~15;  // what the products read
+        constexpr uint32_t kMask = kBf16 ? 0x7f807f80u : 0x7c007c00u;
+        constexpr uint32_t kOne = kBf16 ? 0x00800080u : 0x04000400u;
+        // a lane takes one 16-byte chunk of both halves of a row
+        for (int r = part * 4 + (lane >> 3); r < rows; r += 4 * kCleaners) {
+          for (int h = 0; h < C::kHalves; ++h) {
+            const int byte = (r / box_rows) * box_rows * D * 2 + (h * box_rows + r % box_rows) * 128;
+            uint4* at16 = reinterpret_cast<uint4*>(vs + st * C::kTile + byte) + (lane & 7);
+            if (r >= keys) {
+              *at16 = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 v = *at16;
+            if (nonfinite16(v.x, kMask, kOne) || nonfinite16(v.y, kMask, kOne) ||
+                nonfinite16(v.z, kMask, kOne) || nonfinite16(v.w, kMask, kOne)) {
+              uint32_t* e = &v.x;
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t hit = ((e[k] & kMask) + kOne) & 0x80008000u;
+                e[k] &= ~((hit >> 15) * 0xffffu);
+              }
+              *at16 = v;
+              atomicOr(&d.nonfinite[ja + t - jc][r >> 5], 1u << (r & 31));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __threadfence_block();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.clean[st]);
+      }
+      loads += nt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
+    }
+  }
   }
   if (timed_out) atomic_or_error(p.error_word, PDA_DEVERR_TIMEOUT);
   tc_fence_before();
@@ -888,6 +996,26 @@ pda_status encode_heads(CUtensorMap* tm, const void* base, long long rows, int h
   return r == CUDA_SUCCESS ? PDA_OK : PDA_ERR_INVALID_ARG;
 }
 
+// The V cache with a row's 64-element halves as a dimension of their own: boxes of `box_rows`
+// rows of both halves of one head, half after half.
+pda_status encode_v(CUtensorMap* tm, const void* base, long long rows, int heads, int D, bool bf16,
+                    int box_rows) {
+  const cuuint64_t dims[4] = {64u, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(D / 64),
+                              static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(heads) * D * 2, 128u,
+                                 static_cast<cuuint64_t>(D) * 2};
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(D / 64),
+                             1u};
+  const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = g_encode(
+      tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+      const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B,
+      D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PDA_OK : PDA_ERR_INVALID_ARG;
+}
+
 template <int D, bool kBf16>
 pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaStream_t stream) {
   static std::atomic<bool> raised[64];
@@ -905,7 +1033,7 @@ pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaSt
   const int box = p.block_size < kChunkKeys ? p.block_size : kChunkKeys;
   pda_status st = encode_heads(&tq, p.q, p.T, p.H, D, kBf16, p.G, 128 >> g_shift);
   if (st == PDA_OK) st = encode_heads(&tk, p.k_cache, rows, p.H_kv, D, kBf16, 1, box);
-  if (st == PDA_OK) st = encode_heads(&tv, p.v_cache, rows, p.H_kv, D, kBf16, 1, box);
+  if (st == PDA_OK) st = encode_v(&tv, p.v_cache, rows, p.H_kv, D, kBf16, box);
   if (st != PDA_OK) return st;
   // no more blocks than the host's bound on the units can keep busy
   const long long cap = static_cast<long long>(p.max_blocks) * p.block_size;
