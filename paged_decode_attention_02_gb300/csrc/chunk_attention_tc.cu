@@ -12,6 +12,7 @@
 //   8         plans the block's pieces, publishes them, and loads Q and K with TMA
 //   9         issues the matrix instructions
 //   10        loads V with TMA
+//   11        writes the rows of requests without work
 //   12-15     clean the V tiles at the diagonal and the end (see below)
 // The softmax warps take the registers that the others give back (setmaxnreg).
 // An item of more than 128 rows gives each group 128 rows; both read every K and V tile. An
@@ -37,7 +38,7 @@ namespace pda {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;  // 2 x 128 of each: what 512 x 128 give
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;  // 2 x 128 of each: what 512 x 128 give
 constexpr int kCleaners = 4;
 constexpr int kDescs = 4;
 constexpr int kMinPieceTiles = 6;   // a cut item's pieces are at least this long
@@ -109,81 +110,101 @@ static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "227 KB
 
 // ---------------------------------------------------------------- plan
 // Units of the requests [0, c * per) for every c, built by all threads of the block.
+constexpr int kPlanChunks = 256;
+
+struct Req {
+  int row0;  // first row of q and out
+  ChunkReq r;
+};
+
+struct PlanMemory {
+  long long prefix[kPlanChunks + 1];
+  int3 req[kPlanChunks];  // (row0, n, L) of each request, where there are no more than this
+};
+
 struct Plan {
-  long long* prefix;  // kPlanChunks + 1 entries in shared memory
+  PlanMemory* mem;
   int per, workers;
   long long units;
 };
-constexpr int kPlanChunks = 256;
 
 struct Where {
   int b, kh, i;
   long long start;  // unit
-  ChunkReq r;
+  Req q;
 };
 
 // A request with work to do; n = 0 for one without (empty, padded or in error).
-__device__ __forceinline__ ChunkReq chunk_req(const ChunkParams& p, int b, int lt) {
+__device__ __forceinline__ Req chunk_req(const ChunkParams& p, int b, int lt) {
   const int q0 = p.query_start[b], q1 = p.query_start[b + 1], L = p.context_lens[b];
   const bool ok = q0 >= 0 && q1 <= p.T && q0 < q1 && L >= q1 - q0 && L <= p.max_context_len &&
                   L <= static_cast<long long>(p.max_blocks) * p.block_size;
-  return ChunkReq{ok ? q1 - q0 : 0, ok ? L : 0, lt};
+  return Req{q0, ChunkReq{ok ? q1 - q0 : 0, ok ? L : 0, lt}};
 }
 
 __device__ __forceinline__ Plan make_plan(const ChunkParams& p, int lt, int workers,
-                                          long long* prefix) {
+                                          PlanMemory* mem) {
   Plan pl;
-  pl.prefix = prefix;
+  pl.mem = mem;
   pl.per = (p.B + kPlanChunks - 1) / kPlanChunks;
   const int c = threadIdx.x, lane = c & 31;
   long long x = 0;
   if (c < kPlanChunks)
-    for (int b = c * pl.per; b < min(p.B, (c + 1) * pl.per); ++b)
-      x += chunk_req(p, b, lt).units();
+    for (int b = c * pl.per; b < min(p.B, (c + 1) * pl.per); ++b) {
+      const Req q = chunk_req(p, b, lt);
+      x += q.r.units();
+      if (pl.per == 1) mem->req[b] = make_int3(q.row0, q.r.n, q.r.L);
+    }
   x *= p.H_kv;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(kFullMask, x, o);
     if (lane >= o) x += y;
   }
-  if (c < kPlanChunks) prefix[c + 1] = x;
+  if (c < kPlanChunks) mem->prefix[c + 1] = x;
   __syncthreads();
   long long before = 0;
   if (c < kPlanChunks)
-    for (int w = 0; w < (c >> 5); ++w) before += prefix[32 * w + 32];
+    for (int w = 0; w < (c >> 5); ++w) before += mem->prefix[32 * w + 32];
   __syncthreads();
-  if (c < kPlanChunks) prefix[c + 1] = x + before;
-  if (c == 0) prefix[0] = 0;
+  if (c < kPlanChunks) mem->prefix[c + 1] = x + before;
+  if (c == 0) mem->prefix[0] = 0;
   __syncthreads();
-  pl.units = prefix[kPlanChunks];
+  pl.units = mem->prefix[kPlanChunks];
   pl.workers = chunk_workers(pl.units, workers, kMinWorkerUnits);
   return pl;
 }
 
-// The item that holds unit u < units.
+// The item that holds unit u < units. Valid while the plan's memory is.
 __device__ __forceinline__ Where locate(const ChunkParams& p, const Plan& pl, int lt,
                                         long long u) {
   int lo = 0, hi = kPlanChunks - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (pl.prefix[mid + 1] > u)
+    if (pl.mem->prefix[mid + 1] > u)
       hi = mid;
     else
       lo = mid + 1;
   }
-  long long at = pl.prefix[lo];
+  long long at = pl.mem->prefix[lo];
   int b = lo * pl.per;
-  ChunkReq r = chunk_req(p, b, lt);
-  long long one = r.units();
+  Req q;
+  if (pl.per == 1) {
+    const int3 v = pl.mem->req[b];
+    q = Req{v.x, ChunkReq{v.y, v.z, lt}};
+  } else {
+    q = chunk_req(p, b, lt);
+  }
+  long long one = q.r.units();
   while (at + one * p.H_kv <= u) {
     at += one * p.H_kv;
-    r = chunk_req(p, ++b, lt);
-    one = r.units();
+    q = chunk_req(p, ++b, lt);
+    one = q.r.units();
   }
-  const int kh = static_cast<int>((u - at) / one);
+  const int kh = static_cast<int>(chunk_div(u - at, one));
   at += kh * one;
-  const int i = r.item_of(u - at);
-  return Where{b, kh, i, at + r.units_before(i), r};
+  const int i = q.r.item_of(u - at);
+  return Where{b, kh, i, at + q.r.units_before(i), q};
 }
 
 // The cut before worker c, snapped; *w: the item it falls into (for a cut below `units`).
@@ -192,7 +213,7 @@ __device__ __forceinline__ long long cut_of(const ChunkParams& p, const Plan& pl
   const long long u = chunk_cut(pl.units, pl.workers, c);
   if (u >= pl.units) return pl.units;
   *w = locate(p, pl, lt, u);
-  return chunk_snap(u, w->start, w->r.tiles(w->i), kMinPieceTiles);
+  return chunk_snap(u, w->start, w->q.r.tiles(w->i), kMinPieceTiles);
 }
 
 // ---------------------------------------------------------------- the block's pipeline
@@ -278,6 +299,41 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// Lane q of each quad gives v[c] = its 16 bytes number c and gets v[r] = bytes number q of
+// the quad's lane r.
+__device__ __forceinline__ void quad_transpose(uint4* v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int step = 1; step < 4; step <<= 1) {
+    const bool up = lane & step;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & step) continue;
+      uint4& lo = v[c];
+      uint4& hi = v[c + step];
+      const uint4 give = up ? lo : hi;
+      uint4 take;
+      take.x = __shfl_xor_sync(kFullMask, give.x, step);
+      take.y = __shfl_xor_sync(kFullMask, give.y, step);
+      take.z = __shfl_xor_sync(kFullMask, give.z, step);
+      take.w = __shfl_xor_sync(kFullMask, give.w, step);
+      if (up)
+        lo = take;
+      else
+        hi = take;
+    }
+  }
+}
+
+// A cut item's partial results: per slot (m, l) of 256 rows, then O as [D / 4][256] float4.
+__host__ __device__ constexpr size_t part_floats(int D) { return 256 * (D + 2); }
+__device__ __forceinline__ float2* part_ml(float* partial, int slot, int D) {
+  return reinterpret_cast<float2*>(partial + slot * part_floats(D));
+}
+__device__ __forceinline__ float4* part_o(float* partial, int slot, int D) {
+  return reinterpret_cast<float4*>(partial + slot * part_floats(D) + 512);
+}
+
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
@@ -332,31 +388,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
+  if (tid == 32) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
   if (warp == 9) {
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
   }
-  const Plan pl = make_plan(p, lt, gridDim.x, reinterpret_cast<long long*>(ks));
+  const Plan pl = make_plan(p, lt, gridDim.x, reinterpret_cast<PlanMemory*>(ks));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem;
-
-  // requests without work whose rows are written all the same: padded (zeros) or in error (NaN)
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const int q0 = p.query_start[b], q1 = p.query_start[b + 1], L = p.context_lens[b];
-    if (q0 == q1 && q0 >= 0 && q1 <= p.T) continue;
-    if (q0 < 0 || q1 > p.T || q0 > q1) {
-      if (tid == 0) atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
-      continue;
-    }
-    if (chunk_req(p, b, lt).n > 0) continue;
-    if (L != 0 && tid == 0) atomic_or_error(p.error_word, PDA_DEVERR_CONTEXT_LEN);
-    const uint32_t w = L == 0 ? 0u : 0x7fff7fffu;  // a NaN in either type
-    uint4* rows = reinterpret_cast<uint4*>(p.out) + static_cast<size_t>(q0) * p.H * (D / 8);
-    const long long vecs = static_cast<long long>(q1 - q0) * p.H * (D / 8);
-    for (long long i = tid; i < vecs; i += kThreads) rows[i] = make_uint4(w, w, w, w);
-  }
 
   bool timed_out = false;
   if (warp < 8) {
@@ -400,6 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_ld32(x + 32 * k, tS + 32 * k);
         tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < kChunkKeys; k += 32) tmem_arrived32(x + k);
         if (key0 + kChunkKeys - 1 > first_pos) {
           const int seen = pos - key0;
 #pragma unroll
@@ -424,13 +471,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             l *= c;
             // the product of the step before is complete: its successor's scores are
 #pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
-              float o[32];
-              tmem_ld32(o, tO + k);
+            for (int k = 0; k < D; k += 16) {
+              float o[16];
+              tmem_ld16(o, tO + k);
               tmem_wait_ld();
+              tmem_arrived16(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= c;
-              tmem_st32(tO + k, o);
+              for (int e = 0; e < 16; ++e) o[e] *= c;
+              tmem_st16(tO + k, reinterpret_cast<const uint32_t*>(o));
             }
           }
         }
@@ -500,12 +548,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (d.jb > d.jc)
           for (int k = 0; k < 12; ++k) odd |= d.nonfinite[k >> 2][k & 3] != 0;
         const float inv = dead ? NAN : part >= 0 ? 1.f : p.v_scale / l;
-        const size_t at =
-            (static_cast<size_t>(d.row0 + tok) * p.H + (d.kh << g_shift) + (packed & ((1 << g_shift) - 1))) * D;
-        float* po = partial + (static_cast<size_t>(max(part, 0)) * 256 + packed) * (D + 4);
-        if (write && part >= 0) {
-          po[D] = steps > 0 && top != -INFINITY ? top * sl : -INFINITY;
-          po[D + 1] = dead ? NAN : l;
+        if (part >= 0 && write)
+          part_ml(partial, part, D)[packed] =
+              make_float2(steps > 0 && top != -INFINITY ? top * sl : -INFINITY, dead ? NAN : l);
+        // output rows of the four lanes of this lane's quad (-1: not written)
+        long long at[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row4 = (packed & ~3) + r, tok4 = row4 >> g_shift;
+          at[r] = tok4 < d.tokens
+                      ? (static_cast<long long>(d.row0 + tok4) * p.H + (d.kh << g_shift) +
+                         (row4 & ((1 << g_shift) - 1))) * D + 8 * (lane & 3)
+                      : -1;
         }
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
@@ -513,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (steps > 0) {
             tmem_ld32(o, tO + k);
             tmem_wait_ld();
+            tmem_arrived32(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= c0;
           } else {
@@ -523,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float o1[32];
             tmem_ld32(o1, tO + 128 + k);
             tmem_wait_ld();
+            tmem_arrived32(o1);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], c1, o[e]);
           }
@@ -543,18 +599,29 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (write && part >= 0) {
+          if (part >= 0) {
+            // four columns of a row, rows side by side: a warp writes 512 bytes at a time
+            if (write) {
+              float4* dst = part_o(partial, part, D) + (k / 4) * 256 + packed;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(po + k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          } else if (write) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + k);
+              for (int e = 0; e < 32; e += 4)
+                dst[(e / 4) * 256] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          } else {
+            // a lane holds 64 bytes of its row; exchanged within quads, four lanes store the
+            // 64 bytes of one row together (a row per lane would take four times the passes)
+            uint4 v[4];
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
-              dst[e / 8] = make_uint4(pack2<kBf16>(o[e] * inv, o[e + 1] * inv),
-                                      pack2<kBf16>(o[e + 2] * inv, o[e + 3] * inv),
-                                      pack2<kBf16>(o[e + 4] * inv, o[e + 5] * inv),
-                                      pack2<kBf16>(o[e + 6] * inv, o[e + 7] * inv));
+              v[e / 8] = make_uint4(pack2<kBf16>(o[e] * inv, o[e + 1] * inv),
+                                    pack2<kBf16>(o[e + 2] * inv, o[e + 3] * inv),
+                                    pack2<kBf16>(o[e + 4] * inv, o[e + 5] * inv),
+                                    pack2<kBf16>(o[e + 6] * inv, o[e + 7] * inv));
+            quad_transpose(v);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (at[r] >= 0)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at[r] + k) = v[r];
           }
           __syncwarp();
         }
@@ -571,20 +638,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // ================================================================ plan, load Q and K
     Where w{};
-    Where w_end{};
-    const bool mine = static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0;
     long long u = 0, u_end = 0;
-    if (mine) {
-      u_end = cut_of(p, pl, lt, blockIdx.x + 1, &w_end);
-      u = cut_of(p, pl, lt, blockIdx.x, &w);
-      if (u < u_end && u >= w.start + w.r.tiles(w.i) + 1) w = locate(p, pl, lt, u);
+    if (static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0) {
+      // both ends of the range at once: the odd lanes find the upper one
+      u = cut_of(p, pl, lt, blockIdx.x + (lane & 1), &w);
+      u_end = __shfl_sync(kFullMask, u, 1);
+      u = __shfl_sync(kFullMask, u, 0);
+      w.b = __shfl_sync(kFullMask, w.b, 0);
+      w.kh = __shfl_sync(kFullMask, w.kh, 0);
+      w.i = __shfl_sync(kFullMask, w.i, 0);
+      w.start = __shfl_sync(kFullMask, w.start, 0);
+      w.q.row0 = __shfl_sync(kFullMask, w.q.row0, 0);
+      w.q.r.n = __shfl_sync(kFullMask, w.q.r.n, 0);
+      w.q.r.L = __shfl_sync(kFullMask, w.q.r.L, 0);
+      w.q.r.lt = lt;
+      if (u < u_end && u >= w.start + w.q.r.tiles(w.i) + 1) w = locate(p, pl, lt, u);
     }
     __syncwarp();
     fence_proxy_async_smem();  // the plan's shared memory becomes load stages
     int item = 0;
     int k_at = 0, k_turn = 0;
     while (u < u_end && !timed_out) {
-      const ChunkReq r = w.r;
+      const ChunkReq r = w.q.r;
       const int tiles = r.tiles(w.i);
       const long long end = w.start + tiles + 1;
       const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
@@ -601,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool single = tokens <= half;
       const int kv_end = pos0 + tokens;
       const long long table = static_cast<long long>(w.b) * p.max_blocks;
-      const int row0 = p.query_start[w.b] + tok0;
+      const int row0 = w.q.row0 + tok0;
       if (lane == 0) {
         d.valid = 1;
         d.row0 = row0;
@@ -633,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane < q_tiles * C::kHalves) {
         const int g = lane / C::kHalves, h = lane % C::kHalves;
         tma_box(qs + g * C::kTile + h * C::kHalf, &tm_q, 64 * h, w.kh << g_shift,
-                   row0 + g * half, &ms.q_full);
+                row0 + g * half, &ms.q_full);
       }
       // K: a box of 64 elements of a block's rows (128 at most) for each half of a row
       const int nt = jb - ja;
@@ -672,8 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++w.kh == p.H_kv) {
             w.kh = 0;
             do {
-              w.r = chunk_req(p, ++w.b, lt);
-            } while (w.r.n == 0);
+              w.q = chunk_req(p, ++w.b, lt);
+            } while (w.q.r.n == 0);
           }
         }
       }
@@ -846,6 +921,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (timed_out)
       for (int st = 0; st < 5; ++st)
         for (int turn = 0; turn < 2; ++turn) warp_wait(&ms.v_full[st], turn);
+  } else if (warp == 11) {
+    // ================================================================ rows without work
+    // requests whose rows are written all the same: padded (zeros) or in error (NaN)
+    for (int first = blockIdx.x; first < p.B; first += 32 * gridDim.x) {
+      const int b = first + lane * gridDim.x;
+      int q0 = 0, q1 = 0, L = 0;
+      if (b < p.B) {
+        q0 = p.query_start[b];
+        q1 = p.query_start[b + 1];
+        L = p.context_lens[b];
+        if (q0 < 0 || q1 > p.T || q0 > q1) {
+          atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
+          q0 = q1 = 0;
+        } else if (chunk_req(p, b, lt).r.n > 0) {
+          q0 = q1 = 0;
+        } else if (q0 < q1 && L != 0) {
+          atomic_or_error(p.error_word, PDA_DEVERR_CONTEXT_LEN);
+        }
+      }
+      for (unsigned todo = __ballot_sync(kFullMask, q0 < q1); todo != 0; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1;
+        const int r0 = __shfl_sync(kFullMask, q0, from), r1 = __shfl_sync(kFullMask, q1, from);
+        // 0x7fff is a NaN in either type
+        const uint32_t v = __shfl_sync(kFullMask, L, from) == 0 ? 0u : 0x7fff7fffu;
+        uint4* rows = reinterpret_cast<uint4*>(p.out) + static_cast<size_t>(r0) * p.H * (D / 8);
+        const long long vecs = static_cast<long long>(r1 - r0) * p.H * (D / 8);
+        for (long long i = lane; i < vecs; i += 32) rows[i] = make_uint4(v, v, v, v);
+      }
+    }
   } else if (warp >= 12) {
     // ================================================================ clean V tiles
     const int part = warp - 12;
@@ -918,58 +1022,74 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- merge of cut items
 // Block x handles the item that cut x + 1 falls into, if that is the first cut inside it:
 // piece i of a row holds (m_i, l_i, O_i); with M = max m_i the row is
-// sum O_i 2^(m_i - M) / sum l_i 2^(m_i - M). A warp takes a row at a time.
+// sum O_i 2^(m_i - M) / sum l_i 2^(m_i - M). A lane takes a row, a warp 32 rows and every
+// eighth group of four columns.
 constexpr int kMergeRows = 32;  // rows of a block
 
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(256)
-    chunk_merge_kernel(const ChunkParams p, int g_shift, const float* partial, int grid) {
-  __shared__ long long prefix[kPlanChunks + 1];
+    chunk_merge_kernel(const ChunkParams p, int g_shift, float* partial, int grid) {
+  __shared__ PlanMemory mem;
   const int lt = kItemRowsLog2 - g_shift;
-  const Plan pl = make_plan(p, lt, grid, prefix);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
+  const Plan pl = make_plan(p, lt, grid, &mem);
   const int c = blockIdx.x + 1;
-  if (c >= pl.workers) return;
-  Where w, before;
-  const long long s = cut_of(p, pl, lt, c, &w);
-  const int tiles = w.r.tiles(w.i);
-  const long long end = w.start + tiles + 1;
-  if (s <= w.start || s >= end || cut_of(p, pl, lt, c - 1, &before) > w.start) return;
-  int pieces = 2;  // worker c - 1's, and one for each cut inside the item
-  for (; c + pieces - 1 < pl.workers; ++pieces) {
-    const long long u = chunk_cut(pl.units, pl.workers, c + pieces - 1);
-    if (u >= end || chunk_snap(u, w.start, tiles, kMinPieceTiles) >= end) break;
-  }
-  const int tok0 = w.i << lt, tokens = min(1 << lt, w.r.n - tok0);
-  const int rows = tokens << g_shift;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int V = D / 32;
-  const size_t row0 = static_cast<size_t>(p.query_start[w.b]) + tok0;
-  for (int r = blockIdx.y * kMergeRows + warp; r < min(rows, (static_cast<int>(blockIdx.y) + 1) * kMergeRows); r += 8) {
-    auto piece = [&](int i) {
-      const int slot = i == 0 ? 2 * (c - 1) + 1 : 2 * (c + i - 1);
-      return partial + (static_cast<size_t>(slot) * 256 + r) * (D + 4);
-    };
-    float M = -INFINITY;
-    for (int i = lane; i < pieces; i += 32) M = fmaxf(M, piece(i)[D]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-    float l = 0.f, acc[V] = {};
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-      const float* at = piece(i);
-      const float mi = at[D];
-      const float wgt = mi == -INFINITY ? 0.f : ex2(mi - M);
-      l = fmaf(wgt, at[D + 1], l);
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(wgt, at[lane * V + e], acc[e]);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int pieces = 0, rows = 0;
+  Where w{};
+  if (c < pl.workers) {
+    // the cut and, on the odd lanes, the one before it
+    const long long s = cut_of(p, pl, lt, c - (lane & 1), &w);
+    const int tiles = w.q.r.tiles(w.i);
+    const long long end = w.start + tiles + 1;
+    const long long before = __shfl_sync(kFullMask, s, 1);
+    if (lane == 0 && s > w.start && s < end && before <= w.start) {
+      pieces = 2;  // worker c - 1's, and one for each cut inside the item
+      for (; c + pieces - 1 < pl.workers; ++pieces) {
+        const long long u = chunk_cut(pl.units, pl.workers, c + pieces - 1);
+        if (u >= end || chunk_snap(u, w.start, tiles, kMinPieceTiles) >= end) break;
+      }
+      rows = min(1 << lt, w.q.r.n - (w.i << lt)) << g_shift;
     }
-    const float inv = p.v_scale / l;
-    const size_t at = ((row0 + (r >> g_shift)) * p.H + (w.kh << g_shift) + (r & ((1 << g_shift) - 1))) * D + lane * V;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at);
-#pragma unroll
-    for (int e = 0; e < V; e += 2) out[e / 2] = pack2<kBf16>(acc[e] * inv, acc[e + 1] * inv);
+    pieces = __shfl_sync(kFullMask, pieces, 0);
+    rows = __shfl_sync(kFullMask, rows, 0);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
+  const int r = blockIdx.y * kMergeRows + lane;
+  if (pieces == 0 || blockIdx.y * kMergeRows >= rows) return;
+  const int row0 = __shfl_sync(kFullMask, w.q.row0 + (w.i << lt), 0);
+  const int kh = __shfl_sync(kFullMask, w.kh, 0);
+  if (r >= rows) return;
+  auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c + i - 1); };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) M = fmaxf(M, part_ml(partial, slot(i), D)[r].x);
+  constexpr int V = D / 32;  // groups of four columns of a warp
+  float l = 0.f;
+  float4 acc[V] = {};
+#pragma unroll 2
+  for (int i = 0; i < pieces; ++i) {
+    const float2 ml = part_ml(partial, slot(i), D)[r];
+    if (ml.x == -INFINITY && !isnan(ml.y)) continue;  // the row sees none of the piece's keys
+    const float wgt = ex2(ml.x - M);
+    l = fmaf(wgt, ml.y, l);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float4 o = part_o(partial, slot(i), D)[(warp + 8 * e) * 256 + r];
+      acc[e].x = fmaf(wgt, o.x, acc[e].x);
+      acc[e].y = fmaf(wgt, o.y, acc[e].y);
+      acc[e].z = fmaf(wgt, o.z, acc[e].z);
+      acc[e].w = fmaf(wgt, o.w, acc[e].w);
+    }
+  }
+  const float inv = p.v_scale / l;
+  uint16_t* out = static_cast<uint16_t*>(p.out) +
+                  ((static_cast<size_t>(row0) + (r >> g_shift)) * p.H + (kh << g_shift) +
+                   (r & ((1 << g_shift) - 1))) * D;
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    *reinterpret_cast<uint2*>(out + 4 * (warp + 8 * e)) =
+        make_uint2(pack2<kBf16>(acc[e].x * inv, acc[e].y * inv),
+                   pack2<kBf16>(acc[e].z * inv, acc[e].w * inv));
 }
 
 // ---------------------------------------------------------------- host side
@@ -1056,7 +1176,7 @@ pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaSt
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D, kBf16>, p, g_shift,
-                            static_cast<const float*>(partial), grid) == cudaSuccess
+                            partial, grid) == cudaSuccess
              ? PDA_OK
              : PDA_ERR_CUDA;
 }
@@ -1064,7 +1184,7 @@ pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaSt
 }  // namespace
 
 size_t chunk_tc_workspace(int sms, int D) {
-  return static_cast<size_t>(sms) * 2 * 256 * (D + 4) * sizeof(float);
+  return static_cast<size_t>(sms) * 2 * part_floats(D) * sizeof(float);
 }
 
 pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int dev, int sms,

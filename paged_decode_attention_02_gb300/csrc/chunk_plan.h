@@ -75,15 +75,22 @@ PDA_CHUNK_HD long long chunk_snap(long long u, long long start, int tiles, int l
   return u;
 }
 
+// a / b for 0 <= a, 0 < b; in 32 bits, several times faster, where both fit.
+PDA_CHUNK_HD long long chunk_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
 // First unit of worker c's range, before snapping.
 PDA_CHUNK_HD long long chunk_cut(long long units, int workers, int c) {
-  const long long q = units / workers, r = units % workers;
-  return c * q + c * r / workers;
+  const long long q = chunk_div(units, workers), r = units - q * workers;
+  return c * q + chunk_div(c * r, workers);
 }
 
 // Workers a launch of `units` units uses: no more than leave each `least` of them.
 PDA_CHUNK_HD int chunk_workers(long long units, int workers, int least) {
-  const long long most = (units + least - 1) / least;
+  const long long most = chunk_div(units + least - 1, least);
   return most < 1 ? 1 : most < workers ? static_cast<int>(most) : workers;
 }
 
