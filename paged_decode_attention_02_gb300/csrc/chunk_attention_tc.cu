@@ -783,8 +783,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dq0 = smem_desc_sw128(smem_addr(qs), 16, 1024);
     const int box_rows = min(p.block_size, kChunkKeys);
     const uint64_t dv0 = smem_desc_sw128(smem_addr(vs), box_rows * 128, 1024);
-    // 16 rows further down: in the same box, or in the next one (whose halves are in between)
-    const int box_log2 = 31 - __clz(box_rows);
+    // 16, 32 and 64 rows further down: in the same box, or past the boxes in between
+    auto rows_down = [&](int n) { return static_cast<uint64_t>(n < box_rows ? n * 128 : n * D * 2) >> 4; };
+    const uint64_t v_step1 = rows_down(16), v_step2 = rows_down(32), v_step4 = rows_down(64);
     int k_at = 0, k_turn = 0, v_at = 0, v_turn = 0;  // stage and parity of the next K, V tile
     unsigned p_phase = 0;
     for (int item = 0; !timed_out; ++item) {
@@ -808,8 +809,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       // A tile is used by both groups, the second releasing it, or (single) by one.
       auto qk = [&](int g, int s) {
-        if (!warp_wait(&ms.k_full[k_at], k_turn)) return false;
-        tc_fence_after();
         if (leader) {
           const uint64_t a = dq0 + (single ? 0 : g * (C::kTile >> 4)), b = dk0 + k_at * (C::kTile >> 4);
 #pragma unroll
@@ -821,19 +820,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (single || g == 1) mma_commit(&ms.k_empty[k_at]);
           if (g == last_g && s == steps - 1) mma_commit(&ms.q_empty);
         }
-        __syncwarp();
         if (single || g == 1) {
           if (++k_at == NK) {
             k_at = 0;
             k_turn ^= 1;
           }
         }
-        return true;
       };
-      auto pv = [&](int g, int s, bool last) {
-        if (!warp_wait(&ms.v_full[v_at], v_turn) || !warp_wait(&ms.clean[v_at], v_turn) ||
-            !warp_wait(&ms.p_full[g], (p_phase >> g) & 1))
-          return false;
+      // Group g's P V of step s and its Q K of the next, issued back to back. Their three
+      // barriers are polled at once, a lane each: one wait after the other left the tensor
+      // core idle for a fifth of the time.
+      auto step = [&](int g, int s, int n) {
+        const bool more = s + 1 < n;
+        uint64_t* bar = &ms.p_full[g];
+        uint32_t turn = (p_phase >> g) & 1;
+        if (lane == 1) {
+          bar = &ms.clean[v_at];
+          turn = v_turn;
+        } else if (lane == 2 && more) {
+          bar = &ms.k_full[k_at];
+          turn = k_turn;
+        }
+        if (!warp_wait(bar, turn)) return false;
         p_phase ^= 1u << g;
         tc_fence_after();
         const int left = keys - (single ? 2 * s + g : s) * kChunkKeys;
@@ -843,32 +851,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kChunkKeys / 16; ++k)
             if (16 * k < left)
               mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * k,
-                         b + ((((16 * k) >> box_log2) << box_log2) * (D * 2) + ((16 * k) & (box_rows - 1)) * 128) / 16,
-                         id_pv, s > 0 || k > 0);
+                         b + (k & 1) * v_step1 + (k >> 1 & 1) * v_step2 + (k >> 2) * v_step4, id_pv,
+                         s > 0 || k > 0);
           if (single || g == 1) mma_commit(&ms.v_empty[v_at]);
-          if (last) mma_commit(&ms.o_full[g]);
+          if (!more) mma_commit(&ms.o_full[g]);
         }
-        __syncwarp();
         if (single || g == 1) {
           if (++v_at == NV) {
             v_at = 0;
             v_turn ^= 1;
           }
         }
+        if (more) qk(g, s + 1);
+        __syncwarp();
         return true;
       };
       bool ok = true;
-      if (n0 > 0) ok = qk(0, 0);
-      if (ok && n1 > 0) ok = qk(1, 0);
+      if (n0 > 0) {
+        ok = warp_wait(&ms.k_full[k_at], k_turn);
+        tc_fence_after();
+        if (ok) qk(0, 0);
+      }
+      if (ok && n1 > 0) {
+        ok = warp_wait(&ms.k_full[k_at], k_turn);
+        tc_fence_after();
+        if (ok) qk(1, 0);
+      }
       for (int s = 0; ok && s < steps; ++s) {
-        if (s < n0) {
-          ok = pv(0, s, s + 1 == n0);
-          if (ok && s + 1 < n0) ok = qk(0, s + 1);
-        }
-        if (ok && s < n1) {
-          ok = pv(1, s, s + 1 == n1);
-          if (ok && s + 1 < n1) ok = qk(1, s + 1);
-        }
+        if (s < n0) ok = step(0, s, n0);
+        if (ok && s < n1) ok = step(1, s, n1);
       }
       if (!ok) {
         timed_out = true;
