@@ -104,7 +104,7 @@ void launch_rows(const ChunkParams& p, int D, cudaStream_t stream) {
 }
 
 size_t workspace_for(pda_dtype kv_dtype, int D, int sms) {
-  const size_t n = kv_dtype == PDA_BF16 || kv_dtype == PDA_F16 ? chunk_tc_workspace(sms, D) : 0;
+  const size_t n = kv_dtype != PDA_F32 ? chunk_tc_workspace(sms, D) : 0;
   return n < 256 ? 256 : n;
 }
 
@@ -145,12 +145,8 @@ pda_status launch_chunk(void* out, const void* q, const void* k_cache, const voi
                       v_scale, B,      T,         H,
                       H_kv,    H / H_kv, max_blocks_per_seq, max_context_len,
                       block_size, num_blocks};
-  if (kv_dtype == PDA_BF16 || kv_dtype == PDA_F16)
-    return launch_chunk_tc(p, D, kv_dtype, dev, sms, workspace, stream);
-  if (kv_dtype == PDA_F32)
-    launch_rows<float, float>(p, D, stream);
-  else
-    launch_rows<fp8e4m3, __nv_bfloat16>(p, D, stream);
+  if (kv_dtype != PDA_F32) return launch_chunk_tc(p, D, kv_dtype, dev, sms, workspace, stream);
+  launch_rows<float, float>(p, D, stream);
   return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }
 

@@ -1,4 +1,5 @@
-// chunk_attention_tc.cu -- chunk attention over 16-bit caches on the tcgen05 tensor cores.
+// chunk_attention_tc.cu -- chunk attention over 16-bit and FP8 caches on the tcgen05 tensor
+// cores.
 //
 // Mathematics. With packed rows R = token * G + head (the G query heads of a kv-head share its
 // keys), S = Q K^T per 128 rows x 128 keys, softmax with a running maximum m and sum l,
@@ -13,7 +14,10 @@
 //   9         issues the matrix instructions
 //   10        loads V with TMA
 //   11        writes the rows of requests without work
-//   12-15     clean the V tiles at the diagonal and the end (see below)
+//   12-15     clean the V tiles at the diagonal and the end (see below), or, over an FP8
+//             cache, widen every K and V tile: the TMA brings the codes, these warps write
+//             them as bf16 (exact: an E4M3 code has 4 significant bits) where the products
+//             read them
 // The softmax warps take the registers that the others give back (setmaxnreg).
 // An item of more than 128 rows gives each group 128 rows; both read every K and V tile. An
 // item of fewer gives both groups the same rows and alternate tiles, merged at the end, so
@@ -63,14 +67,15 @@ struct Desc {
   unsigned nonfinite[3][4];  // V rows of tiles jc .. jc + 2 that hold a NaN or infinity
 };
 
-template <int D>
+template <int D, bool kFp8>
 struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kChunkKeys * D * 2;  // bytes of a K, V or Q tile
   static constexpr int kHalf = kChunkKeys * 128;    // of its 64-element half
   // K and V ring apart: every V tile passes through the cleaning warps, K tiles do not
-  static constexpr int kK = D == 128 ? 3 : 5;
-  static constexpr int kV = D == 128 ? 2 : 5;
+  static constexpr int kK = D == 64 ? 5 : kFp8 ? 2 : 3;
+  static constexpr int kV = D == 64 ? 5 : 2;
+  static constexpr int kRaw = kFp8 ? kChunkKeys * D : 0;  // bytes of a tile of codes
 };
 
 // One box of a tensor map into shared memory, completing on `bar`.
@@ -95,6 +100,7 @@ __device__ __forceinline__ void tma_box4(void* dst, const CUtensorMap* tm, int c
 
 struct Misc {
   uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5], clean[5];
+  uint64_t raw_full[2], raw_empty[2];  // codes of a K and of a V tile
   uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], merge_ready, merge_done, done;
   uint64_t desc_full[kDescs], desc_empty[kDescs];
   Desc desc[kDescs];
@@ -102,11 +108,14 @@ struct Misc {
   uint32_t tmem;
 };
 
-template <int D>
+template <int D, bool kFp8>
 constexpr size_t smem_bytes() {
-  return 1024 + static_cast<size_t>(Cfg<D>::kK + Cfg<D>::kV + 2) * Cfg<D>::kTile + sizeof(Misc);
+  using C = Cfg<D, kFp8>;
+  return 1024 + static_cast<size_t>(C::kK + C::kV + 2) * C::kTile + 2 * C::kRaw + sizeof(Misc);
 }
-static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "227 KB a block");
+static_assert(smem_bytes<128, false>() <= 232448 && smem_bytes<64, false>() <= 232448 &&
+                  smem_bytes<128, true>() <= 232448 && smem_bytes<64, true>() <= 232448,
+              "227 KB a block");
 
 // ---------------------------------------------------------------- plan
 // Units of the requests [0, c * per) for every c, built by all threads of the block.
@@ -299,6 +308,60 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Widens this warp's quarter of a tile of E4M3 codes, [128][D] bytes, to bf16 in the products'
+// layout (64-element halves, 128-byte swizzle). Rows from `keys` on become zeros. Where
+// `nonfinite` is given, NaN codes become zeros and their rows' bits are set there.
+template <int D>
+__device__ __forceinline__ void widen(unsigned char* dst, const unsigned char* codes, int part,
+                                      int keys, unsigned* nonfinite) {
+  constexpr int kLanes = D / 16;  // lanes of a row, 16 codes each
+  const int lane = threadIdx.x & 31, c = 2 * (lane % kLanes);
+#pragma unroll 2
+  for (int i = 0; i < 32 * kLanes / 32; ++i) {
+    const int r = 32 * part + i * (32 / kLanes) + lane / kLanes;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < keys) v = *reinterpret_cast<const uint4*>(codes + r * D + 8 * c);
+    uint32_t* w = &v.x;
+    if (nonfinite != nullptr) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t hit = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+        w[k] &= ~((hit >> 7) * 0xffu);
+        any |= hit;
+      }
+      if (any != 0) atomicOr(&nonfinite[r >> 5], 1u << (r & 31));
+    }
+    uint4 o[2];
+    uint32_t* u = &o[0].x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f[4];
+      e4m3x4_to_f32(w[k], f);
+      u[2 * k] = pack2<true>(f[0], f[1]);
+      u[2 * k + 1] = pack2<true>(f[2], f[3]);
+    }
+    // lanes of the second half take their pieces the other way round: no bank conflicts
+    const bool swap = c >= 8;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int piece = c + (swap ? 1 - k : k);
+      *reinterpret_cast<uint4*>(dst + (piece >> 3) * (kChunkKeys * 128) + r * 128 +
+                                (((piece & 7) ^ (r & 7)) << 4)) = swap == (k == 0) ? o[1] : o[0];
+    }
+  }
+}
+
 // Lane q of each quad gives v[c] = its 16 bytes number c and gets v[r] = bytes number q of
 // the quad's lane r.
 __device__ __forceinline__ void quad_transpose(uint4* v) {
@@ -334,23 +397,14 @@ __device__ __forceinline__ float4* part_o(float* partial, int slot, int D) {
   return reinterpret_cast<float4*>(partial + slot * part_floats(D) + 512);
 }
 
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if (kBf16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const ChunkParams p, int g_shift,
                     float* partial) {
-  using C = Cfg<D>;
+  static_assert(kBf16 || !kFp8, "codes are widened to bf16");
+  using C = Cfg<D, kFp8>;
   constexpr int NK = C::kK, NV = C::kV;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -358,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* ks = smem;
   unsigned char* vs = ks + NK * C::kTile;
   unsigned char* qs = vs + NV * C::kTile;
-  Misc& ms = *reinterpret_cast<Misc*>(qs + 2 * C::kTile);
+  unsigned char* raw = qs + 2 * C::kTile;  // codes: a K tile, then a V tile
+  Misc& ms = *reinterpret_cast<Misc*>(raw + 2 * C::kRaw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int lt = kItemRowsLog2 - g_shift;
 
@@ -366,11 +421,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int i = 0; i < 5; ++i) {
-      mbar_init(&ms.k_full[i], 1);
+      mbar_init(&ms.k_full[i], kFp8 ? kCleaners : 1);
       mbar_init(&ms.k_empty[i], 1);
       mbar_init(&ms.v_full[i], 1);
       mbar_init(&ms.v_empty[i], 1);
       mbar_init(&ms.clean[i], kCleaners);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.raw_full[i], 1);
+      mbar_init(&ms.raw_empty[i], kCleaners);
     }
     mbar_init(&ms.q_full, 1);
     mbar_init(&ms.q_empty, 1);
@@ -588,13 +647,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int key = d.jc * kChunkKeys + y;
               const int id = p.block_tables[d.table + key / p.block_size];
               if (id < 0 || id >= p.num_blocks) continue;
-              const uint16_t* v =
-                  static_cast<const uint16_t*>(p.v_cache) +
+              const size_t first =
                   ((static_cast<size_t>(id) * p.block_size + key % p.block_size) * p.H_kv + d.kh) * D + k;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
-                const float f = kBf16 ? __uint_as_float(static_cast<uint32_t>(v[e]) << 16)
-                                      : __half2float(__ushort_as_half(v[e]));
+                float f;
+                if (kFp8) {
+                  f = e4m3_to_f32(static_cast<const uint8_t*>(p.v_cache)[first + e]);
+                } else {
+                  const uint16_t u = static_cast<const uint16_t*>(p.v_cache)[first + e];
+                  f = kBf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16)
+                            : __half2float(__ushort_as_half(u));
+                }
                 if (!isfinite(f) && key <= pos) o[e] += f;
               }
             }
@@ -710,27 +774,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_box(qs + g * C::kTile + h * C::kHalf, &tm_q, 64 * h, w.kh << g_shift,
                 row0 + g * half, &ms.q_full);
       }
-      // K: a box of 64 elements of a block's rows (128 at most) for each half of a row
+      // K: a box of a block's rows (128 at most), for each 64-element half of a row, or of codes
       const int nt = jb - ja;
       const int box_rows = min(p.block_size, kChunkKeys);
       BlockIds ids;
       ids.start(p, d);
       for (int t = 0; t < nt; ++t) {
         ids.advance(t, &d.bad_from, p.error_word);
-        if (!warp_wait(&ms.k_empty[k_at], k_turn ^ 1)) {
+        uint64_t* full = kFp8 ? &ms.raw_full[0] : &ms.k_full[k_at];
+        if (!warp_wait(kFp8 ? &ms.raw_empty[0] : &ms.k_empty[k_at], k_turn ^ 1)) {
           timed_out = true;
           break;
         }
         const int boxes = min(ids.nbt, (kv_end - (ja + t) * kChunkKeys + box_rows - 1) / box_rows);
         if (lane == 0)
-          mbar_arrive_expect_tx(&ms.k_full[k_at], boxes * C::kHalves * box_rows * 128);
+          mbar_arrive_expect_tx(full, boxes * box_rows * (kFp8 ? D : 2 * D));
         __syncwarp();
-        const int blk = lane / C::kHalves, h = lane % C::kHalves;
+        constexpr int kParts = kFp8 ? 1 : C::kHalves;
+        const int blk = lane / kParts, h = lane % kParts;
         const int row = ids.row(t, blk);
         if (blk < boxes)
-          tma_box(ks + k_at * C::kTile + h * C::kHalf + blk * box_rows * 128, &tm_k, 64 * h, w.kh,
-                  row, &ms.k_full[k_at]);
-        if (++k_at == NK) {
+          tma_box(kFp8 ? raw + blk * box_rows * D
+                       : ks + k_at * C::kTile + h * C::kHalf + blk * box_rows * 128,
+                  &tm_k, 64 * h, w.kh, row, full);
+        if (++k_at == (kFp8 ? 1 : NK)) {
           k_at = 0;
           k_turn ^= 1;
         }
@@ -766,8 +833,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (timed_out) {
       // copies in flight land before the block may leave
-      for (int st = 0; st < 5; ++st)
-        for (int turn = 0; turn < 2; ++turn) warp_wait(&ms.k_full[st], turn);
+      for (int st = 0; st < (kFp8 ? 1 : 5); ++st)
+        for (int turn = 0; turn < 2; ++turn)
+          warp_wait(kFp8 ? &ms.raw_full[0] : &ms.k_full[st], turn);
       warp_wait(&ms.q_full, 0);
       warp_wait(&ms.q_full, 1);
     }
@@ -781,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t id_pv = mma_idesc(kBf16, D, false, true);
     const uint64_t dk0 = smem_desc_sw128(smem_addr(ks), 16, 1024);
     const uint64_t dq0 = smem_desc_sw128(smem_addr(qs), 16, 1024);
-    const int box_rows = min(p.block_size, kChunkKeys);
+    const int box_rows = kFp8 ? kChunkKeys : min(p.block_size, kChunkKeys);
     const uint64_t dv0 = smem_desc_sw128(smem_addr(vs), box_rows * 128, 1024);
     // 16, 32 and 64 rows further down: in the same box, or past the boxes in between
     auto rows_down = [&](int n) { return static_cast<uint64_t>(n < box_rows ? n * 128 : n * D * 2) >> 4; };
@@ -909,19 +977,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       ids.start(p, d);
       for (int t = 0; t < ids.nt; ++t) {
         ids.advance(t, nullptr, nullptr);
-        if (!warp_wait(&ms.v_empty[v_at], v_turn ^ 1)) {
+        uint64_t* full = kFp8 ? &ms.raw_full[1] : &ms.v_full[v_at];
+        if (!warp_wait(kFp8 ? &ms.raw_empty[1] : &ms.v_empty[v_at], v_turn ^ 1)) {
           timed_out = true;
           break;
         }
         const int boxes = min(ids.nbt, (ids.end - (ids.ja + t) * kChunkKeys + box_rows - 1) / box_rows);
-        if (lane == 0)
-          mbar_arrive_expect_tx(&ms.v_full[v_at], boxes * box_rows * D * 2);
+        if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_rows * (kFp8 ? D : 2 * D));
         __syncwarp();
         const int row = ids.row(t, lane);
-        if (lane < boxes)
-          tma_box4(vs + v_at * C::kTile + lane * box_rows * D * 2, &tm_v, 0, row, 0, kh,
-                   &ms.v_full[v_at]);
-        if (++v_at == NV) {
+        if (lane < boxes) {
+          if (kFp8)
+            tma_box(raw + C::kRaw + lane * box_rows * D, &tm_v, 0, kh, row, full);
+          else
+            tma_box4(vs + v_at * C::kTile + lane * box_rows * D * 2, &tm_v, 0, row, 0, kh, full);
+        }
+        if (++v_at == (kFp8 ? 1 : NV)) {
           v_at = 0;
           v_turn ^= 1;
         }
@@ -930,8 +1001,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
     }
     if (timed_out)
-      for (int st = 0; st < 5; ++st)
-        for (int turn = 0; turn < 2; ++turn) warp_wait(&ms.v_full[st], turn);
+      for (int st = 0; st < (kFp8 ? 1 : 5); ++st)
+        for (int turn = 0; turn < 2; ++turn)
+          warp_wait(kFp8 ? &ms.raw_full[1] : &ms.v_full[st], turn);
   } else if (warp == 11) {
     // ================================================================ rows without work
     // requests whose rows are written all the same: padded (zeros) or in error (NaN)
@@ -978,6 +1050,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < nt; ++t) {
         const unsigned at = loads + t;
         const int st = at % NV;
+        if (kFp8) {
+          const int keys = min(kChunkKeys, kv_end - (ja + t) * kChunkKeys);
+          const int kst = at % NK;
+          if (!warp_wait(&ms.raw_full[0], at & 1) || !warp_wait(&ms.k_empty[kst], ((at / NK) & 1) ^ 1)) {
+            timed_out = true;
+            break;
+          }
+          widen<D>(ks + kst * C::kTile, raw, part, keys, nullptr);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ms.k_full[kst]);
+            mbar_arrive(&ms.raw_empty[0]);
+          }
+          if (!warp_wait(&ms.raw_full[1], at & 1) || !warp_wait(&ms.v_empty[st], ((at / NV) & 1) ^ 1)) {
+            timed_out = true;
+            break;
+          }
+          widen<D>(vs + st * C::kTile, raw + C::kRaw, part, keys,
+                   ja + t < jc ? nullptr : d.nonfinite[ja + t - jc]);
+          fence_proxy_async_smem();
+          __threadfence_block();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ms.clean[st]);
+            mbar_arrive(&ms.raw_empty[1]);
+          }
+          continue;
+        }
         if (!warp_wait(&ms.v_full[st], (at / NV) & 1)) {
           timed_out = true;
           break;
@@ -1107,22 +1208,29 @@ __global__ void __launch_bounds__(256)
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-// A map over 16-bit rows [rows, heads, D] whose boxes are 64 elements of `box_heads` heads of
-// `box_rows` rows, written with the 128-byte swizzle.
+// A map over rows [rows, heads, D] whose boxes are `box_rows` rows of `box_heads` heads: of
+// 64 16-bit elements, written with the 128-byte swizzle, or of whole rows of codes.
 pda_status encode_heads(CUtensorMap* tm, const void* base, long long rows, int heads, int D,
-                        bool bf16, int box_heads, int box_rows) {
+                        pda_dtype type, int box_heads, int box_rows) {
+  const bool codes = type == PDA_FP8_E4M3;
+  const cuuint64_t e = dtype_bytes(type);
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2,
-                                 static_cast<cuuint64_t>(heads) * D * 2};
-  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads),
+  const cuuint64_t strides[2] = {D * e, heads * D * e};
+  const cuuint32_t box[3] = {codes ? static_cast<cuuint32_t>(D) : 64u,
+                             static_cast<cuuint32_t>(box_heads),
                              static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t one[3] = {1u, 1u, 1u};
   const CUresult r = g_encode(
-      tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-      const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-      CU_TENSOR_MAP_SWIZZLE_128B,
-      D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+      tm,
+      codes              ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+      : type == PDA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+      3, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+      D * e >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+      : D * e >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                     : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PDA_OK : PDA_ERR_INVALID_ARG;
 }
@@ -1147,13 +1255,14 @@ pda_status encode_v(CUtensorMap* tm, const void* base, long long rows, int heads
   return r == CUDA_SUCCESS ? PDA_OK : PDA_ERR_INVALID_ARG;
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kFp8>
 pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaStream_t stream) {
+  constexpr size_t smem = smem_bytes<D, kFp8>();
   static std::atomic<bool> raised[64];
   if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(chunk_tc_kernel<D, kBf16>,
+    if (cudaFuncSetAttribute(chunk_tc_kernel<D, kBf16, kFp8>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem_bytes<D>())) != cudaSuccess)
+                             static_cast<int>(smem)) != cudaSuccess)
       return PDA_ERR_CUDA;
     if (dev < 64) raised[dev].store(true, std::memory_order_release);
   }
@@ -1162,9 +1271,12 @@ pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaSt
   CUtensorMap tq, tk, tv;
   const long long rows = static_cast<long long>(p.num_blocks) * p.block_size;
   const int box = p.block_size < kChunkKeys ? p.block_size : kChunkKeys;
-  pda_status st = encode_heads(&tq, p.q, p.T, p.H, D, kBf16, p.G, 128 >> g_shift);
-  if (st == PDA_OK) st = encode_heads(&tk, p.k_cache, rows, p.H_kv, D, kBf16, 1, box);
-  if (st == PDA_OK) st = encode_v(&tv, p.v_cache, rows, p.H_kv, D, kBf16, box);
+  const pda_dtype q_type = kBf16 ? PDA_BF16 : PDA_F16, kv_type = kFp8 ? PDA_FP8_E4M3 : q_type;
+  pda_status st = encode_heads(&tq, p.q, p.T, p.H, D, q_type, p.G, 128 >> g_shift);
+  if (st == PDA_OK) st = encode_heads(&tk, p.k_cache, rows, p.H_kv, D, kv_type, 1, box);
+  if (st == PDA_OK)
+    st = kFp8 ? encode_heads(&tv, p.v_cache, rows, p.H_kv, D, kv_type, 1, box)
+              : encode_v(&tv, p.v_cache, rows, p.H_kv, D, kBf16, box);
   if (st != PDA_OK) return st;
   // no more blocks than the host's bound on the units can keep busy
   const long long cap = static_cast<long long>(p.max_blocks) * p.block_size;
@@ -1173,8 +1285,8 @@ pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaSt
   const int lt = kItemRowsLog2 - g_shift;
   const long long items = ((static_cast<long long>(p.T) >> lt) + p.B) * p.H_kv;
   const int grid = chunk_workers(items * (tiles + 1), sms, kMinWorkerUnits);
-  chunk_tc_kernel<D, kBf16><<<grid, kThreads, smem_bytes<D>(), stream>>>(tq, tk, tv, p, g_shift,
-                                                                         partial);
+  chunk_tc_kernel<D, kBf16, kFp8><<<grid, kThreads, smem, stream>>>(tq, tk, tv, p, g_shift,
+                                                                    partial);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
   if (grid == 1 || tiles < 2 * kMinPieceTiles) return PDA_OK;  // no item is cut
   cudaLaunchAttribute attr;
@@ -1210,11 +1322,15 @@ pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int 
   });
   if (g_encode == nullptr) return PDA_ERR_CUDA;
   float* partial = static_cast<float*>(workspace);
+  const bool wide = D == 128;
   if (kv_dtype == PDA_BF16)
-    return D == 128 ? launch<128, true>(p, dev, sms, partial, stream)
-                    : launch<64, true>(p, dev, sms, partial, stream);
-  return D == 128 ? launch<128, false>(p, dev, sms, partial, stream)
-                  : launch<64, false>(p, dev, sms, partial, stream);
+    return wide ? launch<128, true, false>(p, dev, sms, partial, stream)
+                : launch<64, true, false>(p, dev, sms, partial, stream);
+  if (kv_dtype == PDA_F16)
+    return wide ? launch<128, false, false>(p, dev, sms, partial, stream)
+                : launch<64, false, false>(p, dev, sms, partial, stream);
+  return wide ? launch<128, true, true>(p, dev, sms, partial, stream)
+              : launch<64, true, true>(p, dev, sms, partial, stream);
 }
 
 }  // namespace pda

@@ -22,7 +22,7 @@ struct ChunkParams {
 // Workspace bytes of the tensor-core kernel on `sms` SMs.
 size_t chunk_tc_workspace(int sms, int D);
 
-// 16-bit caches on the tensor cores.
+// 16-bit and FP8 caches on the tensor cores.
 pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int dev, int sms,
                            void* workspace, cudaStream_t stream);
 
