@@ -53,6 +53,8 @@ def lib_path() -> str:
 def load():
     """Load libpda.so and declare its C signatures. Raises if the library is not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -461,40 +463,44 @@ def kv_unpack_layers(packed, k_caches, v_caches, block_table_row, context_len: i
 
 
 # ---------------------------------------------------------------- a step of new tokens
+# These calls are short on the GPU, so what they cost on the host counts: plain integers go to
+# ctypes, and each tensor is looked at once.
 def _require(ok, what: str):
     if not ok:
         raise ValueError(what)
 
 
-class _on:
-    """Launches on the tensors' own device: checks that all of them (None skipped) live there,
-    makes it current for the call if it is not, and holds the stream to launch on."""
-
-    def __init__(self, stream, *tensors):
-        dev = tensors[0].device
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensors on {t.device} and {dev}: all must share one device")
-        _require(dev.type == "cuda", "tensor must live on a CUDA device")
-        self.device = dev
-        self.stream = torch.cuda.current_stream(dev) if stream is None else stream
-        self.raw = ctypes.c_void_p(self.stream.cuda_stream)
-        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _addr(t, dev: int, name: str, dtype=None, shape=None):
+    """The address of a dense tensor on device ``dev`` (None: NULL), its type and shape
+    checked where given."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}; all tensors must live on one CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if (dtype is not None and t.dtype is not dtype) or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {dtype or t.dtype} of shape {tuple(shape or t.shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _int32(shape, **tensors):
-    for name, t in tensors.items():
-        _require(t.dtype == torch.int32 and t.shape == shape,
-                 f"{name} must be int32 of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+def _cuda_index(t) -> int:
+    dev = t.get_device()
+    _require(dev >= 0, "tensors must live on a CUDA device")
+    return dev
+
+
+def _call(fn, what: str, dev: int, stream, *args):
+    """``fn(*args, stream)`` on device ``dev``, on ``stream`` or the device's current one."""
+    raw = (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != PDA_OK:
+        raise PdaError(status, what)
 
 
 def kv_assign_blocks(block_tables, blocks_held, free_list, free_count, context_lens,
@@ -506,21 +512,19 @@ def kv_assign_blocks(block_tables, blocks_held, free_list, free_count, context_l
     _require(block_tables.dim() == 2 and free_list.dim() == 1,
              "block_tables must be [B, max_blocks] and free_list [num_blocks]")
     B, max_blocks = block_tables.shape
-    held_out = blocks_held if blocks_held_out is None else blocks_held_out
-    count_out = free_count if free_count_out is None else free_count_out
-    _int32((B, max_blocks), block_tables=block_tables)
-    _int32((B,), blocks_held=blocks_held, blocks_held_out=held_out, context_lens=context_lens)
-    if shared_blocks is not None:
-        _int32((B,), shared_blocks=shared_blocks)
-    _int32((1,), free_count=free_count, free_count_out=count_out)
-    _int32(free_list.shape, free_list=free_list)
-    with _on(stream, block_tables, blocks_held, held_out, free_list, free_count, count_out,
-             context_lens, shared_blocks, error_word) as on:
-        _check(load().pda_kv_assign_blocks(
-            _ptr(block_tables), _ptr(blocks_held), _ptr(held_out), _ptr(free_list),
-            _ptr(free_count), _ptr(count_out), _ptr(context_lens), _ptr(shared_blocks), B,
-            max_blocks, int(block_size), free_list.shape[0], _ptr(error_word), on.raw),
-            "pda_kv_assign_blocks")
+    dev, i32, b, one = _cuda_index(block_tables), torch.int32, (B,), (1,)
+    held = _addr(blocks_held, dev, "blocks_held", i32, b)
+    count = _addr(free_count, dev, "free_count", i32, one)
+    held_out = held if blocks_held_out is None else _addr(blocks_held_out, dev,
+                                                          "blocks_held_out", i32, b)
+    count_out = count if free_count_out is None else _addr(free_count_out, dev,
+                                                           "free_count_out", i32, one)
+    _call(load().pda_kv_assign_blocks, "pda_kv_assign_blocks", dev, stream,
+          _addr(block_tables, dev, "block_tables", i32), held, held_out,
+          _addr(free_list, dev, "free_list", i32), count, count_out,
+          _addr(context_lens, dev, "context_lens", i32, b),
+          _addr(shared_blocks, dev, "shared_blocks", i32, b), B, max_blocks, int(block_size),
+          free_list.shape[0], _addr(error_word, dev, "error_word"))
     return block_tables
 
 
@@ -532,25 +536,26 @@ def kv_build_slots(slot_mapping, query_start, query_lens, context_lens, block_ta
     _require(block_tables.dim() == 2 and slot_mapping.dim() == 1,
              "block_tables must be [B, max_blocks] and slot_mapping [N]")
     B, max_blocks = block_tables.shape
-    _int32((B, max_blocks), block_tables=block_tables)
-    _int32((B,), query_lens=query_lens, context_lens=context_lens)
-    _int32((B + 1,), query_start=query_start)
-    _int32(slot_mapping.shape, slot_mapping=slot_mapping)
-    with _on(stream, query_start, slot_mapping, query_lens, context_lens, block_tables,
-             error_word) as on:
-        _check(load().pda_kv_build_slots(
-            _ptr(slot_mapping), _ptr(query_start), _ptr(query_lens), _ptr(context_lens),
-            _ptr(block_tables), slot_mapping.shape[0], B, max_blocks, int(block_size),
-            int(num_blocks), _ptr(error_word), on.raw), "pda_kv_build_slots")
+    dev, i32, b = _cuda_index(query_start), torch.int32, (B,)
+    _call(load().pda_kv_build_slots, "pda_kv_build_slots", dev, stream,
+          _addr(slot_mapping, dev, "slot_mapping", i32),
+          _addr(query_start, dev, "query_start", i32, (B + 1,)),
+          _addr(query_lens, dev, "query_lens", i32, b),
+          _addr(context_lens, dev, "context_lens", i32, b),
+          _addr(block_tables, dev, "block_tables", i32), slot_mapping.shape[0], B, max_blocks,
+          int(block_size), int(num_blocks), _addr(error_word, dev, "error_word"))
     return slot_mapping
+
+
+_KV_DTYPE = {torch.bfloat16: PDA_BF16, torch.float32: PDA_F32, torch.float16: PDA_F16,
+             torch.uint8: PDA_FP8_E4M3, torch.float8_e4m3fn: PDA_FP8_E4M3}
 
 
 def chunk_attention_workspace_size(B, T, H, H_kv, D, block_size=16, kv_dtype=torch.bfloat16,
                                    sm_cap=0) -> int:
     n = ctypes.c_size_t(0)
-    dt = {torch.bfloat16: PDA_BF16, torch.float32: PDA_F32, torch.float16: PDA_F16,
-          torch.uint8: PDA_FP8_E4M3, torch.float8_e4m3fn: PDA_FP8_E4M3}[kv_dtype]
-    _check(load().pda_chunk_attention_workspace_size(B, T, H, H_kv, D, block_size, dt, sm_cap,
+    _check(load().pda_chunk_attention_workspace_size(B, T, H, H_kv, D, block_size,
+                                                     _KV_DTYPE[kv_dtype], sm_cap,
                                                      ctypes.byref(n)),
            "pda_chunk_attention_workspace_size")
     return n.value
@@ -572,22 +577,20 @@ def _chunk(fn, what, scales, out, q, k_cache, v_cache, block_tables, context_len
     T, H, D = q.shape
     NB, bs, H_kv, D2 = k_cache.shape
     B, max_blocks = block_tables.shape
-    _require(D == D2 and v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype,
-             "q, k_cache and v_cache must agree in head size, shape and type")
-    _require(out.shape == q.shape and out.dtype == q.dtype, "out must be like q")
-    _int32((B, max_blocks), block_tables=block_tables)
-    _int32((B,), context_lens=context_lens)
-    _int32((B + 1,), query_start=query_start)
-    with _on(stream, q, out, k_cache, v_cache, block_tables, context_lens, query_start,
-             workspace, error_word) as on:
-        if workspace is None:  # from the launching stream's pool: reused there only
-            with torch.cuda.stream(on.stream):
-                workspace = alloc_chunk_workspace(B, T, H, H_kv, D, bs, k_cache.dtype, sm_cap,
-                                                  on.device)
-        _check(fn(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                  max_blocks, _ptr(context_lens), _ptr(query_start), int(max_context_len), B, T,
-                  H, H_kv, D, bs, NB, *scales, *dtypes, int(sm_cap), _ptr(workspace),
-                  workspace.numel() * workspace.element_size(), _ptr(error_word), on.raw), what)
+    _require(D == D2, "q and the caches must agree in head size")
+    dev, i32 = _cuda_index(q), torch.int32
+    if workspace is None:  # from the launching stream's pool: reused there only
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            workspace = alloc_chunk_workspace(B, T, H, H_kv, D, bs, k_cache.dtype, sm_cap,
+                                              q.device)
+    _call(fn, what, dev, stream, _addr(out, dev, "out", q.dtype, q.shape), _addr(q, dev, "q"),
+          _addr(k_cache, dev, "k_cache"),
+          _addr(v_cache, dev, "v_cache", k_cache.dtype, k_cache.shape),
+          _addr(block_tables, dev, "block_tables", i32), max_blocks,
+          _addr(context_lens, dev, "context_lens", i32, (B,)),
+          _addr(query_start, dev, "query_start", i32, (B + 1,)), int(max_context_len), B, T, H,
+          H_kv, D, bs, NB, *scales, *dtypes, int(sm_cap), _addr(workspace, dev, "workspace"),
+          workspace.numel() * workspace.element_size(), _addr(error_word, dev, "error_word"))
     return out
 
 
