@@ -1,84 +1,24 @@
-// chunk_attention.cu -- attention of a chunk of new tokens over the paged cache: every new
-// token of a request attends to the request's whole history up to and including itself.
+// chunk_attention.cu -- the C entry points of chunk attention: attention of a chunk of new
+// tokens over the paged cache, every new token of a request attending to the request's whole
+// history up to and including itself.
 //
 // Row (token i of request b, head h) at position p = L_b - n_b + i, kv-head k = h / G:
 //   s_t = scale q . K_t[k],  out = sum_{t <= p} softmax(s)_t V_t[k].
-// One warp per row: lanes own D / 32 dims, keys stream past one at a time with a running
-// maximum and sum in fp32.
+// Checks the arguments and hands over to the kernel of the cache's type.
 #include <math.h>
 
 #include "chunk_internal.h"
-#include "pda_device.cuh"
+#include "chunk_plan.cuh"
 
 namespace pda {
+
+size_t chunk_workspace(int sms, int D) {
+  return static_cast<size_t>(sms) * 2 * part_floats(D) * sizeof(float);
+}
+
 namespace {
 
 constexpr int kChunkMaxBatch = 8192;
-
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(fp8e4m3 x) { return e4m3_to_f32(x.bits); }
-__device__ __forceinline__ void from_f32(float* p, float x) { *p = x; }
-__device__ __forceinline__ void from_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
-template <typename KV, typename Q, int D>
-__global__ void __launch_bounds__(256) chunk_rows_kernel(const ChunkParams p) {
-  constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  if (w >= static_cast<long long>(p.T) * p.H) return;
-  const int tok = static_cast<int>(w / p.H), h = static_cast<int>(w % p.H), kh = h / p.G;
-  // the request whose rows hold tok: the last b with query_start[b] <= tok
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.query_start[mid] <= tok)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int q0 = p.query_start[lo], q1 = p.query_start[lo + 1];
-  if (q0 < 0 || q1 > p.T || q0 > q1) {
-    if (lane == 0) atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
-    return;
-  }
-  if (tok < q0 || tok >= q1) return;
-  const int L = p.context_lens[lo], n = q1 - q0;
-  const bool bad_len = L < 0 || L > p.max_context_len ||
-                       L > static_cast<long long>(p.max_blocks) * p.block_size ||
-                       (L > 0 && L < n);
-  if (bad_len && lane == 0) atomic_or_error(p.error_word, PDA_DEVERR_CONTEXT_LEN);
-  const size_t row = (static_cast<size_t>(tok) * p.H + h) * D + lane * V;
-  float q[V], o[V], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < V; ++i) {
-    q[i] = to_f32(static_cast<const Q*>(p.q)[row + i]) * p.scale_log2;
-    o[i] = 0.f;
-  }
-  const int keys = bad_len || L == 0 ? 0 : L - n + (tok - q0) + 1;
-  bool bad_block = false;
-  const int32_t* table = p.block_tables + static_cast<size_t>(lo) * p.max_blocks;
-  for (int t = 0; t < keys; ++t) {
-    const int id = table[t / p.block_size];
-    if (id < 0 || id >= p.num_blocks) {
-      bad_block = true;
-      break;
-    }
-    const size_t at =
-        ((static_cast<size_t>(id) * p.block_size + t % p.block_size) * p.H_kv + kh) * D + lane * V;
-    float s = 0.f;
-    for (int i = 0; i < V; ++i) s = fmaf(q[i], to_f32(static_cast<const KV*>(p.k_cache)[at + i]), s);
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(kFullMask, s, x);
-    const float m1 = fmaxf(m, s);
-    const float c = ex2(m - m1), e = ex2(s - m1);
-    l = l * c + e;
-    for (int i = 0; i < V; ++i)
-      o[i] = fmaf(e, to_f32(static_cast<const KV*>(p.v_cache)[at + i]), o[i] * c);
-    m = m1;
-  }
-  if (bad_block && lane == 0) atomic_or_error(p.error_word, PDA_DEVERR_BLOCK_ID);
-  const float inv = bad_len || bad_block ? NAN : keys == 0 ? 0.f : p.v_scale / l;
-  for (int i = 0; i < V; ++i) from_f32(static_cast<Q*>(p.out) + row + i, o[i] * inv);
-}
 
 bool chunk_block_size_ok(int bs) { return bs >= 16 && bs <= 256 && (bs & (bs - 1)) == 0; }
 bool chunk_group_ok(int G) { return G == 1 || G == 2 || G == 4 || G == 8; }
@@ -92,20 +32,6 @@ pda_status check_shape(int B, int T, int H, int H_kv, int D, int block_size, pda
       B > kChunkMaxBatch || static_cast<long long>(T) * H >= (1ll << 31))
     return PDA_ERR_UNSUPPORTED;
   return PDA_OK;
-}
-
-template <typename KV, typename Q>
-void launch_rows(const ChunkParams& p, int D, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.T) * p.H + 7) / 8);
-  if (D == 128)
-    chunk_rows_kernel<KV, Q, 128><<<grid, 256, 0, stream>>>(p);
-  else
-    chunk_rows_kernel<KV, Q, 64><<<grid, 256, 0, stream>>>(p);
-}
-
-size_t workspace_for(pda_dtype kv_dtype, int D, int sms) {
-  const size_t n = kv_dtype != PDA_F32 ? chunk_tc_workspace(sms, D) : 0;
-  return n < 256 ? 256 : n;
 }
 
 // The launch behind both public entry points.
@@ -138,16 +64,15 @@ pda_status launch_chunk(void* out, const void* q, const void* k_cache, const voi
   const pda_status dst = current_device_sms(&dev, &sms);
   if (dst != PDA_OK) return dst;
   if (sm_cap > 0 && sm_cap < sms) sms = sm_cap;
-  if (workspace_bytes < workspace_for(kv_dtype, D, sms)) return PDA_ERR_WORKSPACE;
+  if (workspace_bytes < chunk_workspace(sms, D)) return PDA_ERR_WORKSPACE;
   const ChunkParams p{out,     q,      k_cache,   v_cache,
                       block_tables, context_lens, query_start, error_word,
                       scale * k_scale * 1.4426950408889634f,
                       v_scale, B,      T,         H,
                       H_kv,    H / H_kv, max_blocks_per_seq, max_context_len,
                       block_size, num_blocks};
-  if (kv_dtype != PDA_F32) return launch_chunk_tc(p, D, kv_dtype, dev, sms, workspace, stream);
-  launch_rows<float, float>(p, D, stream);
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  return kv_dtype == PDA_F32 ? launch_chunk_f32(p, D, dev, sms, workspace, stream)
+                             : launch_chunk_tc(p, D, kv_dtype, dev, sms, workspace, stream);
 }
 
 }  // namespace
@@ -164,7 +89,7 @@ extern "C" pda_status pda_chunk_attention_workspace_size(int B, int T, int H, in
   int dev, sms;
   const pda_status dst = current_device_sms(&dev, &sms);
   if (dst != PDA_OK) return dst;
-  *bytes = workspace_for(kv_dtype, D, sm_cap > 0 && sm_cap < sms ? sm_cap : sms);
+  *bytes = chunk_workspace(sm_cap > 0 && sm_cap < sms ? sm_cap : sms, D);
   return PDA_OK;
 }
 

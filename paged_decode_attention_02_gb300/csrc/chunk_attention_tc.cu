@@ -33,9 +33,9 @@
 
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
-#include "chunk_internal.h"
-#include "chunk_plan.h"
+#include "chunk_plan.cuh"
 #include "tcgen05.cuh"
 
 namespace pda {
@@ -45,8 +45,7 @@ constexpr int kThreads = 512;
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;  // 2 x 128 of each: what 512 x 128 give
 constexpr int kCleaners = 4;
 constexpr int kDescs = 4;
-constexpr int kMinPieceTiles = 6;   // a cut item's pieces are at least this long
-constexpr int kMinWorkerUnits = 4;  // a worker's range is at least this long
+using CutsOf = Cuts<8, 6, 4>;  // 256-row items
 constexpr float kRaise = 8.f;       // the reference maximum moves by at least 2^8
 
 // One piece of work: key tiles [ja, jb) of an item.
@@ -116,114 +115,6 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes<128, false>() <= 232448 && smem_bytes<64, false>() <= 232448 &&
                   smem_bytes<128, true>() <= 232448 && smem_bytes<64, true>() <= 232448,
               "227 KB a block");
-
-// ---------------------------------------------------------------- plan
-// Units of the requests [0, c * per) for every c, built by all threads of the block.
-constexpr int kPlanChunks = 256;
-
-struct Req {
-  int row0;  // first row of q and out
-  ChunkReq r;
-};
-
-struct PlanMemory {
-  long long prefix[kPlanChunks + 1];
-  int3 req[kPlanChunks];  // (row0, n, L) of each request, where there are no more than this
-};
-
-struct Plan {
-  PlanMemory* mem;
-  int per, workers;
-  long long units;
-};
-
-struct Where {
-  int b, kh, i;
-  long long start;  // unit
-  Req q;
-};
-
-// A request with work to do; n = 0 for one without (empty, padded or in error).
-__device__ __forceinline__ Req chunk_req(const ChunkParams& p, int b, int lt) {
-  const int q0 = p.query_start[b], q1 = p.query_start[b + 1], L = p.context_lens[b];
-  const bool ok = q0 >= 0 && q1 <= p.T && q0 < q1 && L >= q1 - q0 && L <= p.max_context_len &&
-                  L <= static_cast<long long>(p.max_blocks) * p.block_size;
-  return Req{q0, ChunkReq{ok ? q1 - q0 : 0, ok ? L : 0, lt}};
-}
-
-__device__ __forceinline__ Plan make_plan(const ChunkParams& p, int lt, int workers,
-                                          PlanMemory* mem) {
-  Plan pl;
-  pl.mem = mem;
-  pl.per = (p.B + kPlanChunks - 1) / kPlanChunks;
-  const int c = threadIdx.x, lane = c & 31;
-  long long x = 0;
-  if (c < kPlanChunks)
-    for (int b = c * pl.per; b < min(p.B, (c + 1) * pl.per); ++b) {
-      const Req q = chunk_req(p, b, lt);
-      x += q.r.units();
-      if (pl.per == 1) mem->req[b] = make_int3(q.row0, q.r.n, q.r.L);
-    }
-  x *= p.H_kv;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(kFullMask, x, o);
-    if (lane >= o) x += y;
-  }
-  if (c < kPlanChunks) mem->prefix[c + 1] = x;
-  __syncthreads();
-  long long before = 0;
-  if (c < kPlanChunks)
-    for (int w = 0; w < (c >> 5); ++w) before += mem->prefix[32 * w + 32];
-  __syncthreads();
-  if (c < kPlanChunks) mem->prefix[c + 1] = x + before;
-  if (c == 0) mem->prefix[0] = 0;
-  __syncthreads();
-  pl.units = mem->prefix[kPlanChunks];
-  pl.workers = chunk_workers(pl.units, workers, kMinWorkerUnits);
-  return pl;
-}
-
-// The item that holds unit u < units. Valid while the plan's memory is.
-__device__ __forceinline__ Where locate(const ChunkParams& p, const Plan& pl, int lt,
-                                        long long u) {
-  int lo = 0, hi = kPlanChunks - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pl.mem->prefix[mid + 1] > u)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  long long at = pl.mem->prefix[lo];
-  int b = lo * pl.per;
-  Req q;
-  if (pl.per == 1) {
-    const int3 v = pl.mem->req[b];
-    q = Req{v.x, ChunkReq{v.y, v.z, lt}};
-  } else {
-    q = chunk_req(p, b, lt);
-  }
-  long long one = q.r.units();
-  while (at + one * p.H_kv <= u) {
-    at += one * p.H_kv;
-    q = chunk_req(p, ++b, lt);
-    one = q.r.units();
-  }
-  const int kh = static_cast<int>(chunk_div(u - at, one));
-  at += kh * one;
-  const int i = q.r.item_of(u - at);
-  return Where{b, kh, i, at + q.r.units_before(i), q};
-}
-
-// The cut before worker c, snapped; *w: the item it falls into (for a cut below `units`).
-__device__ __forceinline__ long long cut_of(const ChunkParams& p, const Plan& pl, int lt, int c,
-                                            Where* w) {
-  const long long u = chunk_cut(pl.units, pl.workers, c);
-  if (u >= pl.units) return pl.units;
-  *w = locate(p, pl, lt, u);
-  return chunk_snap(u, w->start, w->q.r.tiles(w->i), kMinPieceTiles);
-}
 
 // ---------------------------------------------------------------- the block's pipeline
 // A wait of a whole warp: false for all lanes if it ran out for any.
@@ -308,16 +199,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if (kBf16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // Widens this warp's quarter of a tile of E4M3 codes, [128][D] bytes, to bf16 in the products'
 // layout (64-element halves, 128-byte swizzle). Rows from `keys` on become zeros. Where
 // `nonfinite` is given, NaN codes become zeros and their rows' bits are set there.
@@ -388,15 +269,6 @@ __device__ __forceinline__ void quad_transpose(uint4* v) {
   }
 }
 
-// A cut item's partial results: per slot (m, l) of 256 rows, then O as [D / 4][256] float4.
-__host__ __device__ constexpr size_t part_floats(int D) { return 256 * (D + 2); }
-__device__ __forceinline__ float2* part_ml(float* partial, int slot, int D) {
-  return reinterpret_cast<float2*>(partial + slot * part_floats(D));
-}
-__device__ __forceinline__ float4* part_o(float* partial, int slot, int D) {
-  return reinterpret_cast<float4*>(partial + slot * part_floats(D) + 512);
-}
-
 template <int D, bool kBf16, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -415,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* raw = qs + 2 * C::kTile;  // codes: a K tile, then a V tile
   Misc& ms = *reinterpret_cast<Misc*>(raw + 2 * C::kRaw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int lt = kItemRowsLog2 - g_shift;
+  const int lt = CutsOf::kRowsLog2 - g_shift;
 
   // the merge kernel may start its own prologue as soon as blocks leave
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -456,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&ms.tmem, 512);
     tmem_relinquish();
   }
-  const Plan pl = make_plan(p, lt, gridDim.x, reinterpret_cast<PlanMemory*>(ks));
+  const Plan pl = make_plan<CutsOf>(p, lt, gridDim.x, reinterpret_cast<PlanMemory*>(ks));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -705,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long u = 0, u_end = 0;
     if (static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0) {
       // both ends of the range at once: the odd lanes find the upper one
-      u = cut_of(p, pl, lt, blockIdx.x + (lane & 1), &w);
+      u = cut_of<CutsOf>(p, pl, lt, blockIdx.x + (lane & 1), &w);
       u_end = __shfl_sync(kFullMask, u, 1);
       u = __shfl_sync(kFullMask, u, 0);
       w.b = __shfl_sync(kFullMask, w.b, 0);
@@ -1131,79 +1003,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// ---------------------------------------------------------------- merge of cut items
-// Block x handles the item that cut x + 1 falls into, if that is the first cut inside it:
-// piece i of a row holds (m_i, l_i, O_i); with M = max m_i the row is
-// sum O_i 2^(m_i - M) / sum l_i 2^(m_i - M). A lane takes a row, a warp 32 rows and every
-// eighth group of four columns.
-constexpr int kMergeRows = 32;  // rows of a block
-
-template <int D, bool kBf16>
-__global__ void __launch_bounds__(256)
-    chunk_merge_kernel(const ChunkParams p, int g_shift, float* partial, int grid) {
-  __shared__ PlanMemory mem;
-  const int lt = kItemRowsLog2 - g_shift;
-  const Plan pl = make_plan(p, lt, grid, &mem);
-  const int c = blockIdx.x + 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int pieces = 0, rows = 0;
-  Where w{};
-  if (c < pl.workers) {
-    // the cut and, on the odd lanes, the one before it
-    const long long s = cut_of(p, pl, lt, c - (lane & 1), &w);
-    const int tiles = w.q.r.tiles(w.i);
-    const long long end = w.start + tiles + 1;
-    const long long before = __shfl_sync(kFullMask, s, 1);
-    if (lane == 0 && s > w.start && s < end && before <= w.start) {
-      pieces = 2;  // worker c - 1's, and one for each cut inside the item
-      for (; c + pieces - 1 < pl.workers; ++pieces) {
-        const long long u = chunk_cut(pl.units, pl.workers, c + pieces - 1);
-        if (u >= end || chunk_snap(u, w.start, tiles, kMinPieceTiles) >= end) break;
-      }
-      rows = min(1 << lt, w.q.r.n - (w.i << lt)) << g_shift;
-    }
-    pieces = __shfl_sync(kFullMask, pieces, 0);
-    rows = __shfl_sync(kFullMask, rows, 0);
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
-  const int r = blockIdx.y * kMergeRows + lane;
-  if (pieces == 0 || blockIdx.y * kMergeRows >= rows) return;
-  const int row0 = __shfl_sync(kFullMask, w.q.row0 + (w.i << lt), 0);
-  const int kh = __shfl_sync(kFullMask, w.kh, 0);
-  if (r >= rows) return;
-  auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c + i - 1); };
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i < pieces; ++i) M = fmaxf(M, part_ml(partial, slot(i), D)[r].x);
-  constexpr int V = D / 32;  // groups of four columns of a warp
-  float l = 0.f;
-  float4 acc[V] = {};
-#pragma unroll 2
-  for (int i = 0; i < pieces; ++i) {
-    const float2 ml = part_ml(partial, slot(i), D)[r];
-    if (ml.x == -INFINITY && !isnan(ml.y)) continue;  // the row sees none of the piece's keys
-    const float wgt = ex2(ml.x - M);
-    l = fmaf(wgt, ml.y, l);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float4 o = part_o(partial, slot(i), D)[(warp + 8 * e) * 256 + r];
-      acc[e].x = fmaf(wgt, o.x, acc[e].x);
-      acc[e].y = fmaf(wgt, o.y, acc[e].y);
-      acc[e].z = fmaf(wgt, o.z, acc[e].z);
-      acc[e].w = fmaf(wgt, o.w, acc[e].w);
-    }
-  }
-  const float inv = p.v_scale / l;
-  uint16_t* out = static_cast<uint16_t*>(p.out) +
-                  ((static_cast<size_t>(row0) + (r >> g_shift)) * p.H + (kh << g_shift) +
-                   (r & ((1 << g_shift) - 1))) * D;
-#pragma unroll
-  for (int e = 0; e < V; ++e)
-    *reinterpret_cast<uint2*>(out + 4 * (warp + 8 * e)) =
-        make_uint2(pack2<kBf16>(acc[e].x * inv, acc[e].y * inv),
-                   pack2<kBf16>(acc[e].z * inv, acc[e].w * inv));
-}
-
 // ---------------------------------------------------------------- host side
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
@@ -1278,37 +1077,15 @@ pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaSt
     st = kFp8 ? encode_heads(&tv, p.v_cache, rows, p.H_kv, D, kv_type, 1, box)
               : encode_v(&tv, p.v_cache, rows, p.H_kv, D, kBf16, box);
   if (st != PDA_OK) return st;
-  // no more blocks than the host's bound on the units can keep busy
-  const long long cap = static_cast<long long>(p.max_blocks) * p.block_size;
-  const long long keys = p.max_context_len < cap ? p.max_context_len : cap;
-  const int tiles = static_cast<int>((keys + kChunkKeys - 1) / kChunkKeys);
-  const int lt = kItemRowsLog2 - g_shift;
-  const long long items = ((static_cast<long long>(p.T) >> lt) + p.B) * p.H_kv;
-  const int grid = chunk_workers(items * (tiles + 1), sms, kMinWorkerUnits);
+  const int grid = chunk_grid<CutsOf>(p, g_shift, sms);
   chunk_tc_kernel<D, kBf16, kFp8><<<grid, kThreads, smem, stream>>>(tq, tk, tv, p, g_shift,
                                                                     partial);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
-  if (grid == 1 || tiles < 2 * kMinPieceTiles) return PDA_OK;  // no item is cut
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid - 1), 256 / kMergeRows);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D, kBf16>, p, g_shift,
-                            partial, grid) == cudaSuccess
-             ? PDA_OK
-             : PDA_ERR_CUDA;
+  using Out = std::conditional_t<kBf16, __nv_bfloat16, __half>;
+  return launch_merge<D, Out, CutsOf>(p, g_shift, partial, grid, stream);
 }
 
 }  // namespace
-
-size_t chunk_tc_workspace(int sms, int D) {
-  return static_cast<size_t>(sms) * 2 * part_floats(D) * sizeof(float);
-}
 
 pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int dev, int sms,
                            void* workspace, cudaStream_t stream) {

@@ -19,11 +19,14 @@ struct ChunkParams {
   int B, T, H, H_kv, G, max_blocks, max_context_len, block_size, num_blocks;
 };
 
-// Workspace bytes of the tensor-core kernel on `sms` SMs.
-size_t chunk_tc_workspace(int sms, int D);
+// Workspace bytes on `sms` SMs: two cut items' partial results a block.
+size_t chunk_workspace(int sms, int D);
 
-// 16-bit and FP8 caches on the tensor cores.
+// 16-bit and FP8 caches, on the tensor cores.
 pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int dev, int sms,
                            void* workspace, cudaStream_t stream);
+// fp32 caches.
+pda_status launch_chunk_f32(const ChunkParams& p, int D, int dev, int sms, void* workspace,
+                            cudaStream_t stream);
 
 }  // namespace pda

@@ -2,7 +2,7 @@
 // Host and device code both use it (a host test checks its arithmetic against loops).
 //
 // A request's query rows, G heads of a kv-head times its n new tokens, are cut into items of
-// 256 rows (256 / G tokens). An item attends to keys [0, p + 1), p the position of its last
+// 2^lt tokens (256 rows on the tensor cores). An item attends to keys [0, p + 1), p the position of its last
 // token, in tiles of 128 keys, and counts as tiles + 1 units (the one for its own start and
 // end). Units are numbered request after request, kv-head after kv-head, item after item, and
 // each of the launch's workers takes an equal, contiguous range of them, so the split is even
@@ -18,7 +18,6 @@
 namespace pda {
 
 constexpr int kChunkKeys = 128;    // keys of a tile
-constexpr int kItemRowsLog2 = 8;   // rows of an item
 
 struct ChunkReq {
   int n, L;     // new tokens, and all of them; n <= L
