@@ -482,16 +482,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (part >= 0 && write)
           part_ml(partial, part, D)[packed] =
               make_float2(steps > 0 && top != -INFINITY ? top * sl : -INFINITY, dead ? NAN : l);
-        // output rows of the four lanes of this lane's quad (-1: not written)
-        long long at[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row4 = (packed & ~3) + r, tok4 = row4 >> g_shift;
-          at[r] = tok4 < d.tokens
-                      ? (static_cast<long long>(d.row0 + tok4) * p.H + (d.kh << g_shift) +
-                         (row4 & ((1 << g_shift) - 1))) * D + 8 * (lane & 3)
-                      : -1;
-        }
+        // rows of this lane's quad: the first one's place in the output, the steps to the other
+        // three, and how many of them are the item's
+        const int quad = packed & ~3, HD = p.H * D;
+        const int step1 = g_shift == 0 ? HD : D, step2 = g_shift == 0 ? 2 * HD : g_shift == 1 ? HD : 2 * D;
+        const int in_quad = (d.tokens << g_shift) - quad;
+        uint16_t* out = static_cast<uint16_t*>(p.out) +
+                        (static_cast<size_t>(d.row0 + (quad >> g_shift)) * p.H + (d.kh << g_shift) +
+                         (quad & ((1 << g_shift) - 1))) * D + 8 * (lane & 3);
+        const float f0 = c0 * inv, f1 = c1 * inv;
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
           float o[32];
@@ -500,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
             tmem_arrived32(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= c0;
+            for (int e = 0; e < 32; ++e) o[e] *= f0;
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0.f;
@@ -511,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
             tmem_arrived32(o1);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], c1, o[e]);
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e]);
           }
           if (odd) {  // non-finite V values, for the rows that see them
             for (int y = 0; y < 128 * 3; ++y) {
@@ -531,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   f = kBf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16)
                             : __half2float(__ushort_as_half(u));
                 }
-                if (!isfinite(f) && key <= pos) o[e] += f;
+                if (!isfinite(f) && key <= pos) o[e] = fmaf(f, inv, o[e]);
               }
             }
           }
@@ -549,15 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 v[4];
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
-              v[e / 8] = make_uint4(pack2<kBf16>(o[e] * inv, o[e + 1] * inv),
-                                    pack2<kBf16>(o[e + 2] * inv, o[e + 3] * inv),
-                                    pack2<kBf16>(o[e + 4] * inv, o[e + 5] * inv),
-                                    pack2<kBf16>(o[e + 6] * inv, o[e + 7] * inv));
+              v[e / 8] = make_uint4(pack2<kBf16>(o[e], o[e + 1]), pack2<kBf16>(o[e + 2], o[e + 3]),
+                                    pack2<kBf16>(o[e + 4], o[e + 5]), pack2<kBf16>(o[e + 6], o[e + 7]));
             quad_transpose(v);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              if (at[r] >= 0)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at[r] + k) = v[r];
+              if (r < in_quad)
+                *reinterpret_cast<uint4*>(out + (r & 1) * step1 + (r >> 1) * step2 + k) = v[r];
           }
           __syncwarp();
         }
