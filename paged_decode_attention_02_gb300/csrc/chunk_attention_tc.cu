@@ -188,11 +188,6 @@ __device__ __forceinline__ Groups groups_of(const Desc& d) {
   return Groups{max(0, min(d.jb, d.tiles0) - d.ja), max(0, min(d.jb, d.tiles1) - d.ja)};
 }
 
-__device__ __forceinline__ bool nonfinite16(uint32_t w, uint32_t exp_mask, uint32_t exp_one) {
-  // per half: (exponent bits) + 1 carries into the sign place when they are all ones
-  return (((w & exp_mask) + exp_one) & 0x80008000u) != 0;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -239,6 +234,59 @@ __device__ __forceinline__ void widen(unsigned char* dst, const unsigned char* c
       const int piece = c + (swap ? 1 - k : k);
       *reinterpret_cast<uint4*>(dst + (piece >> 3) * (kChunkKeys * 128) + r * 128 +
                                 (((piece & 7) ^ (r & 7)) << 4)) = swap == (k == 0) ? o[1] : o[0];
+    }
+  }
+}
+
+// Cleans this warp's quarter of a V tile of `keys` rows, in boxes of `box_rows` rows: zeroes what
+// the products read behind them, and replaces non-finite values by zeros, setting their rows'
+// bits in `nonfinite`.
+template <int D, bool kBf16>
+__device__ __forceinline__ void clean_tile(unsigned char* tile, int part, int keys, int box_rows,
+                                           unsigned* nonfinite) {
+  constexpr uint32_t kMask = kBf16 ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t kOne = kBf16 ? 0x00800080u : 0x04000400u;
+  const int lane = threadIdx.x & 31;
+  const int rows = (keys + 15) & ~15;
+  // a lane takes one 16-byte chunk of each 128-byte half of every fourth row
+  auto chunk = [&](int i) {
+    const int h = D == 128 ? i & 1 : 0, r = 32 * part + 4 * (D == 128 ? i >> 1 : i) + (lane >> 3);
+    return reinterpret_cast<uint4*>(tile + (r & ~(box_rows - 1)) * (D * 2) +
+                                    (h * box_rows + (r & (box_rows - 1))) * 128) + (lane & 7);
+  };
+  auto row = [&](int i) { return 32 * part + 4 * (D == 128 ? i >> 1 : i) + (lane >> 3); };
+  // exponents of all ones carry into the sign's place when one is added
+  auto hits = [&](uint32_t w) { return ((w & kMask) + kOne) & 0x80008000u; };
+  uint32_t any = 0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < D / 8; i0 += 4) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *chunk(i0 + i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row(i0 + i) < keys) any |= hits(v[i].x) | hits(v[i].y) | hits(v[i].z) | hits(v[i].w);
+  }
+  if (keys < kChunkKeys)
+#pragma unroll 1
+    for (int i = 0; i < D / 8; ++i)
+      if (row(i) >= keys && row(i) < rows) *chunk(i) = make_uint4(0, 0, 0, 0);
+  if (!__any_sync(kFullMask, any != 0)) return;
+#pragma unroll 1
+  for (int i = 0; i < D / 8; ++i) {
+    if (row(i) >= keys) continue;
+    uint4 v = *chunk(i);
+    uint32_t* e = &v.x;
+    uint32_t all = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t hit = hits(e[k]);
+      e[k] &= ~((hit >> 15) * 0xffffu);
+      all |= hit;
+    }
+    if (all != 0) {
+      *chunk(i) = v;
+      atomicOr(&nonfinite[row(i) >> 5], 1u << (row(i) & 31));
     }
   }
 }
@@ -716,13 +764,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool negate = p.scale_log2 < 0.f;  // S is compared and scaled by |scale|
     const uint32_t id_qk = mma_idesc(kBf16, kChunkKeys, negate, false);
     const uint32_t id_pv = mma_idesc(kBf16, D, false, true);
-    const uint64_t dk0 = smem_desc_sw128(smem_addr(ks), 16, 1024);
-    const uint64_t dq0 = smem_desc_sw128(smem_addr(qs), 16, 1024);
+    // descriptors as (address, rest) words: moving along a tile changes the address alone
+    const uint64_t dk = smem_desc_sw128(smem_addr(ks), 16, 1024), dq = smem_desc_sw128(smem_addr(qs), 16, 1024);
+    const uint32_t dk0 = static_cast<uint32_t>(dk), dq0 = static_cast<uint32_t>(dq);
+    const uint32_t hi_qk = static_cast<uint32_t>(dk >> 32);
+    auto desc = [](uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; };
     const int box_rows = kFp8 ? kChunkKeys : min(p.block_size, kChunkKeys);
-    const uint64_t dv0 = smem_desc_sw128(smem_addr(vs), box_rows * 128, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_addr(vs), box_rows * 128, 1024);
+    const uint32_t dv0 = static_cast<uint32_t>(dv), hi_v = static_cast<uint32_t>(dv >> 32);
     // 16, 32 and 64 rows further down: in the same box, or past the boxes in between
-    auto rows_down = [&](int n) { return static_cast<uint64_t>(n < box_rows ? n * 128 : n * D * 2) >> 4; };
-    const uint64_t v_step1 = rows_down(16), v_step2 = rows_down(32), v_step4 = rows_down(64);
+    auto rows_down = [&](int n) { return static_cast<uint32_t>(n < box_rows ? n * 128 : n * D * 2) >> 4; };
+    const uint32_t v_step1 = rows_down(16), v_step2 = rows_down(32), v_step4 = rows_down(64);
     int k_at = 0, k_turn = 0, v_at = 0, v_turn = 0;  // stage and parity of the next K, V tile
     unsigned p_phase = 0;
     for (int item = 0; !timed_out; ++item) {
@@ -747,11 +799,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A tile is used by both groups, the second releasing it, or (single) by one.
       auto qk = [&](int g, int s) {
         if (leader) {
-          const uint64_t a = dq0 + (single ? 0 : g * (C::kTile >> 4)), b = dk0 + k_at * (C::kTile >> 4);
+          const uint32_t a = dq0 + (single ? 0 : g * (C::kTile >> 4)), b = dk0 + k_at * (C::kTile >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
-            mma_f16_ss(tmem + g * 128, a + off, b + off, id_qk, k > 0);
+            mma_f16_ss(tmem + g * 128, desc(a + off, hi_qk), desc(b + off, hi_qk), id_qk, k > 0);
           }
           mma_commit(&ms.s_full[g]);
           if (single || g == 1) mma_commit(&ms.k_empty[k_at]);
@@ -783,12 +835,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int left = keys - (single ? 2 * s + g : s) * kChunkKeys;
         if (leader) {
-          const uint64_t b = dv0 + v_at * (C::kTile >> 4);
+          const uint32_t b = dv0 + v_at * (C::kTile >> 4);
 #pragma unroll
           for (int k = 0; k < kChunkKeys / 16; ++k)
             if (16 * k < left)
               mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * k,
-                         b + (k & 1) * v_step1 + (k >> 1 & 1) * v_step2 + (k >> 2) * v_step4, id_pv,
+                         desc(b + (k & 1) * v_step1 + (k >> 1 & 1) * v_step2 + (k >> 2) * v_step4, hi_v), id_pv,
                          s > 0 || k > 0);
           if (single || g == 1) mma_commit(&ms.v_empty[v_at]);
           if (!more) mma_commit(&ms.o_full[g]);
@@ -957,31 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         const int keys = min(kChunkKeys, kv_end - (ja + t) * kChunkKeys);
-        const int rows = (keys + 15) & ~15;  // what the products read
-        constexpr uint32_t kMask = kBf16 ? 0x7f807f80u : 0x7c007c00u;
-        constexpr uint32_t kOne = kBf16 ? 0x00800080u : 0x04000400u;
-        // a lane takes one 16-byte chunk of both halves of a row
-        for (int r = part * 4 + (lane >> 3); r < rows; r += 4 * kCleaners) {
-          for (int h = 0; h < C::kHalves; ++h) {
-            const int byte = (r / box_rows) * box_rows * D * 2 + (h * box_rows + r % box_rows) * 128;
-            uint4* at16 = reinterpret_cast<uint4*>(vs + st * C::kTile + byte) + (lane & 7);
-            if (r >= keys) {
-              *at16 = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 v = *at16;
-            if (nonfinite16(v.x, kMask, kOne) || nonfinite16(v.y, kMask, kOne) ||
-                nonfinite16(v.z, kMask, kOne) || nonfinite16(v.w, kMask, kOne)) {
-              uint32_t* e = &v.x;
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t hit = ((e[k] & kMask) + kOne) & 0x80008000u;
-                e[k] &= ~((hit >> 15) * 0xffffu);
-              }
-              *at16 = v;
-              atomicOr(&d.nonfinite[ja + t - jc][r >> 5], 1u << (r & 31));
-            }
-          }
-        }
+        clean_tile<D, kBf16>(vs + st * C::kTile, part, keys, box_rows, d.nonfinite[ja + t - jc]);
         fence_proxy_async_smem();
         __threadfence_block();
         __syncwarp();
