@@ -553,8 +553,8 @@ pda_status pda_chunk_attention_workspace_size(int B, int T, int H, int H_kv, int
  *  context_lens   [B] int32 (device). L == 0 gives zero rows (a padded request). L < 0,
  *                 L > max_context_len, L > max_blocks_per_seq * block_size or 0 < L < n
  *                 gives NaN rows and PDA_DEVERR_CONTEXT_LEN.
- *  A request whose pair of query_start is decreasing or outside [0, T] is left out
- *  (PDA_DEVERR_QUERY). A block id out of range gives NaN in the rows that see the block and
+ *  A query_start that decreases or leaves [0, T] anywhere sets PDA_DEVERR_QUERY, and the
+ *  call computes and writes nothing. A block id out of range gives NaN in the rows that see the block and
  *  PDA_DEVERR_BLOCK_ID.
  *  What the cache holds behind a row's position (later tokens, rows behind L, unused blocks)
  *  does not reach that row's output, NaN and infinities included.
@@ -565,7 +565,8 @@ pda_status pda_chunk_attention_workspace_size(int B, int T, int H, int H_kv, int
  *                 256-byte aligned, not shared by calls that may run concurrently; its
  *                 content before and after a call means nothing.
  *  The other arguments, the supported sizes (D, block_size, H / H_kv, B) and alignment are
- *  those of pda_paged_decode_attention; T * H < 2^31.
+ *  those of pda_paged_decode_attention; T * H < 2^31, and (T / t + B) * H_kv *
+ *  (max_context_len / 128 + 1) < 2^31 with t = 256 * H_kv / H tokens (fp32: 64 * H_kv / H).
  */
 pda_status pda_paged_chunk_attention(void* out, const void* q, const void* k_cache,
                                      const void* v_cache, const int32_t* block_tables,

@@ -58,6 +58,18 @@ pda_status launch_chunk(void* out, const void* q, const void* k_cache, const voi
   if (static_cast<long long>(num_blocks) * block_size >= (1ll << 31) ||
       static_cast<long long>(B) * max_blocks_per_seq >= (1ll << 31))
     return PDA_ERR_UNSUPPORTED;
+  const ChunkParams p{out,     q,      k_cache,   v_cache,
+                      block_tables, context_lens, query_start, error_word,
+                      scale * k_scale * 1.4426950408889634f,
+                      v_scale, B,      T,         H,
+                      H_kv,    H / H_kv, max_blocks_per_seq, max_context_len,
+                      block_size, num_blocks};
+  // the kernels number their work, items by key tiles, in 31 bits
+  int g_shift = 0;
+  while ((1 << g_shift) < p.G) ++g_shift;
+  const long long units = kv_dtype == PDA_F32 ? chunk_units<Cuts<6, 1, 1>>(p, g_shift)
+                                              : chunk_units<Cuts<8, 1, 1>>(p, g_shift);
+  if (units >= (1ll << 31)) return PDA_ERR_UNSUPPORTED;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PDA_ERR_WORKSPACE;
   int dev, sms;
@@ -65,12 +77,6 @@ pda_status launch_chunk(void* out, const void* q, const void* k_cache, const voi
   if (dst != PDA_OK) return dst;
   if (sm_cap > 0 && sm_cap < sms) sms = sm_cap;
   if (workspace_bytes < chunk_workspace(sms, D)) return PDA_ERR_WORKSPACE;
-  const ChunkParams p{out,     q,      k_cache,   v_cache,
-                      block_tables, context_lens, query_start, error_word,
-                      scale * k_scale * 1.4426950408889634f,
-                      v_scale, B,      T,         H,
-                      H_kv,    H / H_kv, max_blocks_per_seq, max_context_len,
-                      block_size, num_blocks};
   return kv_dtype == PDA_F32 ? launch_chunk_f32(p, D, dev, sms, workspace, stream)
                              : launch_chunk_tc(p, D, kv_dtype, dev, sms, workspace, stream);
 }

@@ -24,7 +24,7 @@ struct Smem {
   float p[kKeys][kRows + 4];  // key-major, so a thread's four rows are one piece
   PlanMemory plan;
   Where first;
-  long long range[2];
+  int range[2];
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
@@ -51,12 +51,9 @@ __global__ void __launch_bounds__(256, 1)
   const Plan pl = make_plan<CutsOf>(p, lt, gridDim.x, &sm.plan);
 
   // requests without work whose rows are written all the same: padded (zeros) or in error (NaN)
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+  if (!pl.ok && blockIdx.x == 0 && tid == 0) atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
+  for (int b = pl.ok ? blockIdx.x : p.B; b < p.B; b += gridDim.x) {
     const int q0 = p.query_start[b], q1 = p.query_start[b + 1], L = p.context_lens[b];
-    if (q0 < 0 || q1 > p.T || q0 > q1) {
-      if (tid == 0) atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
-      continue;
-    }
     if (q0 == q1 || chunk_req(p, b, lt).r.n > 0) continue;
     if (L != 0 && tid == 0) atomic_or_error(p.error_word, PDA_DEVERR_CONTEXT_LEN);
     const float f = L == 0 ? 0.f : NAN;
@@ -67,13 +64,13 @@ __global__ void __launch_bounds__(256, 1)
 
   if (warp == 0) {
     Where w{};
-    long long u = 0, u_end = 0;
+    int u = 0, u_end = 0;
     if (static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0) {
       u = cut_of<CutsOf>(p, pl, lt, blockIdx.x + (lane & 1), &w);
       u_end = __shfl_sync(kFullMask, u, 1);
       u = __shfl_sync(kFullMask, u, 0);
-      if (lane == 0 && u < u_end && u >= w.start + w.q.r.tiles(w.i) + 1)
-        w = locate(p, pl, lt, u);
+      // lane 0's item is the block's; the others' are not
+      if (lane == 0 && u < u_end && u > w.start + w.q.r.tiles(w.i)) next_item(p, lt, &w);
     }
     if (lane == 0) {
       sm.first = w;
@@ -83,18 +80,18 @@ __global__ void __launch_bounds__(256, 1)
   }
   __syncthreads();
   Where w = sm.first;
-  long long u = sm.range[0];
-  const long long u_end = sm.range[1];
+  int u = sm.range[0];
+  const int u_end = sm.range[1];
   const float* k_cache = static_cast<const float*>(p.k_cache);
   const float* v_cache = static_cast<const float*>(p.v_cache);
 
   while (u < u_end) {
     const ChunkReq r = w.q.r;
     const int tiles = r.tiles(w.i);
-    const long long end = w.start + tiles + 1;
+    const int end = w.start + tiles + 1;
     const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
-    const int ja = u == w.start ? 0 : static_cast<int>(u - w.start - 1);
-    const int jb = u_end >= end ? tiles : static_cast<int>(u_end - w.start - 1);
+    const int ja = u == w.start ? 0 : u - w.start - 1;
+    const int jb = u_end >= end ? tiles : u_end - w.start - 1;
     const int pos0 = r.L - r.n + tok0, kv_end = pos0 + tokens;
     const int32_t* table = p.block_tables + static_cast<size_t>(w.b) * p.max_blocks;
     const int first_key = ja * kChunkKeys, last_key = min(kv_end, jb * kChunkKeys);
@@ -253,20 +250,7 @@ __global__ void __launch_bounds__(256, 1)
     }
     // the next item
     u = end;
-    if (u < u_end) {
-      w.start = end;
-      if (w.i + 1 < r.items()) {
-        ++w.i;
-      } else {
-        w.i = 0;
-        if (++w.kh == p.H_kv) {
-          w.kh = 0;
-          do {
-            w.q = chunk_req(p, ++w.b, lt);
-          } while (w.q.r.n == 0);
-        }
-      }
-    }
+    if (u < u_end) next_item(p, lt, &w);
   }
 }
 

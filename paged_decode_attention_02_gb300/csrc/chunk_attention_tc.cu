@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // ================================================================ plan, load Q and K
     Where w{};
-    long long u = 0, u_end = 0;
+    int u = 0, u_end = 0;
     if (static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0) {
       // both ends of the range at once: the odd lanes find the upper one
       u = cut_of<CutsOf>(p, pl, lt, blockIdx.x + (lane & 1), &w);
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.q.r.n = __shfl_sync(kFullMask, w.q.r.n, 0);
       w.q.r.L = __shfl_sync(kFullMask, w.q.r.L, 0);
       w.q.r.lt = lt;
-      if (u < u_end && u >= w.start + w.q.r.tiles(w.i) + 1) w = locate(p, pl, lt, u);
+      if (u < u_end && u > w.start + w.q.r.tiles(w.i)) next_item(p, lt, &w);
     }
     __syncwarp();
     fence_proxy_async_smem();  // the plan's shared memory becomes load stages
@@ -649,10 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (u < u_end && !timed_out) {
       const ChunkReq r = w.q.r;
       const int tiles = r.tiles(w.i);
-      const long long end = w.start + tiles + 1;
+      const int end = w.start + tiles + 1;
       const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
-      const int ja = u == w.start ? 0 : static_cast<int>(u - w.start - 1);
-      const int jb = u_end >= end ? tiles : static_cast<int>(u_end - w.start - 1);
+      const int ja = u == w.start ? 0 : u - w.start - 1;
+      const int jb = u_end >= end ? tiles : u_end - w.start - 1;
       const int slot = item % kDescs;
       Desc& d = ms.desc[slot];
       if (!warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
@@ -729,20 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++item;
       // the next item
       u = end;
-      if (u < u_end) {
-        w.start = end;
-        if (w.i + 1 < r.items()) {
-          ++w.i;
-        } else {
-          w.i = 0;
-          if (++w.kh == p.H_kv) {
-            w.kh = 0;
-            do {
-              w.q = chunk_req(p, ++w.b, lt);
-            } while (w.q.r.n == 0);
-          }
-        }
-      }
+      if (u < u_end) next_item(p, lt, &w);
     }
     if (!timed_out) {
       const int slot = item % kDescs;
@@ -935,21 +922,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 11) {
     // ================================================================ rows without work
     // requests whose rows are written all the same: padded (zeros) or in error (NaN)
-    for (int first = blockIdx.x; first < p.B; first += 32 * gridDim.x) {
+    if (!pl.ok && blockIdx.x == 0 && lane == 0) atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
+    for (int first = pl.ok ? blockIdx.x : p.B; first < p.B; first += 32 * gridDim.x) {
       const int b = first + lane * gridDim.x;
       int q0 = 0, q1 = 0, L = 0;
-      if (b < p.B) {
+      if (b < p.B && chunk_req(p, b, lt).r.n == 0) {
         q0 = p.query_start[b];
         q1 = p.query_start[b + 1];
         L = p.context_lens[b];
-        if (q0 < 0 || q1 > p.T || q0 > q1) {
-          atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
-          q0 = q1 = 0;
-        } else if (chunk_req(p, b, lt).r.n > 0) {
-          q0 = q1 = 0;
-        } else if (q0 < q1 && L != 0) {
-          atomic_or_error(p.error_word, PDA_DEVERR_CONTEXT_LEN);
-        }
+        if (q0 < q1 && L != 0) atomic_or_error(p.error_word, PDA_DEVERR_CONTEXT_LEN);
       }
       for (unsigned todo = __ballot_sync(kFullMask, q0 < q1); todo != 0; todo &= todo - 1) {
         const int from = __ffs(todo) - 1;

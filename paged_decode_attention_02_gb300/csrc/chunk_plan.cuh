@@ -28,19 +28,18 @@ struct Req {
 };
 
 struct PlanMemory {
-  long long prefix[kPlanChunks + 1];
+  int prefix[kPlanChunks + 1];
   int3 req[kPlanChunks];  // (row0, n, L) of each request, where there are no more than this
 };
 
 struct Plan {
   PlanMemory* mem;
-  int per, workers;
-  long long units;
+  int per, workers, units;
+  bool ok;  // query_start never decreases and stays within [0, T]; otherwise there is no work
 };
 
 struct Where {
-  int b, kh, i;
-  long long start;  // unit
+  int b, kh, i, start;  // start: a unit
   Req q;
 };
 
@@ -60,36 +59,38 @@ __device__ __forceinline__ Plan make_plan(const ChunkParams& p, int lt, int work
   pl.mem = mem;
   pl.per = (p.B + kPlanChunks - 1) / kPlanChunks;
   const int c = threadIdx.x, lane = c & 31;
-  long long x = 0;
+  int x = 0;
+  bool bad = false;
   if (c < kPlanChunks)
     for (int b = c * pl.per; b < min(p.B, (c + 1) * pl.per); ++b) {
       const Req q = chunk_req(p, b, lt);
+      bad |= q.row0 < 0 || q.row0 > p.query_start[b + 1] || p.query_start[b + 1] > p.T;
       x += q.r.units();
       if (pl.per == 1) mem->req[b] = make_int3(q.row0, q.r.n, q.r.L);
     }
   x *= p.H_kv;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(kFullMask, x, o);
+    const int y = __shfl_up_sync(kFullMask, x, o);
     if (lane >= o) x += y;
   }
   if (c < kPlanChunks) mem->prefix[c + 1] = x;
-  __syncthreads();
-  long long before = 0;
+  // overlapping requests could be any amount of work, so there is none at all
+  pl.ok = !__syncthreads_or(bad);
+  int before = 0;
   if (c < kPlanChunks)
     for (int w = 0; w < (c >> 5); ++w) before += mem->prefix[32 * w + 32];
   __syncthreads();
   if (c < kPlanChunks) mem->prefix[c + 1] = x + before;
   if (c == 0) mem->prefix[0] = 0;
   __syncthreads();
-  pl.units = mem->prefix[kPlanChunks];
+  pl.units = pl.ok ? mem->prefix[kPlanChunks] : 0;
   pl.workers = chunk_workers(pl.units, workers, C::kWorkerUnits);
   return pl;
 }
 
 // The item that holds unit u < units. Valid while the plan's memory is.
-__device__ __forceinline__ Where locate(const ChunkParams& p, const Plan& pl, int lt,
-                                        long long u) {
+__device__ __forceinline__ Where locate(const ChunkParams& p, const Plan& pl, int lt, int u) {
   int lo = 0, hi = kPlanChunks - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -98,7 +99,7 @@ __device__ __forceinline__ Where locate(const ChunkParams& p, const Plan& pl, in
     else
       lo = mid + 1;
   }
-  long long at = pl.mem->prefix[lo];
+  int at = pl.mem->prefix[lo];
   int b = lo * pl.per;
   Req q;
   if (pl.per == 1) {
@@ -107,23 +108,35 @@ __device__ __forceinline__ Where locate(const ChunkParams& p, const Plan& pl, in
   } else {
     q = chunk_req(p, b, lt);
   }
-  long long one = q.r.units();
+  int one = q.r.units();
   while (at + one * p.H_kv <= u) {
     at += one * p.H_kv;
     q = chunk_req(p, ++b, lt);
     one = q.r.units();
   }
-  const int kh = static_cast<int>(chunk_div(u - at, one));
+  const int kh = static_cast<unsigned>(u - at) / static_cast<unsigned>(one);
   at += kh * one;
   const int i = q.r.item_of(u - at);
   return Where{b, kh, i, at + q.r.units_before(i), q};
 }
 
+// Moves on to the item behind, of a batch that has one.
+__device__ __forceinline__ void next_item(const ChunkParams& p, int lt, Where* w) {
+  w->start += w->q.r.tiles(w->i) + 1;
+  if (++w->i < w->q.r.items()) return;
+  w->i = 0;
+  if (++w->kh < p.H_kv) return;
+  w->kh = 0;
+  do {
+    w->q = chunk_req(p, ++w->b, lt);
+  } while (w->q.r.n == 0 && w->b + 1 < p.B);
+}
+
 // The cut before worker c, snapped; *w: the item it falls into (for a cut below `units`).
 template <typename C>
-__device__ __forceinline__ long long cut_of(const ChunkParams& p, const Plan& pl, int lt, int c,
-                                            Where* w) {
-  const long long u = chunk_cut(pl.units, pl.workers, c);
+__device__ __forceinline__ int cut_of(const ChunkParams& p, const Plan& pl, int lt, int c,
+                                      Where* w) {
+  const int u = chunk_cut(pl.units, pl.workers, c);
   if (u >= pl.units) return pl.units;
   *w = locate(p, pl, lt, u);
   return chunk_snap(u, w->start, w->q.r.tiles(w->i), C::kPieceTiles);
@@ -179,14 +192,14 @@ __global__ void __launch_bounds__(256)
   Where w{};
   if (c < pl.workers) {
     // the cut and, on the odd lanes, the one before it
-    const long long s = cut_of<C>(p, pl, lt, c - (lane & 1), &w);
+    const int s = cut_of<C>(p, pl, lt, c - (lane & 1), &w);
     const int tiles = w.q.r.tiles(w.i);
-    const long long end = w.start + tiles + 1;
-    const long long before = __shfl_sync(kFullMask, s, 1);
+    const int end = w.start + tiles + 1;
+    const int before = __shfl_sync(kFullMask, s, 1);
     if (lane == 0 && s > w.start && s < end && before <= w.start) {
       pieces = 2;  // worker c - 1's, and one for each cut inside the item
       for (; c + pieces - 1 < pl.workers; ++pieces) {
-        const long long u = chunk_cut(pl.units, pl.workers, c + pieces - 1);
+        const int u = chunk_cut(pl.units, pl.workers, c + pieces - 1);
         if (u >= end || chunk_snap(u, w.start, tiles, C::kPieceTiles) >= end) break;
       }
       rows = min(1 << lt, w.q.r.n - (w.i << lt)) << g_shift;
@@ -240,9 +253,13 @@ inline int chunk_tiles(const ChunkParams& p) {
 }
 // Blocks of a launch: no more than that bound can keep busy.
 template <typename C>
-int chunk_grid(const ChunkParams& p, int g_shift, int sms) {
+long long chunk_units(const ChunkParams& p, int g_shift) {
   const long long items = ((static_cast<long long>(p.T) >> (C::kRowsLog2 - g_shift)) + p.B) * p.H_kv;
-  return chunk_workers(items * (chunk_tiles(p) + 1), sms, C::kWorkerUnits);
+  return items * (chunk_tiles(p) + 1);
+}
+template <typename C>
+int chunk_grid(const ChunkParams& p, int g_shift, int sms) {
+  return chunk_workers(chunk_units<C>(p, g_shift), sms, C::kWorkerUnits);
 }
 
 // Merges what the kernel before it on the stream has cut, where anything can have been.

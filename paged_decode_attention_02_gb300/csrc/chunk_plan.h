@@ -19,39 +19,47 @@ namespace pda {
 
 constexpr int kChunkKeys = 128;    // keys of a tile
 
+// Units fit 31 bits: the host refuses sizes whose bound on them does not. What only passes
+// through larger values on the way is unsigned, where wrapping cancels.
 struct ChunkReq {
   int n, L;     // new tokens, and all of them; n <= L
   int lt;       // log2 of an item's tokens
-  PDA_CHUNK_HD int items() const { return static_cast<int>((static_cast<long long>(n) + (1 << lt) - 1) >> lt); }
+  PDA_CHUNK_HD int items() const {
+    return static_cast<int>((static_cast<unsigned>(n) + (1u << lt) - 1) >> lt);
+  }
   // key tiles of item i
   PDA_CHUNK_HD int tiles(int i) const {
-    const long long end = (static_cast<long long>(i) + 1) << lt;
-    const int last = L - n + static_cast<int>(end < n ? end : n) - 1;
+    const unsigned end = (static_cast<unsigned>(i) + 1) << lt;
+    const int last = L - n + static_cast<int>(end < static_cast<unsigned>(n) ? end : n) - 1;
     return (last >> 7) + 1;
   }
+  // x (x - 1) / 2
+  static PDA_CHUNK_HD unsigned pairs(unsigned x) {
+    return (x & 1) != 0 ? x * ((x - 1) >> 1) : (x >> 1) * (x - 1);
+  }
   // sum of floor(y / 2^s) over 0 <= y < x
-  static PDA_CHUNK_HD long long floor_sum(long long x, int s) {
-    const long long q = x >> s;
-    return ((q * (q - 1)) << s) / 2 + q * (x - (q << s));
+  static PDA_CHUNK_HD unsigned floor_sum(unsigned x, int s) {
+    const unsigned q = x >> s;
+    return (pairs(q) << s) + q * (x - (q << s));
   }
   // units of items [0, i), i < items(): all of them full. With a = L - n, item j's last
   // position is a + (j + 1) 2^lt - 1, so its tiles are a floor of an arithmetic progression.
-  PDA_CHUNK_HD long long units_before(int i) const {
+  PDA_CHUNK_HD int units_before(int i) const {
     const int a1 = L - n - 1;  // may be -1: the shifts below round down
-    const long long m = i;
-    if (lt >= 7) return m * ((a1 >> 7) + 2) + ((m * (m + 1) / 2) << (lt - 7));
+    const unsigned m = i;
+    if (lt >= 7) return static_cast<int>(m * ((a1 >> 7) + 2) + (pairs(m + 1) << (lt - 7)));
     const int s = 7 - lt;
-    const long long x0 = (a1 >> lt) + 1;
-    return 2 * m + floor_sum(x0 + m, s) - floor_sum(x0, s);
+    const unsigned x0 = (a1 >> lt) + 1;
+    return static_cast<int>(2 * m + floor_sum(x0 + m, s) - floor_sum(x0, s));
   }
   // units of one kv-head
-  PDA_CHUNK_HD long long units() const {
+  PDA_CHUNK_HD int units() const {
     if (n == 0) return 0;
     const int last = items() - 1;
     return units_before(last) + tiles(last) + 1;
   }
   // the item that holds unit w of a kv-head
-  PDA_CHUNK_HD int item_of(long long w) const {
+  PDA_CHUNK_HD int item_of(int w) const {
     int lo = 0, hi = items() - 1;
     while (lo < hi) {
       const int mid = lo + (hi - lo + 1) / 2;
@@ -67,29 +75,22 @@ struct ChunkReq {
 // Where a cut at unit u of an item that starts at unit `start` really falls: before key tile
 // u - start - 1, or at the item's start or end where that leaves a piece of fewer than
 // `least` tiles.
-PDA_CHUNK_HD long long chunk_snap(long long u, long long start, int tiles, int least) {
-  const long long j = u - start - 1;
+PDA_CHUNK_HD int chunk_snap(int u, int start, int tiles, int least) {
+  const int j = u - start - 1;
   if (j < least) return start;
   if (tiles - j < least) return start + tiles + 1;
   return u;
 }
 
-// a / b for 0 <= a, 0 < b; in 32 bits, several times faster, where both fit.
-PDA_CHUNK_HD long long chunk_div(long long a, long long b) {
-  if (((a | b) >> 32) == 0)
-    return static_cast<unsigned>(a) / static_cast<unsigned>(b);
-  return a / b;
-}
-
 // First unit of worker c's range, before snapping.
-PDA_CHUNK_HD long long chunk_cut(long long units, int workers, int c) {
-  const long long q = chunk_div(units, workers), r = units - q * workers;
-  return c * q + chunk_div(c * r, workers);
+PDA_CHUNK_HD int chunk_cut(int units, int workers, int c) {
+  const unsigned w = workers, q = static_cast<unsigned>(units) / w, r = units - q * w;
+  return static_cast<int>(c * q + c * r / w);
 }
 
 // Workers a launch of `units` units uses: no more than leave each `least` of them.
 PDA_CHUNK_HD int chunk_workers(long long units, int workers, int least) {
-  const long long most = chunk_div(units + least - 1, least);
+  const long long most = units >> 30 != 0 ? workers : (static_cast<unsigned>(units) + least - 1) / static_cast<unsigned>(least);
   return most < 1 ? 1 : most < workers ? static_cast<int>(most) : workers;
 }
 

@@ -19,7 +19,7 @@ int main() {
   auto rnd = [&](int m) { return static_cast<int>((seed = seed * 1664525u + 1013904223u) >> 8) % m; };
   for (int it = 0; it < 20000; ++it) {
     ChunkReq r;
-    r.lt = 5 + rnd(4);
+    r.lt = 3 + rnd(6);
     r.n = it < 4000 ? 1 + rnd(600) : 1 + rnd(9000);
     r.L = r.n + (rnd(3) ? rnd(it % 2 ? 300 : 20000) : 0);
     long long sum = 0;
@@ -35,12 +35,21 @@ int main() {
     }
     require(r.units() == sum, "units", r.n, r.L, r.lt);
   }
-  // a very long request stays exact in 64 bits
-  ChunkReq big{1 << 30, 1 << 30, 5};
-  require(big.units() > (1ll << 40), "big", big.n, big.L, big.lt);
+  // intermediate sums past 32 bits cancel: long histories, few rows of small items
+  for (int k = 0; k < 40; ++k) {
+    ChunkReq r;
+    r.lt = 3 + rnd(6);
+    r.n = 1 + rnd(4000);
+    r.L = (1 << 24) + rnd(1 << 28);
+    long long sum = 0;
+    for (int i = 0; i < r.items() && sum < (1ll << 30); ++i) {
+      require(r.units_before(i) == sum, "long", r.n, r.L, r.lt);
+      sum += r.tiles(i) + 1;
+    }
+  }
   for (int it = 0; it < 300; ++it) {
     std::vector<ChunkReq> reqs;
-    const int B = 1 + rnd(9), H_kv = 1 + rnd(4), lt = 5 + rnd(4), least = 1 + rnd(6);
+    const int B = 1 + rnd(9), H_kv = 1 + rnd(4), lt = 3 + rnd(6), least = 1 + rnd(6);
     std::vector<long long> start;
     std::vector<int> tiles;
     long long W = 0;
@@ -59,12 +68,12 @@ int main() {
     const int workers = chunk_workers(W, 1 + rnd(152), 1 + rnd(8));
     std::vector<std::vector<int>> seen;
     for (int t : tiles) seen.push_back(std::vector<int>(t, 0));
-    auto snapped = [&](int c) {
-      const long long u = chunk_cut(W, workers, c);
+    auto snapped = [&](int c) -> long long {
+      const int u = chunk_cut(static_cast<int>(W), workers, c);
       if (u >= W) return W;
       size_t i = 0;
       while (i + 1 < start.size() && start[i + 1] <= u) ++i;
-      return chunk_snap(u, start[i], tiles[i], least);
+      return chunk_snap(u, static_cast<int>(start[i]), tiles[i], least);
     };
     require(snapped(0) == 0 && snapped(workers) == W, "ends", B, H_kv, lt);
     for (int c = 0; c < workers; ++c) {
