@@ -566,7 +566,7 @@ pda_status pda_chunk_attention_workspace_size(int B, int T, int H, int H_kv, int
  *                 content before and after a call means nothing.
  *  The other arguments, the supported sizes (D, block_size, H / H_kv, B) and alignment are
  *  those of pda_paged_decode_attention; T * H < 2^31, and (T / t + B) * H_kv *
- *  (max_context_len / 128 + 1) < 2^31 with t = 256 * H_kv / H tokens (fp32: 64 * H_kv / H).
+ *  (max_context_len / 128 + 5) < 2^31 with t = 256 * H_kv / H tokens (fp32: 64 * H_kv / H).
  */
 pda_status pda_paged_chunk_attention(void* out, const void* q, const void* k_cache,
                                      const void* v_cache, const int32_t* block_tables,

@@ -13,7 +13,7 @@
 namespace pda {
 namespace {
 
-using CutsOf = Cuts<6, 4, 4>;  // 64-row items
+using CutsOf = Cuts<6, 4, 6>;  // 64-row items
 constexpr int kRows = 64, kKeys = 64;
 
 template <int D>
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256, 1)
       u_end = __shfl_sync(kFullMask, u, 1);
       u = __shfl_sync(kFullMask, u, 0);
       // lane 0's item is the block's; the others' are not
-      if (lane == 0 && u < u_end && u > w.start + w.q.r.tiles(w.i)) next_item(p, lt, &w);
+      if (lane == 0 && u < u_end && u >= w.start + w.q.r.tiles(w.i) + kItemUnits) next_item(p, lt, &w);
     }
     if (lane == 0) {
       sm.first = w;
@@ -88,10 +88,10 @@ __global__ void __launch_bounds__(256, 1)
   while (u < u_end) {
     const ChunkReq r = w.q.r;
     const int tiles = r.tiles(w.i);
-    const int end = w.start + tiles + 1;
+    const int end = w.start + tiles + kItemUnits;
     const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
-    const int ja = u == w.start ? 0 : u - w.start - 1;
-    const int jb = u_end >= end ? tiles : u_end - w.start - 1;
+    const int ja = u == w.start ? 0 : u - w.start - kItemUnits;
+    const int jb = u_end >= end ? tiles : u_end - w.start - kItemUnits;
     const int pos0 = r.L - r.n + tok0, kv_end = pos0 + tokens;
     const int32_t* table = p.block_tables + static_cast<size_t>(w.b) * p.max_blocks;
     const int first_key = ja * kChunkKeys, last_key = min(kv_end, jb * kChunkKeys);

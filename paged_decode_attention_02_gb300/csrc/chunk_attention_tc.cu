@@ -45,7 +45,7 @@ constexpr int kThreads = 512;
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;  // 2 x 128 of each: what 512 x 128 give
 constexpr int kCleaners = 4;
 constexpr int kDescs = 4;
-using CutsOf = Cuts<8, 6, 4>;  // 256-row items
+using CutsOf = Cuts<8, 4, 6>;  // 256-row items
 constexpr float kRaise = 8.f;       // the reference maximum moves by at least 2^8
 
 // One piece of work: key tiles [ja, jb) of an item.
@@ -567,28 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e]);
           }
-          if (odd) {  // non-finite V values, for the rows that see them
-            for (int y = 0; y < 128 * 3; ++y) {
-              if (!((d.nonfinite[y >> 7][(y >> 5) & 3] >> (y & 31)) & 1)) continue;
-              const int key = d.jc * kChunkKeys + y;
-              const int id = p.block_tables[d.table + key / p.block_size];
-              if (id < 0 || id >= p.num_blocks) continue;
-              const size_t first =
-                  ((static_cast<size_t>(id) * p.block_size + key % p.block_size) * p.H_kv + d.kh) * D + k;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float f;
-                if (kFp8) {
-                  f = e4m3_to_f32(static_cast<const uint8_t*>(p.v_cache)[first + e]);
-                } else {
-                  const uint16_t u = static_cast<const uint16_t*>(p.v_cache)[first + e];
-                  f = kBf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16)
-                            : __half2float(__ushort_as_half(u));
-                }
-                if (!isfinite(f) && key <= pos) o[e] = fmaf(f, inv, o[e]);
-              }
-            }
-          }
           if (part >= 0) {
             // four columns of a row, rows side by side: a warp writes 512 bytes at a time
             if (write) {
@@ -612,6 +590,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(out + (r & 1) * step1 + (r >> 1) * step2 + k) = v[r];
           }
           __syncwarp();
+        }
+        if (odd && write) {  // non-finite V values, for the rows that see them (__syncwarp: the
+                             // row's values, stored by its quad, are this thread's to change)
+#pragma unroll 1
+          for (int y = 0; y < 128 * 3; ++y) {
+            const int key = d.jc * kChunkKeys + y;
+            if (!((d.nonfinite[y >> 7][(y >> 5) & 3] >> (y & 31)) & 1) || key > pos) continue;
+            const int id = p.block_tables[d.table + key / p.block_size];
+            if (id < 0 || id >= p.num_blocks) continue;
+            const size_t first =
+                ((static_cast<size_t>(id) * p.block_size + key % p.block_size) * p.H_kv + d.kh) * D;
+#pragma unroll 1
+            for (int k = 0; k < D; ++k) {
+              float f;
+              if (kFp8) {
+                f = e4m3_to_f32(static_cast<const uint8_t*>(p.v_cache)[first + k]);
+              } else {
+                const uint16_t u = static_cast<const uint16_t*>(p.v_cache)[first + k];
+                f = kBf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16)
+                          : __half2float(__ushort_as_half(u));
+              }
+              if (isfinite(f)) continue;
+              if (part >= 0) {
+                float* at = reinterpret_cast<float*>(part_o(partial, part, D) + (k / 4) * 256 + packed) + (k & 3);
+                *at = fmaf(f, inv, *at);
+              } else {
+                using Out = std::conditional_t<kBf16, __nv_bfloat16, __half>;
+                Out* at = static_cast<Out*>(p.out) +
+                          ((static_cast<size_t>(d.row0) + tok) * p.H + (d.kh << g_shift) +
+                           (packed & ((1 << g_shift) - 1))) * D + k;
+                *at = static_cast<Out>(fmaf(f, inv, static_cast<float>(*at)));
+              }
+            }
+          }
         }
         if (other) {
           tc_fence_before();
@@ -640,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       w.q.r.n = __shfl_sync(kFullMask, w.q.r.n, 0);
       w.q.r.L = __shfl_sync(kFullMask, w.q.r.L, 0);
       w.q.r.lt = lt;
-      if (u < u_end && u > w.start + w.q.r.tiles(w.i)) next_item(p, lt, &w);
+      if (u < u_end && u >= w.start + w.q.r.tiles(w.i) + kItemUnits) next_item(p, lt, &w);
     }
     __syncwarp();
     fence_proxy_async_smem();  // the plan's shared memory becomes load stages
@@ -649,10 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (u < u_end && !timed_out) {
       const ChunkReq r = w.q.r;
       const int tiles = r.tiles(w.i);
-      const int end = w.start + tiles + 1;
+      const int end = w.start + tiles + kItemUnits;
       const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
-      const int ja = u == w.start ? 0 : u - w.start - 1;
-      const int jb = u_end >= end ? tiles : u_end - w.start - 1;
+      const int ja = u == w.start ? 0 : u - w.start - kItemUnits;
+      const int jb = u_end >= end ? tiles : u_end - w.start - kItemUnits;
       const int slot = item % kDescs;
       Desc& d = ms.desc[slot];
       if (!warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {

@@ -122,7 +122,7 @@ __device__ __forceinline__ Where locate(const ChunkParams& p, const Plan& pl, in
 
 // Moves on to the item behind, of a batch that has one.
 __device__ __forceinline__ void next_item(const ChunkParams& p, int lt, Where* w) {
-  w->start += w->q.r.tiles(w->i) + 1;
+  w->start += w->q.r.tiles(w->i) + kItemUnits;
   if (++w->i < w->q.r.items()) return;
   w->i = 0;
   if (++w->kh < p.H_kv) return;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256)
     // the cut and, on the odd lanes, the one before it
     const int s = cut_of<C>(p, pl, lt, c - (lane & 1), &w);
     const int tiles = w.q.r.tiles(w.i);
-    const int end = w.start + tiles + 1;
+    const int end = w.start + tiles + kItemUnits;
     const int before = __shfl_sync(kFullMask, s, 1);
     if (lane == 0 && s > w.start && s < end && before <= w.start) {
       pieces = 2;  // worker c - 1's, and one for each cut inside the item
@@ -255,7 +255,7 @@ inline int chunk_tiles(const ChunkParams& p) {
 template <typename C>
 long long chunk_units(const ChunkParams& p, int g_shift) {
   const long long items = ((static_cast<long long>(p.T) >> (C::kRowsLog2 - g_shift)) + p.B) * p.H_kv;
-  return items * (chunk_tiles(p) + 1);
+  return items * (chunk_tiles(p) + kItemUnits);
 }
 template <typename C>
 int chunk_grid(const ChunkParams& p, int g_shift, int sms) {

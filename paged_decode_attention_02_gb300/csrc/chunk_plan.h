@@ -3,8 +3,9 @@
 //
 // A request's query rows, G heads of a kv-head times its n new tokens, are cut into items of
 // 2^lt tokens (256 rows on the tensor cores). An item attends to keys [0, p + 1), p the position of its last
-// token, in tiles of 128 keys, and counts as tiles + 1 units (the one for its own start and
-// end). Units are numbered request after request, kv-head after kv-head, item after item, and
+// token, in tiles of 128 keys, and counts as tiles + 4 units: its own start and end, with the
+// masked tiles, cost about four tiles (weighed as one, the busiest block of a batch of short
+// prompts had a quarter more to do than the mean one). Units are numbered request after request, kv-head after kv-head, item after item, and
 // each of the launch's workers takes an equal, contiguous range of them, so the split is even
 // whatever the lengths; an item cut by a range's end is merged afterwards.
 #pragma once
@@ -18,6 +19,7 @@
 namespace pda {
 
 constexpr int kChunkKeys = 128;    // keys of a tile
+constexpr int kItemUnits = 4;      // units of an item besides its tiles
 
 // Units fit 31 bits: the host refuses sizes whose bound on them does not. What only passes
 // through larger values on the way is unsigned, where wrapping cancels.
@@ -47,16 +49,16 @@ struct ChunkReq {
   PDA_CHUNK_HD int units_before(int i) const {
     const int a1 = L - n - 1;  // may be -1: the shifts below round down
     const unsigned m = i;
-    if (lt >= 7) return static_cast<int>(m * ((a1 >> 7) + 2) + (pairs(m + 1) << (lt - 7)));
+    if (lt >= 7) return static_cast<int>(m * ((a1 >> 7) + 1 + kItemUnits) + (pairs(m + 1) << (lt - 7)));
     const int s = 7 - lt;
     const unsigned x0 = (a1 >> lt) + 1;
-    return static_cast<int>(2 * m + floor_sum(x0 + m, s) - floor_sum(x0, s));
+    return static_cast<int>((1 + kItemUnits) * m + floor_sum(x0 + m, s) - floor_sum(x0, s));
   }
   // units of one kv-head
   PDA_CHUNK_HD int units() const {
     if (n == 0) return 0;
     const int last = items() - 1;
-    return units_before(last) + tiles(last) + 1;
+    return units_before(last) + tiles(last) + kItemUnits;
   }
   // the item that holds unit w of a kv-head
   PDA_CHUNK_HD int item_of(int w) const {
@@ -73,12 +75,12 @@ struct ChunkReq {
 };
 
 // Where a cut at unit u of an item that starts at unit `start` really falls: before key tile
-// u - start - 1, or at the item's start or end where that leaves a piece of fewer than
+// u - start - kItemUnits, or at the item's start or end where that leaves a piece of fewer than
 // `least` tiles.
 PDA_CHUNK_HD int chunk_snap(int u, int start, int tiles, int least) {
-  const int j = u - start - 1;
+  const int j = u - start - kItemUnits;
   if (j < least) return start;
-  if (tiles - j < least) return start + tiles + 1;
+  if (tiles - j < least) return start + tiles + kItemUnits;
   return u;
 }
 

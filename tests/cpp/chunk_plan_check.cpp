@@ -31,7 +31,7 @@ int main() {
       const int tiles = (r.L - r.n + last + 127) / 128;
       require(r.tiles(i) == tiles, "tiles", r.n, r.L, r.lt);
       require(r.item_of(sum) == i && r.item_of(sum + tiles) == i, "item_of", r.n, r.L, r.lt);
-      sum += tiles + 1;
+      sum += tiles + kItemUnits;
     }
     require(r.units() == sum, "units", r.n, r.L, r.lt);
   }
@@ -44,7 +44,7 @@ int main() {
     long long sum = 0;
     for (int i = 0; i < r.items() && sum < (1ll << 30); ++i) {
       require(r.units_before(i) == sum, "long", r.n, r.L, r.lt);
-      sum += r.tiles(i) + 1;
+      sum += r.tiles(i) + kItemUnits;
     }
   }
   for (int it = 0; it < 300; ++it) {
@@ -62,7 +62,7 @@ int main() {
         for (int i = 0; i < r.items(); ++i) {
           start.push_back(W);
           tiles.push_back(r.tiles(i));
-          W += r.tiles(i) + 1;
+          W += r.tiles(i) + kItemUnits;
         }
     }
     const int workers = chunk_workers(W, 1 + rnd(152), 1 + rnd(8));
@@ -81,11 +81,11 @@ int main() {
       require(s0 <= s1, "order", B, H_kv, lt);
       int inside = 0;
       for (size_t i = 0; i < start.size(); ++i) {
-        const long long end = start[i] + tiles[i] + 1;
+        const long long end = start[i] + tiles[i] + kItemUnits;
         const long long a = s0 > start[i] ? s0 : start[i], b = s1 < end ? s1 : end;
         if (a >= b) continue;
-        const int ja = a == start[i] ? 0 : static_cast<int>(a - start[i] - 1);
-        const int jb = b == end ? tiles[i] : static_cast<int>(b - start[i] - 1);
+        const int ja = a == start[i] ? 0 : static_cast<int>(a - start[i] - kItemUnits);
+        const int jb = b == end ? tiles[i] : static_cast<int>(b - start[i] - kItemUnits);
         require(jb > ja, "empty piece", B, H_kv, lt);
         if (jb - ja < tiles[i]) require(jb - ja >= least || workers > W / least, "short piece", jb - ja, least, lt);
         inside += ja > 0;
