@@ -16,8 +16,11 @@
 //   11        writes the rows of requests without work
 //   12-15     clean the V tiles at the diagonal and the end (see below), or, over an FP8
 //             cache, widen every K and V tile: the TMA brings the codes, these warps write
-//             them as bf16 (exact: an E4M3 code has 4 significant bits) where the products
-//             read them
+//             them as fp16 (exact, and one instruction for two codes, where bf16 took four:
+//             370 -> FP8NEW us on three chunks of up to 2048 tokens) where the products read
+//             them. The softmax warps then bring Q, each row scaled by a power of two that
+//             puts its largest value at 2^14: what falls under fp16's smallest step is below
+//             2^-39 of that value.
 // The softmax warps take the registers that the others give back (setmaxnreg).
 // An item of more than 128 rows gives each group 128 rows; both read every K and V tile. An
 // item of fewer gives both groups the same rows and alternate tiles, merged at the end, so
@@ -100,7 +103,8 @@ __device__ __forceinline__ void tma_box4(void* dst, const CUtensorMap* tm, int c
 struct Misc {
   uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5], clean[5];
   uint64_t raw_full[2], raw_empty[2];  // codes of a K and of a V tile
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], merge_ready, merge_done, done;
+  uint64_t q_full, q_full1, q_empty,  // q_full1: group 1's, where the softmax warps bring Q
+           s_full[2], p_full[2], o_full[2], merge_ready, merge_done, done;
   uint64_t desc_full[kDescs], desc_empty[kDescs];
   Desc desc[kDescs];
   float2 ml[128];
@@ -201,7 +205,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Widens this warp's quarter of a tile of E4M3 codes, [128][D] bytes, to bf16 in the products'
+// Widens this warp's quarter of a tile of E4M3 codes, [128][D] bytes, to fp16 in the products'
 // layout (64-element halves, 128-byte swizzle). Rows from `keys` on become zeros. Where
 // `nonfinite` is given, NaN codes become zeros and their rows' bits are set there.
 template <int D>
@@ -228,12 +232,7 @@ __device__ __forceinline__ void widen(unsigned char* dst, const unsigned char* c
     uint4 o[2];
     uint32_t* u = &o[0].x;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float f[4];
-      e4m3x4_to_f32(w[k], f);
-      u[2 * k] = pack2<true>(f[0], f[1]);
-      u[2 * k + 1] = pack2<true>(f[2], f[3]);
-    }
+    for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2(w[k], u[2 * k], u[2 * k + 1]);
     // lanes of the second half take their pieces the other way round: no bank conflicts
     const bool swap = c >= 8;
 #pragma unroll
@@ -243,6 +242,37 @@ __device__ __forceinline__ void widen(unsigned char* dst, const unsigned char* c
                                 (((piece & 7) ^ (r & 7)) << 4)) = swap == (k == 0) ? o[1] : o[0];
     }
   }
+}
+
+// One row of Q, D bf16 values, into row r of a tile in the products' layout as fp16, scaled by a
+// power of two that puts its largest value into [2^14, 2^15). Returns the factor that undoes it.
+// `store`: false only finds the factor.
+template <int D>
+__device__ __forceinline__ float scale_q_row(const uint4* row, unsigned char* tile, int r, bool store) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 v = row[c];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
+  }
+  // the largest value's exponent field; 15 keeps the factor's own exponent in range
+  const int e = max(static_cast<int>(top >> 7), 15);
+  const float up = __uint_as_float(static_cast<uint32_t>(min(268 - e, 253)) << 23);
+  if (store) {
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 v = row[c];
+      const uint4 o = make_uint4(pack2<false>(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
+                                 pack2<false>(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                                 pack2<false>(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
+                                 pack2<false>(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+      *reinterpret_cast<uint4*>(tile + (c >> 3) * (kChunkKeys * 128) + r * 128 +
+                                (((c & 7) ^ (r & 7)) << 4)) = o;
+    }
+  }
+  return 1.f / up;
 }
 
 // Cleans this warp's quarter of a V tile of `keys` rows, in boxes of `box_rows` rows: zeroes what
@@ -330,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const ChunkParams p, int g_shift,
                     float* partial) {
-  static_assert(kBf16 || !kFp8, "codes are widened to bf16");
+  static_assert(kBf16 || !kFp8, "q and out are bf16 over a cache of codes");
+  constexpr bool kOpBf16 = kBf16 && !kFp8;  // the products' operands
   using C = Cfg<D, kFp8>;
   constexpr int NK = C::kK, NV = C::kV;
   extern __shared__ unsigned char smem_raw[];
@@ -358,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ms.raw_full[i], 1);
       mbar_init(&ms.raw_empty[i], kCleaners);
     }
-    mbar_init(&ms.q_full, 1);
+    mbar_init(&ms.q_full, kFp8 ? 4 : 1);  // a group's softmax warps, or the copy
+    mbar_init(&ms.q_full1, 4);
     mbar_init(&ms.q_empty, 1);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&ms.s_full[g], 1);
@@ -397,10 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4) << 16
     const uint32_t tS = tmem + lanes + g * 128, tO = tmem + lanes + 256 + g * 128;
-    const float sl = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    const float sl_all = fmaxf(fabsf(p.scale_log2), 1e-30f);
     // fp16 probabilities are kept 2^4 higher (the factor cancels in O / l): with the
     // reference up to 2^8 below the maximum they stay below 2^13, and fewer are subnormal
-    const float lift = kBf16 ? 0.f : 4.f;
+    const float lift = kOpBf16 ? 0.f : 4.f;
     unsigned s_phase = 0, o_phase = 0, m_phase = 0;
     for (int item = 0; !timed_out; ++item) {
       const int slot = item % kDescs;
@@ -418,6 +450,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = packed >> g_shift;
       const int pos = d.pos0 + min(tok, d.tokens - 1);  // this row's position
       const int first_pos = d.pos0 + ((single ? 0 : g * 128) >> g_shift);
+      float sl = sl_all;  // of a score, in log2 units
+      if (kFp8) {
+        // this row of Q; where the groups share their rows, group 0's warps store it
+        if (!warp_wait(&ms.q_empty, (item & 1) ^ 1)) {
+          timed_out = true;
+          break;
+        }
+        const int there = min(tok, d.tokens - 1);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q) +
+            ((static_cast<size_t>(d.row0) + there) * p.H + (d.kh << g_shift) +
+             (packed & ((1 << g_shift) - 1))) * D);
+        // (not 0: masked scores are -inf times this)
+        sl = fmaxf(1e-37f, sl * scale_q_row<D>(src, qs + (single ? 0 : g * C::kTile), row,
+                                               g == 0 || !single));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(g == 0 ? &ms.q_full : &ms.q_full1);
+      }
       float m = -INFINITY, l = 0.f;
       for (int s = 0; s < steps; ++s) {
         if (!warp_wait(&ms.s_full[g], s_phase)) {
@@ -480,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.x = ex2(a.x);
             a.y = ex2(a.y);
             sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], a);
-            pk[e / 2] = pack2<kBf16>(a.x, a.y);
+            pk[e / 2] = pack2<kOpBf16>(a.x, a.y);
           }
           tmem_st16(tS + k / 2, pk);
         }
@@ -697,18 +748,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&ms.desc_full[slot]);
       }
       __syncwarp();
-      // Q
-      if (!warp_wait(&ms.q_empty, (item & 1) ^ 1)) {
-        timed_out = true;
-        break;
-      }
-      const int q_tiles = single ? 1 : 2;
-      if (lane == 0) mbar_arrive_expect_tx(&ms.q_full, q_tiles * C::kTile);
-      __syncwarp();
-      if (lane < q_tiles * C::kHalves) {
-        const int g = lane / C::kHalves, h = lane % C::kHalves;
-        tma_box(qs + g * C::kTile + h * C::kHalf, &tm_q, 64 * h, w.kh << g_shift,
-                row0 + g * half, &ms.q_full);
+      // Q (over codes the softmax warps bring it)
+      if (!kFp8) {
+        if (!warp_wait(&ms.q_empty, (item & 1) ^ 1)) {
+          timed_out = true;
+          break;
+        }
+        const int q_tiles = single ? 1 : 2;
+        if (lane == 0) mbar_arrive_expect_tx(&ms.q_full, q_tiles * C::kTile);
+        __syncwarp();
+        if (lane < q_tiles * C::kHalves) {
+          const int g = lane / C::kHalves, h = lane % C::kHalves;
+          tma_box(qs + g * C::kTile + h * C::kHalf, &tm_q, 64 * h, w.kh << g_shift,
+                  row0 + g * half, &ms.q_full);
+        }
       }
       // K: a box of a block's rows (128 at most), for each 64-element half of a row, or of codes
       const int nt = jb - ja;
@@ -759,8 +812,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int st = 0; st < (kFp8 ? 1 : 5); ++st)
         for (int turn = 0; turn < 2; ++turn)
           warp_wait(kFp8 ? &ms.raw_full[0] : &ms.k_full[st], turn);
-      warp_wait(&ms.q_full, 0);
-      warp_wait(&ms.q_full, 1);
+      if (!kFp8) {
+        warp_wait(&ms.q_full, 0);
+        warp_wait(&ms.q_full, 1);
+      }
     }
   } else if (warp == 9) {
     // ================================================================ matrix instructions
@@ -768,8 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // elected lane issues.
     const bool leader = elect_one();
     const bool negate = p.scale_log2 < 0.f;  // S is compared and scaled by |scale|
-    const uint32_t id_qk = mma_idesc(kBf16, kChunkKeys, negate, false);
-    const uint32_t id_pv = mma_idesc(kBf16, D, false, true);
+    const uint32_t id_qk = mma_idesc(kOpBf16, kChunkKeys, negate, false);
+    const uint32_t id_pv = mma_idesc(kOpBf16, D, false, true);
     // descriptors as (address, rest) words: moving along a tile changes the address alone
     const uint64_t dk = smem_desc_sw128(smem_addr(ks), 16, 1024), dq = smem_desc_sw128(smem_addr(qs), 16, 1024);
     const uint32_t dk0 = static_cast<uint32_t>(dk), dq0 = static_cast<uint32_t>(dq);
@@ -867,6 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (ok) qk(0, 0);
       }
+      if (kFp8 && ok) ok = warp_wait(&ms.q_full1, item & 1);
       if (ok && n1 > 0) {
         ok = warp_wait(&ms.k_full[k_at], k_turn);
         tc_fence_after();
