@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(256, 1)
             make_float4(sc[0][b], sc[1][b], sc[2][b], sc[3][b]);
       __syncwarp();  // a warp reads back its own rows only
       const int keys = min(kKeys, last_key - key0);
-      for (int j = 0; j < keys; ++j) {
+      auto accumulate = [&](int j, bool masked) {
         const float4 pr = *reinterpret_cast<const float4*>(&sm.p[j][4 * y]);
         const float pa[4] = {pr.x, pr.y, pr.z, pr.w};
 #pragma unroll
@@ -205,13 +205,19 @@ __global__ void __launch_bounds__(256, 1)
           const float4 v = *reinterpret_cast<const float4*>(&sm.v[buf][j][16 * e + 4 * x]);
 #pragma unroll
           for (int a = 0; a < 4; ++a) {
-            if (edge && key0 + j > pos[a]) continue;
+            if (masked && key0 + j > pos[a]) continue;
             o[a][e] = fmaf(pa[a], v.x, o[a][e]);
             o[a][e + 1] = fmaf(pa[a], v.y, o[a][e + 1]);
             o[a][e + 2] = fmaf(pa[a], v.z, o[a][e + 2]);
             o[a][e + 3] = fmaf(pa[a], v.w, o[a][e + 3]);
           }
         }
+      };
+      if (edge || keys < kKeys) {
+        for (int j = 0; j < keys; ++j) accumulate(j, true);
+      } else {
+#pragma unroll 8
+        for (int j = 0; j < kKeys; ++j) accumulate(j, false);
       }
       __syncthreads();  // the step's buffers are free
     }

@@ -17,7 +17,7 @@
 //   12-15     clean the V tiles at the diagonal and the end (see below), or, over an FP8
 //             cache, widen every K and V tile: the TMA brings the codes, these warps write
 //             them as fp16 (exact, and one instruction for two codes, where bf16 took four:
-//             370 -> FP8NEW us on three chunks of up to 2048 tokens) where the products read
+//             365 -> 341 us on three chunks of up to 2048 tokens) where the products read
 //             them. The softmax warps then bring Q, each row scaled by a power of two that
 //             puts its largest value at 2^14: what falls under fp16's smallest step is below
 //             2^-39 of that value.
@@ -917,12 +917,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       bool ok = true;
-      if (n0 > 0) {
+      // group 1's warps bring their Q at their own pace; an item without steps of theirs waits
+      // for them all the same, so that they see every turn of q_empty
+      if (kFp8 && n1 == 0) ok = warp_wait(&ms.q_full1, item & 1);
+      if (ok && n0 > 0) {
         ok = warp_wait(&ms.k_full[k_at], k_turn);
         tc_fence_after();
         if (ok) qk(0, 0);
       }
-      if (kFp8 && ok) ok = warp_wait(&ms.q_full1, item & 1);
+      if (kFp8 && ok && n1 > 0) ok = warp_wait(&ms.q_full1, item & 1);
       if (ok && n1 > 0) {
         ok = warp_wait(&ms.k_full[k_at], k_turn);
         tc_fence_after();

@@ -57,6 +57,18 @@ def test_sm_cap(kv, sm_cap):
 
 
 @pytest.mark.parametrize("kv", ["f32", "bf16", "f16", "fp8"])
+@pytest.mark.parametrize("sm_cap", [1, 3])
+def test_many_short_items_in_one_block(kv, sm_cap):
+    """One-tile, two-tile and two-group items behind each other, hundreds to a block: every
+    buffer and barrier of the pipeline turns over at item borders."""
+    rng = np.random.RandomState(7)
+    n = rng.choice([1, 1, 2, 3, 40, 70], 150)
+    past = rng.choice([0, 3, 100, 126, 127, 128, 250, 400], 150)
+    c = Chunk(n, past, kv, H=8, H_kv=4, seed=11)
+    c.assert_close(c.call(sm_cap=sm_cap))
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16", "f16", "fp8"])
 def test_repeatable_and_workspace_content_means_nothing(kv):
     c = Chunk([1, 70, 300, 1, 9, 2], [5000, 100, 900, 64, 777, 3333], kv, seed=5)
     ws = pda.alloc_chunk_workspace(c.B, c.T, c.H, c.H_kv, c.D, c.bs, c.k.dtype)
