@@ -565,7 +565,8 @@ pda_status pda_chunk_attention_workspace_size(int B, int T, int H, int H_kv, int
  *                 256-byte aligned, not shared by calls that may run concurrently; its
  *                 content before and after a call means nothing.
  *  The other arguments, the supported sizes (D, block_size, H / H_kv, B) and alignment are
- *  those of pda_paged_decode_attention; T * H < 2^31, and (T / t + B) * H_kv *
+ *  those of pda_paged_decode_attention; T * H < 2^31, the smaller of max_context_len and
+ *  max_blocks_per_seq * block_size at most 2^30, and (T / t + B) * H_kv *
  *  (max_context_len / 128 + 5) < 2^31 with t = 256 * H_kv / H tokens (fp32: 64 * H_kv / H).
  */
 pda_status pda_paged_chunk_attention(void* out, const void* q, const void* k_cache,

@@ -64,7 +64,9 @@ pda_status launch_chunk(void* out, const void* q, const void* k_cache, const voi
                       v_scale, B,      T,         H,
                       H_kv,    H / H_kv, max_blocks_per_seq, max_context_len,
                       block_size, num_blocks};
-  // the kernels number their work, items by key tiles, in 31 bits
+  // the kernels number keys in 31 bits with a tile to spare, and their work, items by key
+  // tiles, in 31 bits
+  if (chunk_tiles(p) > (1 << 23)) return PDA_ERR_UNSUPPORTED;
   int g_shift = 0;
   while ((1 << g_shift) < p.G) ++g_shift;
   const long long units = kv_dtype == PDA_F32 ? chunk_units<Cuts<6, 1, 1>>(p, g_shift)

@@ -429,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4) << 16
     const uint32_t tS = tmem + lanes + g * 128, tO = tmem + lanes + 256 + g * 128;
-    const float sl_all = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    // never 0: masked scores are -inf times this
+    const float least = __uint_as_float(1), sl_all = fmaxf(fabsf(p.scale_log2), least);
     // fp16 probabilities are kept 2^4 higher (the factor cancels in O / l): with the
     // reference up to 2^8 below the maximum they stay below 2^13, and fewer are subnormal
     const float lift = kOpBf16 ? 0.f : 4.f;
@@ -462,9 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             static_cast<const uint16_t*>(p.q) +
             ((static_cast<size_t>(d.row0) + there) * p.H + (d.kh << g_shift) +
              (packed & ((1 << g_shift) - 1))) * D);
-        // (not 0: masked scores are -inf times this)
-        sl = fmaxf(1e-37f, sl * scale_q_row<D>(src, qs + (single ? 0 : g * C::kTile), row,
-                                               g == 0 || !single));
+        sl = fmaxf(least, sl * scale_q_row<D>(src, qs + (single ? 0 : g * C::kTile), row,
+                                              g == 0 || !single));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(g == 0 ? &ms.q_full : &ms.q_full1);

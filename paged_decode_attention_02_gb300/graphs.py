@@ -54,6 +54,8 @@ class DecodeStepGraphs:
         self.lens = torch.zeros((n,), dtype=torch.int32, device=dev)
         self.out = torch.zeros((n, H, D), dtype=self.dtype, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.ones = torch.ones((n,), dtype=torch.int32, device=dev)
+        self.starts = torch.zeros((n + 1,), dtype=torch.int32, device=dev)
         self.side = torch.cuda.Stream(dev)
         self.ws = {}
         self.graphs = {}
@@ -128,7 +130,8 @@ class DecodeStepGraphs:
 
     def stage(self, local: dict, remote: dict):
         """Copies one step's inputs into the rows of the smallest fitting bucket and pads the
-        rest as empty; returns the bucket. In a model, the tables, lengths and slots change
+        rest as empty; returns the bucket. Without a ``slot_mapping`` the slots are built on
+        the GPU from the tables and the lengths. In a model, the tables, lengths and slots change
         once per step, while each layer's q and new K/V would be written straight into
         ``self.q``, ``self.k_new`` and ``self.v_new`` by the layer before."""
         n_l = local["q"].shape[0] if local else 0
@@ -145,10 +148,16 @@ class DecodeStepGraphs:
             self.q[start:start + n].copy_(part["q"], non_blocking=True)
             self.k_new[start:start + n].copy_(part["k_new"], non_blocking=True)
             self.v_new[start:start + n].copy_(part["v_new"], non_blocking=True)
-            self.slots[start:start + n].copy_(part["slot_mapping"], non_blocking=True)
             t = part["block_tables"]
             self.tables[start:start + n, :t.shape[1]].copy_(t, non_blocking=True)
             self.lens[start:start + n].copy_(part["context_lens"], non_blocking=True)
+            if part.get("slot_mapping") is not None:
+                self.slots[start:start + n].copy_(part["slot_mapping"], non_blocking=True)
+            else:  # each row's new token is its last; padded rows have length 0 and get -1
+                binding.kv_build_slots(self.slots[start:start + nb], self.starts[:nb + 1],
+                                       self.ones[:nb], self.lens[start:start + nb],
+                                       self.tables[start:start + nb], self.bs,
+                                       self.k_cache.shape[0], error_word=self.err)
         return bl, br
 
     def replay(self, bucket):

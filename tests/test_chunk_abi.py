@@ -42,6 +42,8 @@ COMMON = [(dict(H=5), INVALID), (dict(H=0), INVALID), (dict(H_kv=0), INVALID),
           (dict(B=9000), UNSUPPORTED), (dict(qd=0), UNSUPPORTED),
           (dict(NB=1 << 28), UNSUPPORTED), (dict(T=1 << 29), UNSUPPORTED),
           (dict(mb=1 << 30), UNSUPPORTED),
+          (dict(mb=1 << 27, max_ctx=(1 << 30) + 1, B=1), UNSUPPORTED),  # keys past 2^30
+          (dict(mb=1 << 16, max_ctx=1 << 20, T=1 << 22, H=64, H_kv=64), UNSUPPORTED),  # work past 2^31
           (dict(ws=None), binding.PDA_ERR_WORKSPACE),
           (dict(ws=ctypes.c_void_p((1 << 20) + 16)), binding.PDA_ERR_WORKSPACE)]
 COMMON += [({x: None}, INVALID) for x in "out q k v bt cl qs".split()]

@@ -245,3 +245,25 @@ def test_slots_empty_batch():
     slots, start = i32(np.zeros(5)), i32([9])
     pda.kv_build_slots(slots, start, z, z, e, 16, 8)
     assert (slots == -1).all() and start.tolist() == [0]
+
+
+def test_graph_steps_build_their_own_slots():
+    """A captured decode step staged without a slot mapping writes and reads what one staged
+    with it does."""
+    from paged_decode_attention_02_gb300 import graphs as pg
+    from paged_decode_attention_02_gb300 import workloads as wl
+    got = []
+    for with_slots in (True, False):
+        s = wl.make_step("sm_sweep_b128", device="cuda", B=7)
+        g = pg.DecodeStepGraphs(s.k_cache, s.v_cache, s.w.H, s.max_blocks, max_local=8, max_remote=8,
+                                interval=8, scale=s.scale, remote_sm_cap=40).capture()
+
+        def part(sel):
+            p = {"q": s.q[sel], "k_new": s.k_new[sel], "v_new": s.v_new[sel],
+                 "block_tables": s.block_tables[sel], "context_lens": s.context_lens[sel]}
+            return dict(p, slot_mapping=s.slot_mapping[sel]) if with_slots else p
+
+        out = [x.clone() for x in g.run(part(slice(0, 5)), part(slice(5, 7)))]
+        pda.check_error(g.err)
+        got.append(out + [s.k_cache, s.v_cache])
+    assert all(torch.equal(a, b) for a, b in zip(*got))

@@ -49,6 +49,25 @@ def test_large_scores(kv):
     assert ((out - ref).abs() <= u * (mag + ref.abs()) + 5e-4 * mag + 1e-30).all()
 
 
+@pytest.mark.parametrize("kv", ["f32", "bf16", "f16", "fp8"])
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 1e-3])
+def test_any_finite_scale(kv, scale):
+    """A negative scale turns the order of the scores; zero makes every visible key equal."""
+    c = Chunk([150, 1, 3], [40, 700, 3000], kv, H=4, H_kv=2, seed=13)
+    c.scale = scale
+    c.assert_close(c.call())
+
+
+@pytest.mark.parametrize("exponent", [-120, -40, 60, 100])
+def test_fp8_takes_q_of_any_magnitude(exponent):
+    """Rows of q far outside fp16's range, each with its own exponent, at a scale that brings
+    the scores back (q K^T stays far below fp32's largest value)."""
+    c = Chunk([150, 2], [40, 700], "fp8", H=4, H_kv=2, seed=14)
+    c.q = (c.q.double() * 2.0 ** exponent).to(torch.bfloat16)
+    c.scale = float(np.float32(c.scale * 2.0 ** -exponent)) if exponent > -100 else 2.0 ** 100
+    c.assert_close(c.call())
+
+
 @pytest.mark.parametrize("sm_cap", [1, 7, 151])
 @pytest.mark.parametrize("kv", ["f32", "bf16", "fp8"])
 def test_sm_cap(kv, sm_cap):
