@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(256, 1)
       u_end = __shfl_sync(kFullMask, u, 1);
       u = __shfl_sync(kFullMask, u, 0);
       // lane 0's item is the block's; the others' are not
-      if (lane == 0 && u < u_end && u >= w.start + w.q.r.tiles(w.i) + kItemUnits) next_item(p, lt, &w);
+      if (lane == 0 && u < u_end && u >= w.start + w.q.r.tiles(w.i) + kItemUnits)
+        next_item(p, lt, &w);
     }
     if (lane == 0) {
       sm.first = w;
@@ -229,7 +230,8 @@ __global__ void __launch_bounds__(256, 1)
       for (int i = 0; i < 8; ++i) bad_from = min(bad_from, all[i]);
       __syncthreads();
     }
-    const int part = ja == 0 && jb == tiles ? -1 : static_cast<int>(blockIdx.x) * 2 + (ja == 0 ? 1 : 0);
+    const int part =
+        ja == 0 && jb == tiles ? -1 : static_cast<int>(blockIdx.x) * 2 + (ja == 0 ? 1 : 0);
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
 #pragma unroll

@@ -174,7 +174,8 @@ struct BlockIds {
       if (bad_from != nullptr) {
         bool used;
         const int blk = block_of(group, &used);
-        atomicMin(bad_from, max(blk * bs, (ja + group * per_group + (threadIdx.x & 31) / nbt) * kChunkKeys));
+        const int tile = ja + group * per_group + (threadIdx.x & 31) / nbt;
+        atomicMin(bad_from, max(blk * bs, tile * kChunkKeys));
         atomic_or_error(error_word, PDA_DEVERR_BLOCK_ID);
         __threadfence_block();
       }
@@ -248,7 +249,8 @@ __device__ __forceinline__ void widen(unsigned char* dst, const unsigned char* c
 // power of two that puts its largest value into [2^14, 2^15). Returns the factor that undoes it.
 // `store`: false only finds the factor.
 template <int D>
-__device__ __forceinline__ float scale_q_row(const uint4* row, unsigned char* tile, int r, bool store) {
+__device__ __forceinline__ float scale_q_row(const uint4* row, unsigned char* tile, int r,
+                                             bool store) {
   uint32_t top = 0;
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
@@ -591,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rows of this lane's quad: the first one's place in the output, the steps to the other
         // three, and how many of them are the item's
         const int quad = packed & ~3, HD = p.H * D;
-        const int step1 = g_shift == 0 ? HD : D, step2 = g_shift == 0 ? 2 * HD : g_shift == 1 ? HD : 2 * D;
+        const int step1 = g_shift == 0 ? HD : D;
+        const int step2 = g_shift == 0 ? 2 * HD : g_shift == 1 ? HD : 2 * D;
         const int in_quad = (d.tokens << g_shift) - quad;
         uint16_t* out = static_cast<uint16_t*>(p.out) +
                         (static_cast<size_t>(d.row0 + (quad >> g_shift)) * p.H + (d.kh << g_shift) +
@@ -632,8 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 v[4];
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
-              v[e / 8] = make_uint4(pack2<kBf16>(o[e], o[e + 1]), pack2<kBf16>(o[e + 2], o[e + 3]),
-                                    pack2<kBf16>(o[e + 4], o[e + 5]), pack2<kBf16>(o[e + 6], o[e + 7]));
+              v[e / 8] =
+                  make_uint4(pack2<kBf16>(o[e], o[e + 1]), pack2<kBf16>(o[e + 2], o[e + 3]),
+                             pack2<kBf16>(o[e + 4], o[e + 5]), pack2<kBf16>(o[e + 6], o[e + 7]));
             quad_transpose(v);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -664,7 +668,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (isfinite(f)) continue;
               if (part >= 0) {
-                float* at = reinterpret_cast<float*>(part_o(partial, part, D) + (k / 4) * 256 + packed) + (k & 3);
+                float* at =
+                    reinterpret_cast<float*>(part_o(partial, part, D) + (k / 4) * 256 + packed) +
+                    (k & 3);
                 *at = fmaf(f, inv, *at);
               } else {
                 using Out = std::conditional_t<kBf16, __nv_bfloat16, __half>;
@@ -686,399 +692,409 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     reg_dec<kOtherRegs>();
-  if (warp == 8) {
-    // ================================================================ plan, load Q and K
-    Where w{};
-    int u = 0, u_end = 0;
-    if (static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0) {
-      // both ends of the range at once: the odd lanes find the upper one
-      u = cut_of<CutsOf>(p, pl, lt, blockIdx.x + (lane & 1), &w);
-      u_end = __shfl_sync(kFullMask, u, 1);
-      u = __shfl_sync(kFullMask, u, 0);
-      w.b = __shfl_sync(kFullMask, w.b, 0);
-      w.kh = __shfl_sync(kFullMask, w.kh, 0);
-      w.i = __shfl_sync(kFullMask, w.i, 0);
-      w.start = __shfl_sync(kFullMask, w.start, 0);
-      w.q.row0 = __shfl_sync(kFullMask, w.q.row0, 0);
-      w.q.r.n = __shfl_sync(kFullMask, w.q.r.n, 0);
-      w.q.r.L = __shfl_sync(kFullMask, w.q.r.L, 0);
-      w.q.r.lt = lt;
-      if (u < u_end && u >= w.start + w.q.r.tiles(w.i) + kItemUnits) next_item(p, lt, &w);
-    }
-    __syncwarp();
-    fence_proxy_async_smem();  // the plan's shared memory becomes load stages
-    int item = 0;
-    int k_at = 0, k_turn = 0;
-    while (u < u_end && !timed_out) {
-      const ChunkReq r = w.q.r;
-      const int tiles = r.tiles(w.i);
-      const int end = w.start + tiles + kItemUnits;
-      const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
-      const int ja = u == w.start ? 0 : u - w.start - kItemUnits;
-      const int jb = u_end >= end ? tiles : u_end - w.start - kItemUnits;
-      const int slot = item % kDescs;
-      Desc& d = ms.desc[slot];
-      if (!warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
-        timed_out = true;
-        break;
-      }
-      const int pos0 = r.L - r.n + tok0;
-      const int half = 128 >> g_shift;  // tokens of a row group
-      const bool single = tokens <= half;
-      const int kv_end = pos0 + tokens;
-      const long long table = static_cast<long long>(w.b) * p.max_blocks;
-      const int row0 = w.q.row0 + tok0;
-      if (lane == 0) {
-        d.valid = 1;
-        d.row0 = row0;
-        d.tokens = tokens;
-        d.pos0 = pos0;
-        d.kh = w.kh;
-        d.ja = ja;
-        d.jb = jb;
-        d.tiles0 = single ? tiles : ((pos0 + half - 1) >> 7) + 1;
-        d.tiles1 = tiles;
-        d.single = single;
-        d.jc = (pos0 + 1) >> 7;
-        d.end = kv_end;
-        d.slot = ja == 0 && jb == tiles ? -1 : static_cast<int>(blockIdx.x) * 2 + (ja == 0 ? 1 : 0);
-        d.bad_from = 0x7fffffff;
-        d.table = table;
-        for (int k = 0; k < 12; ++k) d.nonfinite[k >> 2][k & 3] = 0;
-        mbar_arrive(&ms.desc_full[slot]);
+    if (warp == 8) {
+      // ================================================================ plan, load Q and K
+      Where w{};
+      int u = 0, u_end = 0;
+      if (static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0) {
+        // both ends of the range at once: the odd lanes find the upper one
+        u = cut_of<CutsOf>(p, pl, lt, blockIdx.x + (lane & 1), &w);
+        u_end = __shfl_sync(kFullMask, u, 1);
+        u = __shfl_sync(kFullMask, u, 0);
+        w.b = __shfl_sync(kFullMask, w.b, 0);
+        w.kh = __shfl_sync(kFullMask, w.kh, 0);
+        w.i = __shfl_sync(kFullMask, w.i, 0);
+        w.start = __shfl_sync(kFullMask, w.start, 0);
+        w.q.row0 = __shfl_sync(kFullMask, w.q.row0, 0);
+        w.q.r.n = __shfl_sync(kFullMask, w.q.r.n, 0);
+        w.q.r.L = __shfl_sync(kFullMask, w.q.r.L, 0);
+        w.q.r.lt = lt;
+        if (u < u_end && u >= w.start + w.q.r.tiles(w.i) + kItemUnits) next_item(p, lt, &w);
       }
       __syncwarp();
-      // Q (over codes the softmax warps bring it)
-      if (!kFp8) {
-        if (!warp_wait(&ms.q_empty, (item & 1) ^ 1)) {
+      fence_proxy_async_smem();  // the plan's shared memory becomes load stages
+      int item = 0;
+      int k_at = 0, k_turn = 0;
+      while (u < u_end && !timed_out) {
+        const ChunkReq r = w.q.r;
+        const int tiles = r.tiles(w.i);
+        const int end = w.start + tiles + kItemUnits;
+        const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
+        const int ja = u == w.start ? 0 : u - w.start - kItemUnits;
+        const int jb = u_end >= end ? tiles : u_end - w.start - kItemUnits;
+        const int slot = item % kDescs;
+        Desc& d = ms.desc[slot];
+        if (!warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
           timed_out = true;
           break;
         }
-        const int q_tiles = single ? 1 : 2;
-        if (lane == 0) mbar_arrive_expect_tx(&ms.q_full, q_tiles * C::kTile);
-        __syncwarp();
-        if (lane < q_tiles * C::kHalves) {
-          const int g = lane / C::kHalves, h = lane % C::kHalves;
-          tma_box(qs + g * C::kTile + h * C::kHalf, &tm_q, 64 * h, w.kh << g_shift,
-                  row0 + g * half, &ms.q_full);
-        }
-      }
-      // K: a box of a block's rows (128 at most), for each 64-element half of a row, or of codes
-      const int nt = jb - ja;
-      const int box_rows = min(p.block_size, kChunkKeys);
-      BlockIds ids;
-      ids.start(p, d);
-      for (int t = 0; t < nt; ++t) {
-        ids.advance(t, &d.bad_from, p.error_word);
-        uint64_t* full = kFp8 ? &ms.raw_full[0] : &ms.k_full[k_at];
-        if (!warp_wait(kFp8 ? &ms.raw_empty[0] : &ms.k_empty[k_at], k_turn ^ 1)) {
-          timed_out = true;
-          break;
-        }
-        const int boxes = min(ids.nbt, (kv_end - (ja + t) * kChunkKeys + box_rows - 1) / box_rows);
-        if (lane == 0)
-          mbar_arrive_expect_tx(full, boxes * box_rows * (kFp8 ? D : 2 * D));
-        __syncwarp();
-        constexpr int kParts = kFp8 ? 1 : C::kHalves;
-        const int blk = lane / kParts, h = lane % kParts;
-        const int row = ids.row(t, blk);
-        if (blk < boxes)
-          tma_box(kFp8 ? raw + blk * box_rows * D
-                       : ks + k_at * C::kTile + h * C::kHalf + blk * box_rows * 128,
-                  &tm_k, 64 * h, w.kh, row, full);
-        if (++k_at == (kFp8 ? 1 : NK)) {
-          k_at = 0;
-          k_turn ^= 1;
-        }
-      }
-      ++item;
-      // the next item
-      u = end;
-      if (u < u_end) next_item(p, lt, &w);
-    }
-    if (!timed_out) {
-      const int slot = item % kDescs;
-      if (warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
+        const int pos0 = r.L - r.n + tok0;
+        const int half = 128 >> g_shift;  // tokens of a row group
+        const bool single = tokens <= half;
+        const int kv_end = pos0 + tokens;
+        const long long table = static_cast<long long>(w.b) * p.max_blocks;
+        const int row0 = w.q.row0 + tok0;
         if (lane == 0) {
-          ms.desc[slot].valid = 0;
+          d.valid = 1;
+          d.row0 = row0;
+          d.tokens = tokens;
+          d.pos0 = pos0;
+          d.kh = w.kh;
+          d.ja = ja;
+          d.jb = jb;
+          d.tiles0 = single ? tiles : ((pos0 + half - 1) >> 7) + 1;
+          d.tiles1 = tiles;
+          d.single = single;
+          d.jc = (pos0 + 1) >> 7;
+          d.end = kv_end;
+          d.slot =
+              ja == 0 && jb == tiles ? -1 : static_cast<int>(blockIdx.x) * 2 + (ja == 0 ? 1 : 0);
+          d.bad_from = 0x7fffffff;
+          d.table = table;
+          for (int k = 0; k < 12; ++k) d.nonfinite[k >> 2][k & 3] = 0;
           mbar_arrive(&ms.desc_full[slot]);
         }
-      } else {
-        timed_out = true;
-      }
-    }
-    if (timed_out) {
-      // copies in flight land before the block may leave
-      for (int st = 0; st < (kFp8 ? 1 : 5); ++st)
-        for (int turn = 0; turn < 2; ++turn)
-          warp_wait(kFp8 ? &ms.raw_full[0] : &ms.k_full[st], turn);
-      if (!kFp8) {
-        warp_wait(&ms.q_full, 0);
-        warp_wait(&ms.q_full, 1);
-      }
-    }
-  } else if (warp == 9) {
-    // ================================================================ matrix instructions
-    // The whole warp walks the steps, so that descriptors stay in uniform registers; one
-    // elected lane issues.
-    const bool leader = elect_one();
-    const bool negate = p.scale_log2 < 0.f;  // S is compared and scaled by |scale|
-    const uint32_t id_qk = mma_idesc(kOpBf16, kChunkKeys, negate, false);
-    const uint32_t id_pv = mma_idesc(kOpBf16, D, false, true);
-    // descriptors as (address, rest) words: moving along a tile changes the address alone
-    const uint64_t dk = smem_desc_sw128(smem_addr(ks), 16, 1024), dq = smem_desc_sw128(smem_addr(qs), 16, 1024);
-    const uint32_t dk0 = static_cast<uint32_t>(dk), dq0 = static_cast<uint32_t>(dq);
-    const uint32_t hi_qk = static_cast<uint32_t>(dk >> 32);
-    auto desc = [](uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; };
-    const int box_rows = kFp8 ? kChunkKeys : min(p.block_size, kChunkKeys);
-    const uint64_t dv = smem_desc_sw128(smem_addr(vs), box_rows * 128, 1024);
-    const uint32_t dv0 = static_cast<uint32_t>(dv), hi_v = static_cast<uint32_t>(dv >> 32);
-    // 16, 32 and 64 rows further down: in the same box, or past the boxes in between
-    auto rows_down = [&](int n) { return static_cast<uint32_t>(n < box_rows ? n * 128 : n * D * 2) >> 4; };
-    const uint32_t v_step1 = rows_down(16), v_step2 = rows_down(32), v_step4 = rows_down(64);
-    int k_at = 0, k_turn = 0, v_at = 0, v_turn = 0;  // stage and parity of the next K, V tile
-    unsigned p_phase = 0;
-    for (int item = 0; !timed_out; ++item) {
-      const int slot = item % kDescs;
-      if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
-        timed_out = true;
-        break;
-      }
-      const Desc& d = ms.desc[slot];
-      if (!__shfl_sync(kFullMask, d.valid, 0)) break;
-      const Groups grp = groups_of(d);
-      const int n0 = __shfl_sync(kFullMask, grp.n0, 0), n1 = __shfl_sync(kFullMask, grp.n1, 0);
-      const bool single = __shfl_sync(kFullMask, d.single, 0) != 0;
-      // keys the rows may see from the piece's first tile on
-      const int keys = __shfl_sync(kFullMask, d.end - d.ja * kChunkKeys, 0);
-      const int steps = max(n0, n1), last_g = n1 >= n0 ? 1 : 0;
-      if (!warp_wait(&ms.q_full, item & 1)) {
-        timed_out = true;
-        break;
-      }
-      tc_fence_after();
-      // A tile is used by both groups, the second releasing it, or (single) by one.
-      auto qk = [&](int g, int s) {
-        if (leader) {
-          const uint32_t a = dq0 + (single ? 0 : g * (C::kTile >> 4)), b = dk0 + k_at * (C::kTile >> 4);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
-            mma_f16_ss(tmem + g * 128, desc(a + off, hi_qk), desc(b + off, hi_qk), id_qk, k > 0);
+        __syncwarp();
+        // Q (over codes the softmax warps bring it)
+        if (!kFp8) {
+          if (!warp_wait(&ms.q_empty, (item & 1) ^ 1)) {
+            timed_out = true;
+            break;
           }
-          mma_commit(&ms.s_full[g]);
-          if (single || g == 1) mma_commit(&ms.k_empty[k_at]);
-          if (g == last_g && s == steps - 1) mma_commit(&ms.q_empty);
+          const int q_tiles = single ? 1 : 2;
+          if (lane == 0) mbar_arrive_expect_tx(&ms.q_full, q_tiles * C::kTile);
+          __syncwarp();
+          if (lane < q_tiles * C::kHalves) {
+            const int g = lane / C::kHalves, h = lane % C::kHalves;
+            tma_box(qs + g * C::kTile + h * C::kHalf, &tm_q, 64 * h, w.kh << g_shift,
+                    row0 + g * half, &ms.q_full);
+          }
         }
-        if (single || g == 1) {
-          if (++k_at == NK) {
+        // K: a box of a block's rows (128 at most), for each 64-element half of a row, or of codes
+        const int nt = jb - ja;
+        const int box_rows = min(p.block_size, kChunkKeys);
+        BlockIds ids;
+        ids.start(p, d);
+        for (int t = 0; t < nt; ++t) {
+          ids.advance(t, &d.bad_from, p.error_word);
+          uint64_t* full = kFp8 ? &ms.raw_full[0] : &ms.k_full[k_at];
+          if (!warp_wait(kFp8 ? &ms.raw_empty[0] : &ms.k_empty[k_at], k_turn ^ 1)) {
+            timed_out = true;
+            break;
+          }
+          const int keys = kv_end - (ja + t) * kChunkKeys;
+          const int boxes = min(ids.nbt, (keys + box_rows - 1) / box_rows);
+          if (lane == 0)
+            mbar_arrive_expect_tx(full, boxes * box_rows * (kFp8 ? D : 2 * D));
+          __syncwarp();
+          constexpr int kParts = kFp8 ? 1 : C::kHalves;
+          const int blk = lane / kParts, h = lane % kParts;
+          const int row = ids.row(t, blk);
+          if (blk < boxes)
+            tma_box(kFp8 ? raw + blk * box_rows * D
+                         : ks + k_at * C::kTile + h * C::kHalf + blk * box_rows * 128,
+                    &tm_k, 64 * h, w.kh, row, full);
+          if (++k_at == (kFp8 ? 1 : NK)) {
             k_at = 0;
             k_turn ^= 1;
           }
         }
+        ++item;
+        // the next item
+        u = end;
+        if (u < u_end) next_item(p, lt, &w);
+      }
+      if (!timed_out) {
+        const int slot = item % kDescs;
+        if (warp_wait(&ms.desc_empty[slot], ((item / kDescs) & 1) ^ 1)) {
+          if (lane == 0) {
+            ms.desc[slot].valid = 0;
+            mbar_arrive(&ms.desc_full[slot]);
+          }
+        } else {
+          timed_out = true;
+        }
+      }
+      if (timed_out) {
+        // copies in flight land before the block may leave
+        for (int st = 0; st < (kFp8 ? 1 : 5); ++st)
+          for (int turn = 0; turn < 2; ++turn)
+            warp_wait(kFp8 ? &ms.raw_full[0] : &ms.k_full[st], turn);
+        if (!kFp8) {
+          warp_wait(&ms.q_full, 0);
+          warp_wait(&ms.q_full, 1);
+        }
+      }
+    } else if (warp == 9) {
+      // ================================================================ matrix instructions
+      // The whole warp walks the steps, so that descriptors stay in uniform registers; one
+      // elected lane issues.
+      const bool leader = elect_one();
+      const bool negate = p.scale_log2 < 0.f;  // S is compared and scaled by |scale|
+      const uint32_t id_qk = mma_idesc(kOpBf16, kChunkKeys, negate, false);
+      const uint32_t id_pv = mma_idesc(kOpBf16, D, false, true);
+      // descriptors as (address, rest) words: moving along a tile changes the address alone
+      const uint64_t dk = smem_desc_sw128(smem_addr(ks), 16, 1024);
+      const uint64_t dq = smem_desc_sw128(smem_addr(qs), 16, 1024);
+      const uint32_t dk0 = static_cast<uint32_t>(dk), dq0 = static_cast<uint32_t>(dq);
+      const uint32_t hi_qk = static_cast<uint32_t>(dk >> 32);
+      auto desc = [](uint32_t lo, uint32_t hi) { return static_cast<uint64_t>(hi) << 32 | lo; };
+      const int box_rows = kFp8 ? kChunkKeys : min(p.block_size, kChunkKeys);
+      const uint64_t dv = smem_desc_sw128(smem_addr(vs), box_rows * 128, 1024);
+      const uint32_t dv0 = static_cast<uint32_t>(dv), hi_v = static_cast<uint32_t>(dv >> 32);
+      // 16, 32 and 64 rows further down: in the same box, or past the boxes in between
+      auto rows_down = [&](int n) {
+        return static_cast<uint32_t>(n < box_rows ? n * 128 : n * D * 2) >> 4;
       };
-      // Group g's P V of step s and its Q K of the next, issued back to back. Their three
-      // barriers are polled at once, a lane each: one wait after the other left the tensor
-      // core idle for a fifth of the time.
-      auto step = [&](int g, int s, int n) {
-        const bool more = s + 1 < n;
-        uint64_t* bar = &ms.p_full[g];
-        uint32_t turn = (p_phase >> g) & 1;
-        if (lane == 1) {
-          bar = &ms.clean[v_at];
-          turn = v_turn;
-        } else if (lane == 2 && more) {
-          bar = &ms.k_full[k_at];
-          turn = k_turn;
+      const uint32_t v_step1 = rows_down(16), v_step2 = rows_down(32), v_step4 = rows_down(64);
+      int k_at = 0, k_turn = 0, v_at = 0, v_turn = 0;  // stage and parity of the next K, V tile
+      unsigned p_phase = 0;
+      for (int item = 0; !timed_out; ++item) {
+        const int slot = item % kDescs;
+        if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
+          timed_out = true;
+          break;
         }
-        if (!warp_wait(bar, turn)) return false;
-        p_phase ^= 1u << g;
+        const Desc& d = ms.desc[slot];
+        if (!__shfl_sync(kFullMask, d.valid, 0)) break;
+        const Groups grp = groups_of(d);
+        const int n0 = __shfl_sync(kFullMask, grp.n0, 0), n1 = __shfl_sync(kFullMask, grp.n1, 0);
+        const bool single = __shfl_sync(kFullMask, d.single, 0) != 0;
+        // keys the rows may see from the piece's first tile on
+        const int keys = __shfl_sync(kFullMask, d.end - d.ja * kChunkKeys, 0);
+        const int steps = max(n0, n1), last_g = n1 >= n0 ? 1 : 0;
+        if (!warp_wait(&ms.q_full, item & 1)) {
+          timed_out = true;
+          break;
+        }
         tc_fence_after();
-        const int left = keys - (single ? 2 * s + g : s) * kChunkKeys;
-        if (leader) {
-          const uint32_t b = dv0 + v_at * (C::kTile >> 4);
+        // A tile is used by both groups, the second releasing it, or (single) by one.
+        auto qk = [&](int g, int s) {
+          if (leader) {
+            const uint32_t a = dq0 + (single ? 0 : g * (C::kTile >> 4));
+            const uint32_t b = dk0 + k_at * (C::kTile >> 4);
 #pragma unroll
-          for (int k = 0; k < kChunkKeys / 16; ++k)
-            if (16 * k < left)
-              mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 8 * k,
-                         desc(b + (k & 1) * v_step1 + (k >> 1 & 1) * v_step2 + (k >> 2) * v_step4, hi_v), id_pv,
-                         s > 0 || k > 0);
-          if (single || g == 1) mma_commit(&ms.v_empty[v_at]);
-          if (!more) mma_commit(&ms.o_full[g]);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
+              mma_f16_ss(tmem + g * 128, desc(a + off, hi_qk), desc(b + off, hi_qk), id_qk, k > 0);
+            }
+            mma_commit(&ms.s_full[g]);
+            if (single || g == 1) mma_commit(&ms.k_empty[k_at]);
+            if (g == last_g && s == steps - 1) mma_commit(&ms.q_empty);
+          }
+          if (single || g == 1) {
+            if (++k_at == NK) {
+              k_at = 0;
+              k_turn ^= 1;
+            }
+          }
+        };
+        // Group g's P V of step s and its Q K of the next, issued back to back. Their three
+        // barriers are polled at once, a lane each: one wait after the other left the tensor
+        // core idle for a fifth of the time.
+        auto step = [&](int g, int s, int n) {
+          const bool more = s + 1 < n;
+          uint64_t* bar = &ms.p_full[g];
+          uint32_t turn = (p_phase >> g) & 1;
+          if (lane == 1) {
+            bar = &ms.clean[v_at];
+            turn = v_turn;
+          } else if (lane == 2 && more) {
+            bar = &ms.k_full[k_at];
+            turn = k_turn;
+          }
+          if (!warp_wait(bar, turn)) return false;
+          p_phase ^= 1u << g;
+          tc_fence_after();
+          const int left = keys - (single ? 2 * s + g : s) * kChunkKeys;
+          if (leader) {
+            const uint32_t b = dv0 + v_at * (C::kTile >> 4);
+#pragma unroll
+            for (int k = 0; k < kChunkKeys / 16; ++k)
+              if (16 * k < left)
+                mma_f16_ts(
+                    tmem + 256 + g * 128, tmem + g * 128 + 8 * k,
+                    desc(b + (k & 1) * v_step1 + (k >> 1 & 1) * v_step2 + (k >> 2) * v_step4, hi_v),
+                    id_pv, s > 0 || k > 0);
+            if (single || g == 1) mma_commit(&ms.v_empty[v_at]);
+            if (!more) mma_commit(&ms.o_full[g]);
+          }
+          if (single || g == 1) {
+            if (++v_at == NV) {
+              v_at = 0;
+              v_turn ^= 1;
+            }
+          }
+          if (more) qk(g, s + 1);
+          __syncwarp();
+          return true;
+        };
+        bool ok = true;
+        // group 1's warps bring their Q at their own pace; an item without steps of theirs waits
+        // for them all the same, so that they see every turn of q_empty
+        if (kFp8 && n1 == 0) ok = warp_wait(&ms.q_full1, item & 1);
+        if (ok && n0 > 0) {
+          ok = warp_wait(&ms.k_full[k_at], k_turn);
+          tc_fence_after();
+          if (ok) qk(0, 0);
         }
-        if (single || g == 1) {
-          if (++v_at == NV) {
+        if (kFp8 && ok && n1 > 0) ok = warp_wait(&ms.q_full1, item & 1);
+        if (ok && n1 > 0) {
+          ok = warp_wait(&ms.k_full[k_at], k_turn);
+          tc_fence_after();
+          if (ok) qk(1, 0);
+        }
+        for (int s = 0; ok && s < steps; ++s) {
+          if (s < n0) ok = step(0, s, n0);
+          if (ok && s < n1) ok = step(1, s, n1);
+        }
+        if (!ok) {
+          timed_out = true;
+          break;
+        }
+        if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
+      }
+      // nothing of this warp's is in flight when the block gives its TMEM back
+      if (leader) mma_commit(&ms.done);
+      if (!warp_wait(&ms.done, 0)) timed_out = true;
+    } else if (warp == 10) {
+      // ================================================================ load V
+      // A block's rows (128 at most) come as one box, both halves of its rows one behind the
+      // other: the P V product takes 16 rows of one block at a time, so blocks need not join.
+      int v_at = 0, v_turn = 0;
+      for (int item = 0; !timed_out; ++item) {
+        const int slot = item % kDescs;
+        if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
+          timed_out = true;
+          break;
+        }
+        const Desc& d = ms.desc[slot];
+        if (!d.valid) break;
+        const int box_rows = min(p.block_size, kChunkKeys);
+        const int kh = d.kh;
+        BlockIds ids;
+        ids.start(p, d);
+        for (int t = 0; t < ids.nt; ++t) {
+          ids.advance(t, nullptr, nullptr);
+          uint64_t* full = kFp8 ? &ms.raw_full[1] : &ms.v_full[v_at];
+          if (!warp_wait(kFp8 ? &ms.raw_empty[1] : &ms.v_empty[v_at], v_turn ^ 1)) {
+            timed_out = true;
+            break;
+          }
+          const int keys = ids.end - (ids.ja + t) * kChunkKeys;
+          const int boxes = min(ids.nbt, (keys + box_rows - 1) / box_rows);
+          if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_rows * (kFp8 ? D : 2 * D));
+          __syncwarp();
+          const int row = ids.row(t, lane);
+          if (lane < boxes) {
+            if (kFp8)
+              tma_box(raw + C::kRaw + lane * box_rows * D, &tm_v, 0, kh, row, full);
+            else
+              tma_box4(vs + v_at * C::kTile + lane * box_rows * D * 2, &tm_v, 0, row, 0, kh, full);
+          }
+          if (++v_at == (kFp8 ? 1 : NV)) {
             v_at = 0;
             v_turn ^= 1;
           }
         }
-        if (more) qk(g, s + 1);
         __syncwarp();
-        return true;
-      };
-      bool ok = true;
-      // group 1's warps bring their Q at their own pace; an item without steps of theirs waits
-      // for them all the same, so that they see every turn of q_empty
-      if (kFp8 && n1 == 0) ok = warp_wait(&ms.q_full1, item & 1);
-      if (ok && n0 > 0) {
-        ok = warp_wait(&ms.k_full[k_at], k_turn);
-        tc_fence_after();
-        if (ok) qk(0, 0);
+        if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
       }
-      if (kFp8 && ok && n1 > 0) ok = warp_wait(&ms.q_full1, item & 1);
-      if (ok && n1 > 0) {
-        ok = warp_wait(&ms.k_full[k_at], k_turn);
-        tc_fence_after();
-        if (ok) qk(1, 0);
+      if (timed_out)
+        for (int st = 0; st < (kFp8 ? 1 : 5); ++st)
+          for (int turn = 0; turn < 2; ++turn)
+            warp_wait(kFp8 ? &ms.raw_full[1] : &ms.v_full[st], turn);
+    } else if (warp == 11) {
+      // ================================================================ rows without work
+      // requests whose rows are written all the same: padded (zeros) or in error (NaN)
+      if (!pl.ok && blockIdx.x == 0 && lane == 0) atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
+      for (int first = pl.ok ? blockIdx.x : p.B; first < p.B; first += 32 * gridDim.x) {
+        const int b = first + lane * gridDim.x;
+        int q0 = 0, q1 = 0, L = 0;
+        if (b < p.B && chunk_req(p, b, lt).r.n == 0) {
+          q0 = p.query_start[b];
+          q1 = p.query_start[b + 1];
+          L = p.context_lens[b];
+          if (q0 < q1 && L != 0) atomic_or_error(p.error_word, PDA_DEVERR_CONTEXT_LEN);
+        }
+        for (unsigned todo = __ballot_sync(kFullMask, q0 < q1); todo != 0; todo &= todo - 1) {
+          const int from = __ffs(todo) - 1;
+          const int r0 = __shfl_sync(kFullMask, q0, from), r1 = __shfl_sync(kFullMask, q1, from);
+          // 0x7fff is a NaN in either type
+          const uint32_t v = __shfl_sync(kFullMask, L, from) == 0 ? 0u : 0x7fff7fffu;
+          uint4* rows = reinterpret_cast<uint4*>(p.out) + static_cast<size_t>(r0) * p.H * (D / 8);
+          const long long vecs = static_cast<long long>(r1 - r0) * p.H * (D / 8);
+          for (long long i = lane; i < vecs; i += 32) rows[i] = make_uint4(v, v, v, v);
+        }
       }
-      for (int s = 0; ok && s < steps; ++s) {
-        if (s < n0) ok = step(0, s, n0);
-        if (ok && s < n1) ok = step(1, s, n1);
-      }
-      if (!ok) {
-        timed_out = true;
-        break;
-      }
-      if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
-    }
-    // nothing of this warp's is in flight when the block gives its TMEM back
-    if (leader) mma_commit(&ms.done);
-    if (!warp_wait(&ms.done, 0)) timed_out = true;
-  } else if (warp == 10) {
-    // ================================================================ load V
-    // A block's rows (128 at most) come as one box, both halves of its rows one behind the
-    // other: the P V product takes 16 rows of one block at a time, so blocks need not join.
-    int v_at = 0, v_turn = 0;
-    for (int item = 0; !timed_out; ++item) {
-      const int slot = item % kDescs;
-      if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
-        timed_out = true;
-        break;
-      }
-      const Desc& d = ms.desc[slot];
-      if (!d.valid) break;
+    } else if (warp >= 12) {
+      // ================================================================ clean V tiles
+      const int part = warp - 12;
       const int box_rows = min(p.block_size, kChunkKeys);
-      const int kh = d.kh;
-      BlockIds ids;
-      ids.start(p, d);
-      for (int t = 0; t < ids.nt; ++t) {
-        ids.advance(t, nullptr, nullptr);
-        uint64_t* full = kFp8 ? &ms.raw_full[1] : &ms.v_full[v_at];
-        if (!warp_wait(kFp8 ? &ms.raw_empty[1] : &ms.v_empty[v_at], v_turn ^ 1)) {
+      unsigned loads = 0;
+      for (int item = 0; !timed_out; ++item) {
+        const int slot = item % kDescs;
+        if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
           timed_out = true;
           break;
         }
-        const int boxes = min(ids.nbt, (ids.end - (ids.ja + t) * kChunkKeys + box_rows - 1) / box_rows);
-        if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_rows * (kFp8 ? D : 2 * D));
-        __syncwarp();
-        const int row = ids.row(t, lane);
-        if (lane < boxes) {
-          if (kFp8)
-            tma_box(raw + C::kRaw + lane * box_rows * D, &tm_v, 0, kh, row, full);
-          else
-            tma_box4(vs + v_at * C::kTile + lane * box_rows * D * 2, &tm_v, 0, row, 0, kh, full);
-        }
-        if (++v_at == (kFp8 ? 1 : NV)) {
-          v_at = 0;
-          v_turn ^= 1;
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
-    }
-    if (timed_out)
-      for (int st = 0; st < (kFp8 ? 1 : 5); ++st)
-        for (int turn = 0; turn < 2; ++turn)
-          warp_wait(kFp8 ? &ms.raw_full[1] : &ms.v_full[st], turn);
-  } else if (warp == 11) {
-    // ================================================================ rows without work
-    // requests whose rows are written all the same: padded (zeros) or in error (NaN)
-    if (!pl.ok && blockIdx.x == 0 && lane == 0) atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
-    for (int first = pl.ok ? blockIdx.x : p.B; first < p.B; first += 32 * gridDim.x) {
-      const int b = first + lane * gridDim.x;
-      int q0 = 0, q1 = 0, L = 0;
-      if (b < p.B && chunk_req(p, b, lt).r.n == 0) {
-        q0 = p.query_start[b];
-        q1 = p.query_start[b + 1];
-        L = p.context_lens[b];
-        if (q0 < q1 && L != 0) atomic_or_error(p.error_word, PDA_DEVERR_CONTEXT_LEN);
-      }
-      for (unsigned todo = __ballot_sync(kFullMask, q0 < q1); todo != 0; todo &= todo - 1) {
-        const int from = __ffs(todo) - 1;
-        const int r0 = __shfl_sync(kFullMask, q0, from), r1 = __shfl_sync(kFullMask, q1, from);
-        // 0x7fff is a NaN in either type
-        const uint32_t v = __shfl_sync(kFullMask, L, from) == 0 ? 0u : 0x7fff7fffu;
-        uint4* rows = reinterpret_cast<uint4*>(p.out) + static_cast<size_t>(r0) * p.H * (D / 8);
-        const long long vecs = static_cast<long long>(r1 - r0) * p.H * (D / 8);
-        for (long long i = lane; i < vecs; i += 32) rows[i] = make_uint4(v, v, v, v);
-      }
-    }
-  } else if (warp >= 12) {
-    // ================================================================ clean V tiles
-    const int part = warp - 12;
-    const int box_rows = min(p.block_size, kChunkKeys);
-    unsigned loads = 0;
-    for (int item = 0; !timed_out; ++item) {
-      const int slot = item % kDescs;
-      if (!warp_wait(&ms.desc_full[slot], (item / kDescs) & 1)) {
-        timed_out = true;
-        break;
-      }
-      Desc& d = ms.desc[slot];
-      if (!d.valid) break;
-      const int ja = d.ja, nt = d.jb - ja, jc = d.jc, kv_end = d.end;
-      for (int t = 0; t < nt; ++t) {
-        const unsigned at = loads + t;
-        const int st = at % NV;
-        if (kFp8) {
+        Desc& d = ms.desc[slot];
+        if (!d.valid) break;
+        const int ja = d.ja, nt = d.jb - ja, jc = d.jc, kv_end = d.end;
+        for (int t = 0; t < nt; ++t) {
+          const unsigned at = loads + t;
+          const int st = at % NV;
+          if (kFp8) {
+            const int keys = min(kChunkKeys, kv_end - (ja + t) * kChunkKeys);
+            const int kst = at % NK;
+            if (!warp_wait(&ms.raw_full[0], at & 1) ||
+                !warp_wait(&ms.k_empty[kst], ((at / NK) & 1) ^ 1)) {
+              timed_out = true;
+              break;
+            }
+            widen<D>(ks + kst * C::kTile, raw, part, keys, nullptr);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&ms.k_full[kst]);
+              mbar_arrive(&ms.raw_empty[0]);
+            }
+            if (!warp_wait(&ms.raw_full[1], at & 1) ||
+                !warp_wait(&ms.v_empty[st], ((at / NV) & 1) ^ 1)) {
+              timed_out = true;
+              break;
+            }
+            widen<D>(vs + st * C::kTile, raw + C::kRaw, part, keys,
+                     ja + t < jc ? nullptr : d.nonfinite[ja + t - jc]);
+            fence_proxy_async_smem();
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&ms.clean[st]);
+              mbar_arrive(&ms.raw_empty[1]);
+            }
+            continue;
+          }
+          if (!warp_wait(&ms.v_full[st], (at / NV) & 1)) {
+            timed_out = true;
+            break;
+          }
+          if (ja + t < jc) {  // every row sees every key
+            if (lane == 0) mbar_arrive(&ms.clean[st]);
+            continue;
+          }
           const int keys = min(kChunkKeys, kv_end - (ja + t) * kChunkKeys);
-          const int kst = at % NK;
-          if (!warp_wait(&ms.raw_full[0], at & 1) || !warp_wait(&ms.k_empty[kst], ((at / NK) & 1) ^ 1)) {
-            timed_out = true;
-            break;
-          }
-          widen<D>(ks + kst * C::kTile, raw, part, keys, nullptr);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ms.k_full[kst]);
-            mbar_arrive(&ms.raw_empty[0]);
-          }
-          if (!warp_wait(&ms.raw_full[1], at & 1) || !warp_wait(&ms.v_empty[st], ((at / NV) & 1) ^ 1)) {
-            timed_out = true;
-            break;
-          }
-          widen<D>(vs + st * C::kTile, raw + C::kRaw, part, keys,
-                   ja + t < jc ? nullptr : d.nonfinite[ja + t - jc]);
+          clean_tile<D, kBf16>(vs + st * C::kTile, part, keys, box_rows, d.nonfinite[ja + t - jc]);
           fence_proxy_async_smem();
           __threadfence_block();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&ms.clean[st]);
-            mbar_arrive(&ms.raw_empty[1]);
-          }
-          continue;
-        }
-        if (!warp_wait(&ms.v_full[st], (at / NV) & 1)) {
-          timed_out = true;
-          break;
-        }
-        if (ja + t < jc) {  // every row sees every key
           if (lane == 0) mbar_arrive(&ms.clean[st]);
-          continue;
         }
-        const int keys = min(kChunkKeys, kv_end - (ja + t) * kChunkKeys);
-        clean_tile<D, kBf16>(vs + st * C::kTile, part, keys, box_rows, d.nonfinite[ja + t - jc]);
-        fence_proxy_async_smem();
-        __threadfence_block();
+        loads += nt;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.clean[st]);
+        if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
       }
-      loads += nt;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms.desc_empty[slot]);
     }
-  }
   }
   if (timed_out) atomic_or_error(p.error_word, PDA_DEVERR_TIMEOUT);
   tc_fence_before();
@@ -1126,8 +1142,8 @@ pda_status encode_v(CUtensorMap* tm, const void* base, long long rows, int heads
                               static_cast<cuuint64_t>(heads)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(heads) * D * 2, 128u,
                                  static_cast<cuuint64_t>(D) * 2};
-  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(D / 64),
-                             1u};
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(D / 64), 1u};
   const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
   const CUresult r = g_encode(
       tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,

@@ -249,12 +249,14 @@ __global__ void __launch_bounds__(256)
 // Most key tiles of an item, by the host's bound on the lengths.
 inline int chunk_tiles(const ChunkParams& p) {
   const long long cap = static_cast<long long>(p.max_blocks) * p.block_size;
-  return static_cast<int>((std::min<long long>(p.max_context_len, cap) + kChunkKeys - 1) / kChunkKeys);
+  const long long keys = std::min<long long>(p.max_context_len, cap);
+  return static_cast<int>((keys + kChunkKeys - 1) / kChunkKeys);
 }
 // Blocks of a launch: no more than that bound can keep busy.
 template <typename C>
 long long chunk_units(const ChunkParams& p, int g_shift) {
-  const long long items = ((static_cast<long long>(p.T) >> (C::kRowsLog2 - g_shift)) + p.B) * p.H_kv;
+  const long long items =
+      ((static_cast<long long>(p.T) >> (C::kRowsLog2 - g_shift)) + p.B) * p.H_kv;
   return items * (chunk_tiles(p) + kItemUnits);
 }
 template <typename C>

@@ -2,12 +2,13 @@
 // Host and device code both use it (a host test checks its arithmetic against loops).
 //
 // A request's query rows, G heads of a kv-head times its n new tokens, are cut into items of
-// 2^lt tokens (256 rows on the tensor cores). An item attends to keys [0, p + 1), p the position of its last
-// token, in tiles of 128 keys, and counts as tiles + 4 units: its own start and end, with the
-// masked tiles, cost about four tiles (weighed as one, the busiest block of a batch of short
-// prompts had a quarter more to do than the mean one). Units are numbered request after request, kv-head after kv-head, item after item, and
-// each of the launch's workers takes an equal, contiguous range of them, so the split is even
-// whatever the lengths; an item cut by a range's end is merged afterwards.
+// 2^lt tokens (256 rows on the tensor cores). An item attends to keys [0, p + 1), p the
+// position of its last token, in tiles of 128 keys, and counts as tiles + 4 units: its own
+// start and end, with the masked tiles, cost about four tiles (weighed as one, the busiest
+// block of a batch of short prompts had a quarter more to do than the mean one). Units are
+// numbered request after request, kv-head after kv-head, item after item, and each of the
+// launch's workers takes an equal, contiguous range of them, so the split is even whatever the
+// lengths; an item cut by a range's end is merged afterwards.
 #pragma once
 
 #if defined(__CUDACC__)
@@ -49,7 +50,8 @@ struct ChunkReq {
   PDA_CHUNK_HD int units_before(int i) const {
     const int a1 = L - n - 1;  // may be -1: the shifts below round down
     const unsigned m = i;
-    if (lt >= 7) return static_cast<int>(m * ((a1 >> 7) + 1 + kItemUnits) + (pairs(m + 1) << (lt - 7)));
+    if (lt >= 7)
+      return static_cast<int>(m * ((a1 >> 7) + 1 + kItemUnits) + (pairs(m + 1) << (lt - 7)));
     const int s = 7 - lt;
     const unsigned x0 = (a1 >> lt) + 1;
     return static_cast<int>((1 + kItemUnits) * m + floor_sum(x0 + m, s) - floor_sum(x0, s));
@@ -92,7 +94,9 @@ PDA_CHUNK_HD int chunk_cut(int units, int workers, int c) {
 
 // Workers a launch of `units` units uses: no more than leave each `least` of them.
 PDA_CHUNK_HD int chunk_workers(long long units, int workers, int least) {
-  const long long most = units >> 30 != 0 ? workers : (static_cast<unsigned>(units) + least - 1) / static_cast<unsigned>(least);
+  const long long most = units >> 30 != 0 ? workers
+                                          : (static_cast<unsigned>(units) + least - 1) /
+                                                static_cast<unsigned>(least);
   return most < 1 ? 1 : most < workers ? static_cast<int>(most) : workers;
 }
 
