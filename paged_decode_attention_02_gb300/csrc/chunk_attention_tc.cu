@@ -17,8 +17,8 @@
 //   12-15     clean the V tiles at the diagonal and the end (see below), or, over an FP8
 //             cache, widen every K and V tile: the TMA brings the codes, these warps write
 //             them as fp16 (exact, and one instruction for two codes, where bf16 took four:
-//             365 -> 341 us on three chunks of up to 2048 tokens) where the products read
-//             them. The softmax warps then bring Q, each row scaled by a power of two that
+//             365 -> 341 us on three chunks of up to 2048 tokens; 312 with K and V
+//             through one copy of the loop) where the products read them. The softmax warps then bring Q, each row scaled by a power of two that
 //             puts its largest value at 2^14: what falls under fp16's smallest step is below
 //             2^-39 of that value.
 // The softmax warps take the registers that the others give back (setmaxnreg).
@@ -206,41 +206,66 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Widens this warp's quarter of a tile of E4M3 codes, [128][D] bytes, to fp16 in the products'
-// layout (64-element halves, 128-byte swizzle). Rows from `keys` on become zeros. Where
-// `nonfinite` is given, NaN codes become zeros and their rows' bits are set there.
+// This warp's quarter of a tile of E4M3 codes, [128][D] bytes: NaN codes of the first `keys` rows
+// become zeros, and their rows' bits are set in `nonfinite`.
+template <int D>
+__device__ __forceinline__ void clean_codes(unsigned char* codes, int part, int keys,
+                                            unsigned* nonfinite) {
+  constexpr int kLanes = D / 16;  // lanes of a row, 16 codes each
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int i = 0; i < kLanes; ++i) {
+    const int r = 32 * part + i * (32 / kLanes) + lane / kLanes;
+    uint4* at = reinterpret_cast<uint4*>(codes + r * D) + lane % kLanes;
+    uint4 v = *at;
+    uint32_t* w = &v.x;
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t hit = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+      w[k] &= ~((hit >> 7) * 0xffu);
+      any |= hit;
+    }
+    if (any != 0 && r < keys) {
+      *at = v;
+      atomicOr(&nonfinite[r >> 5], 1u << (r & 31));
+    }
+  }
+  __syncwarp();
+}
+
+// Widens this warp's quarter of a tile of E4M3 codes to fp16 in the products' layout (64-element
+// halves, 128-byte swizzle). Rows from `keys` on become zeros.
 template <int D>
 __device__ __forceinline__ void widen(unsigned char* dst, const unsigned char* codes, int part,
-                                      int keys, unsigned* nonfinite) {
-  constexpr int kLanes = D / 16;  // lanes of a row, 16 codes each
+                                      int keys) {
+  constexpr int kLanes = D / 16, kBatch = 4;
   const int lane = threadIdx.x & 31, c = 2 * (lane % kLanes);
-#pragma unroll 2
-  for (int i = 0; i < 32 * kLanes / 32; ++i) {
-    const int r = 32 * part + i * (32 / kLanes) + lane / kLanes;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < keys) v = *reinterpret_cast<const uint4*>(codes + r * D + 8 * c);
-    uint32_t* w = &v.x;
-    if (nonfinite != nullptr) {
-      uint32_t any = 0;
+  // lanes of the second half take their pieces the other way round: no bank conflicts
+  const bool swap = c >= 8;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kLanes; i0 += kBatch) {
+    uint4 v[kBatch];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t hit = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-        w[k] &= ~((hit >> 7) * 0xffu);
-        any |= hit;
-      }
-      if (any != 0) atomicOr(&nonfinite[r >> 5], 1u << (r & 31));
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = 32 * part + (i0 + i) * (32 / kLanes) + lane / kLanes;
+      v[i] = r < keys ? *reinterpret_cast<const uint4*>(codes + r * D + 8 * c)
+                      : make_uint4(0, 0, 0, 0);
     }
-    uint4 o[2];
-    uint32_t* u = &o[0].x;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2(w[k], u[2 * k], u[2 * k + 1]);
-    // lanes of the second half take their pieces the other way round: no bank conflicts
-    const bool swap = c >= 8;
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = 32 * part + (i0 + i) * (32 / kLanes) + lane / kLanes;
+      uint4 o[2];
+      e4m3x4_to_f16x2(v[i].x, o[0].x, o[0].y);
+      e4m3x4_to_f16x2(v[i].y, o[0].z, o[0].w);
+      e4m3x4_to_f16x2(v[i].z, o[1].x, o[1].y);
+      e4m3x4_to_f16x2(v[i].w, o[1].z, o[1].w);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int piece = c + (swap ? 1 - k : k);
-      *reinterpret_cast<uint4*>(dst + (piece >> 3) * (kChunkKeys * 128) + r * 128 +
-                                (((piece & 7) ^ (r & 7)) << 4)) = swap == (k == 0) ? o[1] : o[0];
+      for (int k = 0; k < 2; ++k) {
+        const int piece = c + (swap ? 1 - k : k);
+        *reinterpret_cast<uint4*>(dst + (piece >> 3) * (kChunkKeys * 128) + r * 128 +
+                                  (((piece & 7) ^ (r & 7)) << 4)) = swap == (k == 0) ? o[1] : o[0];
+      }
     }
   }
 }
@@ -1047,31 +1072,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kFp8) {
             const int keys = min(kChunkKeys, kv_end - (ja + t) * kChunkKeys);
             const int kst = at % NK;
-            if (!warp_wait(&ms.raw_full[0], at & 1) ||
-                !warp_wait(&ms.k_empty[kst], ((at / NK) & 1) ^ 1)) {
+            bool ok = true;
+#pragma unroll 1
+            for (int v = 0; ok && v < 2; ++v) {  // K, then V
+              ok = warp_wait(&ms.raw_full[v], at & 1) &&
+                   warp_wait(v == 0 ? &ms.k_empty[kst] : &ms.v_empty[st],
+                             ((v == 0 ? at / NK : at / NV) & 1) ^ 1);
+              if (!ok) break;
+              unsigned char* codes = raw + v * C::kRaw;
+              if (v == 1 && ja + t >= jc)
+                clean_codes<D>(codes, part, keys, d.nonfinite[ja + t - jc]);
+              widen<D>(v == 0 ? ks + kst * C::kTile : vs + st * C::kTile, codes, part, keys);
+              fence_proxy_async_smem();
+              __threadfence_block();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(v == 0 ? &ms.k_full[kst] : &ms.clean[st]);
+                mbar_arrive(&ms.raw_empty[v]);
+              }
+            }
+            if (!ok) {
               timed_out = true;
               break;
-            }
-            widen<D>(ks + kst * C::kTile, raw, part, keys, nullptr);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&ms.k_full[kst]);
-              mbar_arrive(&ms.raw_empty[0]);
-            }
-            if (!warp_wait(&ms.raw_full[1], at & 1) ||
-                !warp_wait(&ms.v_empty[st], ((at / NV) & 1) ^ 1)) {
-              timed_out = true;
-              break;
-            }
-            widen<D>(vs + st * C::kTile, raw + C::kRaw, part, keys,
-                     ja + t < jc ? nullptr : d.nonfinite[ja + t - jc]);
-            fence_proxy_async_smem();
-            __threadfence_block();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&ms.clean[st]);
-              mbar_arrive(&ms.raw_empty[1]);
             }
             continue;
           }
