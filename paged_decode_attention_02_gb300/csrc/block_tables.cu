@@ -7,6 +7,8 @@
 // (8192 lengths are 32 KB of L2 reads) rather than passed through memory from a first kernel.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "pda_device.cuh"
 #include "pda_internal.h"
 
@@ -244,12 +246,22 @@ __global__ void __launch_bounds__(kSlotThreads)
 
 namespace {
 
-// More shared memory than the default 48 KB, for the largest batches.
-template <typename K>
-bool raise_smem(K kernel, size_t bytes) {
-  return bytes <= 48 * 1024 ||
-         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(bytes)) == cudaSuccess;
+// Shared memory of an assignment, 12 bytes a row. Together with the kernel's own it passes the
+// default 48 KB from 4085 rows on, so the limit is raised, once a device, to what the largest
+// batch takes: a limit of each call's own size could be lowered by one host thread between
+// another's raise and its launch. (Slots take 4 bytes a row: 32 KB at most.)
+constexpr size_t assign_smem(int B) { return static_cast<size_t>(B) * 3 * sizeof(int); }
+
+bool raise_assign_smem() {
+  static std::atomic<bool> raised[64];
+  int dev;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && raised[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kv_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(assign_smem(kTableMaxBatch))) != cudaSuccess)
+    return false;
+  if (dev < 64) raised[dev].store(true, std::memory_order_release);
+  return true;
 }
 
 pda_status check_tables(int B, int max_blocks, int block_size, int num_blocks) {
@@ -280,9 +292,8 @@ extern "C" pda_status pda_kv_assign_blocks(int32_t* block_tables, const int32_t*
   if (B > 0 && (block_tables == nullptr || blocks_held == nullptr || blocks_held_out == nullptr ||
                 context_lens == nullptr))
     return PDA_ERR_INVALID_ARG;
-  const size_t smem = static_cast<size_t>(B) * 3 * sizeof(int);
-  if (!raise_smem(kv_assign_kernel, smem)) return PDA_ERR_CUDA;
-  kv_assign_kernel<<<kAssignCluster, kAssignThreads, smem, stream>>>(
+  if (!raise_assign_smem()) return PDA_ERR_CUDA;
+  kv_assign_kernel<<<kAssignCluster, kAssignThreads, assign_smem(B), stream>>>(
       block_tables, blocks_held, blocks_held_out, free_list, free_count, free_count_out,
       context_lens, shared_blocks, B, max_blocks_per_seq, block_size, num_blocks, error_word);
   return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
@@ -303,7 +314,6 @@ extern "C" pda_status pda_kv_build_slots(int32_t* slot_mapping, int32_t* query_s
   const long long per = static_cast<long long>(kSlotThreads) * kSlotPerThread;
   const long long blocks = (static_cast<long long>(N) + per - 1) / per;
   const size_t smem = static_cast<size_t>(B) * sizeof(int);
-  if (!raise_smem(kv_slots_kernel, smem)) return PDA_ERR_CUDA;
   kv_slots_kernel<<<static_cast<unsigned>(blocks > 0 ? blocks : 1), kSlotThreads, smem, stream>>>(
       slot_mapping, query_start, query_lens, context_lens, block_tables, N, B,
       max_blocks_per_seq, block_size, num_blocks, error_word);
