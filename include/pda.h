@@ -482,7 +482,12 @@ pda_status pda_kv_unpack_block_scales_batched(const void* const* ins,
  *  context_lens   [B] int32: the length each row must cover; 0 gives every block back.
  *  shared_blocks  [B] int32 or NULL: the row's first shared_blocks[b] entries belong to
  *                 somebody else (a prefix that several rows share) and are never given back.
- *                 No other block may be in two rows, or it is given back twice.
+ *                 No other block may be in two rows, or it is given back twice. Updated in
+ *                 place: a row that shrinks into its prefix and grows again gets blocks of
+ *                 its own from blocks_held[b] on, not the shared ones, which it may not
+ *                 write; its shared_blocks[b] falls to blocks_held[b], so that they are
+ *                 given back. It is set anew, with the entries and blocks_held[b], when the
+ *                 row takes its next request.
  *  A row with context_lens < 0 or beyond max_blocks_per_seq * block_size, or with blocks_held
  *  outside [0, max_blocks_per_seq], is left as it is (PDA_DEVERR_CONTEXT_LEN). free_count
  *  outside [0, num_blocks] (PDA_DEVERR_NO_BLOCKS), or more blocks given back than the list
@@ -494,7 +499,7 @@ pda_status pda_kv_unpack_block_scales_batched(const void* const* ins,
 pda_status pda_kv_assign_blocks(int32_t* block_tables, const int32_t* blocks_held,
                                 int32_t* blocks_held_out, int32_t* free_list,
                                 const int32_t* free_count, int32_t* free_count_out,
-                                const int32_t* context_lens, const int32_t* shared_blocks, int B,
+                                const int32_t* context_lens, int32_t* shared_blocks, int B,
                                 int max_blocks_per_seq, int block_size, int num_blocks,
                                 int32_t* error_word, cudaStream_t stream);
 

@@ -508,7 +508,9 @@ def kv_assign_blocks(block_tables, blocks_held, free_list, free_count, context_l
                      shared_blocks=None, error_word=None, stream=None):
     """Grow and shrink the rows of ``block_tables`` to ``context_lens`` tokens, taking blocks
     off the top of the stack ``free_list[:free_count]`` and giving them back to it, in place
-    (``blocks_held`` and ``free_count`` too, unless other outputs are given for them)."""
+    (``blocks_held`` and ``free_count`` too, unless other outputs are given for them). A row's
+    first ``shared_blocks[b]`` entries are somebody else's; where a row shrinks into them and
+    grows again, ``shared_blocks[b]`` falls to the entries it still had (in place)."""
     _require(block_tables.dim() == 2 and free_list.dim() == 1,
              "block_tables must be [B, max_blocks] and free_list [num_blocks]")
     B, max_blocks = block_tables.shape

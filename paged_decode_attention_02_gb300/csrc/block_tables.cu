@@ -62,19 +62,21 @@ __device__ __forceinline__ int owner_of(const int* end, int n, int i) {
 // ---------------------------------------------------------------- block assignment
 // need_b = ceil(L_b / block_size). Rows that shrink push entries [max(need, shared), held)
 // onto the stack free_list[0, F); rows that grow pop need - held entries off its top, first
-// come first served in row order.
+// come first served in row order. A row that grows from inside its shared prefix owns what it
+// gets there, so the prefix ends at held from then on.
 //
 // One cluster of 8 blocks does the whole call: every block reads the lengths, the held
 // counts and F and computes both prefix sums; the cluster's barrier then separates the pushes
-// (and every read of `held` and F) from the pops and from the writes of the new counts, so
-// the outputs may be the inputs' own buffers and no workspace or second launch is needed.
+// (and every other block's read of `held`, `shared_blocks` and F) from the pops and from the
+// writes of the new counts, so the outputs may be the inputs' own buffers and no workspace or
+// second launch is needed.
 constexpr int kAssignCluster = 8;
 constexpr int kAssignThreads = 1024;
 
 __global__ void __cluster_dims__(kAssignCluster, 1, 1) __launch_bounds__(kAssignThreads)
     kv_assign_kernel(int32_t* tables, const int32_t* held, int32_t* held_out, int32_t* free_list,
                      const int32_t* free_count, int32_t* free_count_out, const int32_t* lens,
-                     const int32_t* shared_blocks, int B, int max_blocks, int block_size,
+                     int32_t* shared_blocks, int B, int max_blocks, int block_size,
                      int num_blocks, int32_t* error_word) {
   extern __shared__ int smem_ints[];
   __shared__ int warp_sums[32];
@@ -171,7 +173,10 @@ __global__ void __cluster_dims__(kAssignCluster, 1, 1) __launch_bounds__(kAssign
     int now = h;
     if (!bad && room_ok) {
       const int need = static_cast<int>((static_cast<long long>(L) + block_size - 1) / block_size);
-      if (need <= h || grow_end[b] <= granted) now = need;
+      if (need <= h || grow_end[b] <= granted) {
+        now = need;
+        if (need > h && shared_blocks != nullptr && shared_blocks[b] > h) shared_blocks[b] = h;
+      }
     }
     held_out[b] = now;
   }
@@ -281,7 +286,7 @@ extern "C" pda_status pda_kv_assign_blocks(int32_t* block_tables, const int32_t*
                                            int32_t* blocks_held_out, int32_t* free_list,
                                            const int32_t* free_count, int32_t* free_count_out,
                                            const int32_t* context_lens,
-                                           const int32_t* shared_blocks, int B,
+                                           int32_t* shared_blocks, int B,
                                            int max_blocks_per_seq, int block_size,
                                            int num_blocks, int32_t* error_word,
                                            cudaStream_t stream) {

@@ -1,5 +1,5 @@
-"""Block assignment at the batch sizes around the default shared-memory limit, and from several
-host threads."""
+"""Block assignment at the batch sizes around the default shared-memory limit, from several
+host threads, and with shared prefixes over several calls."""
 import os
 import subprocess
 import sys
@@ -89,3 +89,58 @@ def test_assign_from_threads_with_batches_of_their_own():
     for t in threads:
         t.join()
     assert not failed
+
+
+def test_assign_shrunk_into_its_prefix_and_grown_again():
+    """A row that ends inside its shared prefix and grows again gets blocks of its own from
+    there on, and gives every one of them back."""
+    bs, NB = 16, 16
+    tables, held = i32([[0, 1, 2, 3, 4, 5, -1, -1]]), i32([6])  # 0 .. 3 are somebody else's
+    free, count, shared, err = i32(list(range(6, 16)) + [-7] * 6), i32([10]), i32([4]), i32([0])
+
+    def to(length):
+        pda.kv_assign_blocks(tables, held, free, count, i32([length]), bs, shared_blocks=shared,
+                             error_word=err)
+        return tables[0, :int(held)].tolist(), free[:int(count)].tolist()
+
+    live, rest = to(2 * bs)
+    assert live == [0, 1] and sorted(rest) == list(range(4, 16))
+    live, rest = to(5 * bs)
+    assert live[:2] == [0, 1] and not set(live[2:]) & {0, 1, 2, 3}
+    assert sorted(live[2:] + rest) == list(range(4, 16))
+    live, rest = to(0)
+    assert live == [] and sorted(rest) == list(range(4, 16))
+    pda.check_error(err)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_assign_shared_prefixes_over_many_steps(seed):
+    """Rows over one prefix grow and shrink at random, also into the prefix and to nothing: at
+    each step every other block is in one row or on the stack, once."""
+    rng = np.random.RandomState(seed)
+    B, mb, bs, P, NB = 24, 20, 16, 6, 300
+    prefix = list(range(P))
+    table = np.full((B, mb), -1)
+    table[:, :P] = prefix
+    tables, held, shared = i32(table), i32(np.full(B, P)), i32(np.full(B, P))
+    free, count, err = i32(list(range(P, NB)) + [-7] * P), i32([NB - P]), i32([0])
+    for _ in range(40):
+        # rows that ended are admitted again behind the prefix
+        h = held.cpu().numpy()
+        for b in np.flatnonzero((h == 0) & (rng.rand(B) < 0.7)):
+            tables[b, :P], held[b], shared[b] = i32(prefix), P, P
+        h = held.cpu().numpy()
+        lens = np.where(rng.rand(B) < 0.2, 0, rng.randint(1, mb * bs + 1, B))
+        lens = np.where(h == 0, 0, lens)
+        pda.kv_assign_blocks(tables, held, free, count, i32(lens), bs, shared_blocks=shared,
+                             error_word=err)
+        bits = int(err.item())
+        assert bits in (0, binding.PDA_DEVERR_NO_BLOCKS)
+        err.zero_()
+        h, t, s = held.tolist(), tables.cpu().numpy(), shared.tolist()
+        own = []
+        for b in range(B):
+            at = min(s[b], h[b])
+            assert t[b, :at].tolist() == prefix[:at]
+            own += t[b, at:h[b]].tolist()
+        assert sorted(own + free[:int(count)].tolist()) == list(range(P, NB))
