@@ -77,10 +77,11 @@ pda_status launch_chunk(void* out, const void* q, const void* k_cache, const voi
   int dev, sms;
   const pda_status dst = current_device_sms(&dev, &sms);
   if (dst != PDA_OK) return dst;
-  if (sm_cap > 0 && sm_cap < sms) sms = sm_cap;
+  const bool capped = sm_cap > 0 && sm_cap < sms;
+  if (capped) sms = sm_cap;
   if (workspace_bytes < chunk_workspace(sms, D)) return PDA_ERR_WORKSPACE;
-  return kv_dtype == PDA_F32 ? launch_chunk_f32(p, D, dev, sms, workspace, stream)
-                             : launch_chunk_tc(p, D, kv_dtype, dev, sms, workspace, stream);
+  return kv_dtype == PDA_F32 ? launch_chunk_f32(p, D, dev, sms, capped, workspace, stream)
+                             : launch_chunk_tc(p, D, kv_dtype, dev, sms, capped, workspace, stream);
 }
 
 }  // namespace

@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(256, 1)
 }
 
 template <int D>
-pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaStream_t stream) {
+pda_status launch(const ChunkParams& p, int dev, int sms, bool capped, float* partial,
+                  cudaStream_t stream) {
   constexpr int smem = static_cast<int>(sizeof(Smem<D>));
   static_assert(smem <= 232448, "227 KB a block");
   static std::atomic<bool> raised[64];
@@ -280,16 +281,16 @@ pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaSt
   const int grid = chunk_grid<CutsOf>(p, g_shift, sms);
   chunk_f32_kernel<D><<<grid, 256, smem, stream>>>(p, g_shift, partial);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
-  return launch_merge<D, float, CutsOf>(p, g_shift, partial, grid, stream);
+  return launch_merge<D, float, CutsOf>(p, g_shift, partial, grid, capped, stream);
 }
 
 }  // namespace
 
-pda_status launch_chunk_f32(const ChunkParams& p, int D, int dev, int sms, void* workspace,
-                            cudaStream_t stream) {
+pda_status launch_chunk_f32(const ChunkParams& p, int D, int dev, int sms, bool capped,
+                            void* workspace, cudaStream_t stream) {
   float* partial = static_cast<float*>(workspace);
-  return D == 128 ? launch<128>(p, dev, sms, partial, stream)
-                  : launch<64>(p, dev, sms, partial, stream);
+  return D == 128 ? launch<128>(p, dev, sms, capped, partial, stream)
+                  : launch<64>(p, dev, sms, capped, partial, stream);
 }
 
 }  // namespace pda

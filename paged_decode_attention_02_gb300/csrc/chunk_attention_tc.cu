@@ -1183,7 +1183,8 @@ pda_status encode_v(CUtensorMap* tm, const void* base, long long rows, int heads
 }
 
 template <int D, bool kBf16, bool kFp8>
-pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaStream_t stream) {
+pda_status launch(const ChunkParams& p, int dev, int sms, bool capped, float* partial,
+                  cudaStream_t stream) {
   constexpr size_t smem = smem_bytes<D, kFp8>();
   static std::atomic<bool> raised[64];
   if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
@@ -1210,13 +1211,13 @@ pda_status launch(const ChunkParams& p, int dev, int sms, float* partial, cudaSt
                                                                     partial);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
   using Out = std::conditional_t<kBf16, __nv_bfloat16, __half>;
-  return launch_merge<D, Out, CutsOf>(p, g_shift, partial, grid, stream);
+  return launch_merge<D, Out, CutsOf>(p, g_shift, partial, grid, capped, stream);
 }
 
 }  // namespace
 
 pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int dev, int sms,
-                           void* workspace, cudaStream_t stream) {
+                           bool capped, void* workspace, cudaStream_t stream) {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -1229,13 +1230,13 @@ pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int 
   float* partial = static_cast<float*>(workspace);
   const bool wide = D == 128;
   if (kv_dtype == PDA_BF16)
-    return wide ? launch<128, true, false>(p, dev, sms, partial, stream)
-                : launch<64, true, false>(p, dev, sms, partial, stream);
+    return wide ? launch<128, true, false>(p, dev, sms, capped, partial, stream)
+                : launch<64, true, false>(p, dev, sms, capped, partial, stream);
   if (kv_dtype == PDA_F16)
-    return wide ? launch<128, false, false>(p, dev, sms, partial, stream)
-                : launch<64, false, false>(p, dev, sms, partial, stream);
-  return wide ? launch<128, true, true>(p, dev, sms, partial, stream)
-              : launch<64, true, true>(p, dev, sms, partial, stream);
+    return wide ? launch<128, false, false>(p, dev, sms, capped, partial, stream)
+                : launch<64, false, false>(p, dev, sms, capped, partial, stream);
+  return wide ? launch<128, true, true>(p, dev, sms, capped, partial, stream)
+              : launch<64, true, true>(p, dev, sms, capped, partial, stream);
 }
 
 }  // namespace pda

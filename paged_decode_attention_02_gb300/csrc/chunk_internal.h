@@ -22,11 +22,12 @@ struct ChunkParams {
 // Workspace bytes on `sms` SMs: two cut items' partial results a block.
 size_t chunk_workspace(int sms, int D);
 
-// 16-bit and FP8 caches, on the tensor cores.
+// 16-bit and FP8 caches, on the tensor cores. No kernel of the call has more than `sms` blocks
+// where it is `capped` to them.
 pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int dev, int sms,
-                           void* workspace, cudaStream_t stream);
+                           bool capped, void* workspace, cudaStream_t stream);
 // fp32 caches.
-pda_status launch_chunk_f32(const ChunkParams& p, int D, int dev, int sms, void* workspace,
-                            cudaStream_t stream);
+pda_status launch_chunk_f32(const ChunkParams& p, int D, int dev, int sms, bool capped,
+                            void* workspace, cudaStream_t stream);
 
 }  // namespace pda

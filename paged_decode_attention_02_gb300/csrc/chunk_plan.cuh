@@ -177,17 +177,22 @@ __device__ __forceinline__ void store4(float* p, float a, float b, float c, floa
 // Block x handles the item that cut x + 1 falls into, if that is the first cut inside it:
 // piece i of a row holds (m_i, l_i, O_i); with M = max m_i the row is
 // sum O_i 2^(m_i - M) / sum l_i 2^(m_i - M). A lane takes a row, a warp 32 rows and every
-// eighth group of four columns.
-constexpr int kMergeRows = 32;  // rows of a block
+// eighth group of four columns. Eight warps share 32 rows; an item's rows are spread over the
+// grid's y or, in a capped call, over the warps of one block a cut and a loop, so that there are
+// no more blocks than the cap has SMs.
+constexpr int kMergeRows = 32;
+constexpr int kMergeThreads = 256;  // of 32 rows
 
 template <int D, typename Out, typename C>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     chunk_merge_kernel(const ChunkParams p, int g_shift, float* partial, int grid) {
   __shared__ PlanMemory mem;
   const int lt = C::kRowsLog2 - g_shift;
   const Plan pl = make_plan<C>(p, lt, grid, &mem);
   const int c = blockIdx.x + 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 7;
+  const int sets = static_cast<int>(blockDim.x) / kMergeThreads;
+  const int first = (blockIdx.y * sets + threadIdx.x / kMergeThreads) * kMergeRows;
   int pieces = 0, rows = 0;
   Where w{};
   if (c < pl.workers) {
@@ -208,41 +213,41 @@ __global__ void __launch_bounds__(256)
     rows = __shfl_sync(kFullMask, rows, 0);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
-  const int r = blockIdx.y * kMergeRows + lane;
-  if (pieces == 0 || blockIdx.y * kMergeRows >= rows) return;
+  if (first >= rows) return;
   const int row0 = __shfl_sync(kFullMask, w.q.row0 + (w.i << lt), 0);
   const int kh = __shfl_sync(kFullMask, w.kh, 0);
-  if (r >= rows) return;
   auto slot = [&](int i) { return i == 0 ? 2 * (c - 1) + 1 : 2 * (c + i - 1); };
-  float M = -INFINITY;
+  for (int r = first + lane; r < rows; r += gridDim.y * sets * kMergeRows) {
+    float M = -INFINITY;
 #pragma unroll 4
-  for (int i = 0; i < pieces; ++i) M = fmaxf(M, part_ml(partial, slot(i), D)[r].x);
-  constexpr int V = D / 32;  // groups of four columns of a warp
-  float l = 0.f;
-  float4 acc[V] = {};
+    for (int i = 0; i < pieces; ++i) M = fmaxf(M, part_ml(partial, slot(i), D)[r].x);
+    constexpr int V = D / 32;  // groups of four columns of a warp
+    float l = 0.f;
+    float4 acc[V] = {};
 #pragma unroll 2
-  for (int i = 0; i < pieces; ++i) {
-    const float2 ml = part_ml(partial, slot(i), D)[r];
-    if (ml.x == -INFINITY && !isnan(ml.y)) continue;  // the row sees none of the piece's keys
-    const float wgt = ex2(ml.x - M);
-    l = fmaf(wgt, ml.y, l);
+    for (int i = 0; i < pieces; ++i) {
+      const float2 ml = part_ml(partial, slot(i), D)[r];
+      if (ml.x == -INFINITY && !isnan(ml.y)) continue;  // the row sees none of the piece's keys
+      const float wgt = ex2(ml.x - M);
+      l = fmaf(wgt, ml.y, l);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float4 o = part_o(partial, slot(i), D)[(warp + 8 * e) * 256 + r];
-      acc[e].x = fmaf(wgt, o.x, acc[e].x);
-      acc[e].y = fmaf(wgt, o.y, acc[e].y);
-      acc[e].z = fmaf(wgt, o.z, acc[e].z);
-      acc[e].w = fmaf(wgt, o.w, acc[e].w);
+      for (int e = 0; e < V; ++e) {
+        const float4 o = part_o(partial, slot(i), D)[(warp + 8 * e) * 256 + r];
+        acc[e].x = fmaf(wgt, o.x, acc[e].x);
+        acc[e].y = fmaf(wgt, o.y, acc[e].y);
+        acc[e].z = fmaf(wgt, o.z, acc[e].z);
+        acc[e].w = fmaf(wgt, o.w, acc[e].w);
+      }
     }
-  }
-  const float inv = p.v_scale / l;
-  Out* out = static_cast<Out*>(p.out) +
-             ((static_cast<size_t>(row0) + (r >> g_shift)) * p.H + (kh << g_shift) +
-              (r & ((1 << g_shift) - 1))) * D;
+    const float inv = p.v_scale / l;
+    Out* out = static_cast<Out*>(p.out) +
+               ((static_cast<size_t>(row0) + (r >> g_shift)) * p.H + (kh << g_shift) +
+                (r & ((1 << g_shift) - 1))) * D;
 #pragma unroll
-  for (int e = 0; e < V; ++e)
-    store4(out + 4 * (warp + 8 * e), acc[e].x * inv, acc[e].y * inv, acc[e].z * inv,
-           acc[e].w * inv);
+    for (int e = 0; e < V; ++e)
+      store4(out + 4 * (warp + 8 * e), acc[e].x * inv, acc[e].y * inv, acc[e].z * inv,
+             acc[e].w * inv);
+  }
 }
 
 // ---------------------------------------------------------------- host side
@@ -264,20 +269,23 @@ int chunk_grid(const ChunkParams& p, int g_shift, int sms) {
   return chunk_workers(chunk_units<C>(p, g_shift), sms, C::kWorkerUnits);
 }
 
-// Merges what the kernel before it on the stream has cut, where anything can have been.
+// Merges what the kernel before it on the stream has cut, where anything can have been. Without
+// a cap the merge starts early and looks its items up beside that kernel's last blocks; with one
+// (`capped`) it waits for its end, and its grid - 1 blocks fit the cap that `grid` keeps to.
 template <int D, typename Out, typename C>
-pda_status launch_merge(const ChunkParams& p, int g_shift, float* partial, int grid,
+pda_status launch_merge(const ChunkParams& p, int g_shift, float* partial, int grid, bool capped,
                         cudaStream_t stream) {
   if (grid == 1 || chunk_tiles(p) < 2 * C::kPieceTiles) return PDA_OK;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid - 1), (1 << C::kRowsLog2) / kMergeRows);
-  cfg.blockDim = dim3(256);
+  constexpr int kSets = (1 << C::kRowsLog2) / kMergeRows;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid - 1), capped ? 1 : kSets);
+  cfg.blockDim = dim3((capped ? std::min(kSets, 4) : 1) * kMergeThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = capped ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D, Out, C>, p, g_shift, partial, grid) ==
                  cudaSuccess
              ? PDA_OK
