@@ -496,8 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             static_cast<const uint16_t*>(p.q) +
             ((static_cast<size_t>(d.row0) + there) * p.H + (d.kh << g_shift) +
              (packed & ((1 << g_shift) - 1))) * D);
-        sl = fmaxf(least, sl * scale_q_row<D>(src, qs + (single ? 0 : g * C::kTile), row,
-                                              g == 0 || !single));
+        const float back = scale_q_row<D>(src, qs + (single ? 0 : g * C::kTile), row,
+                                          g == 0 || !single);
+        // times the row's factor, up to 2^113, the floor of a scale of zero would count
+        sl = p.scale_log2 == 0.f ? least : fmaxf(least, sl * back);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(g == 0 ? &ms.q_full : &ms.q_full1);

@@ -1,4 +1,5 @@
-"""Chunk attention at the edges of its arguments: what a call may occupy under an SM cap."""
+"""Chunk attention at the edges of its arguments: what a call may occupy under an SM
+cap, a scale of zero."""
 import ctypes
 
 import pytest
@@ -80,3 +81,16 @@ def test_capped_calls_stay_within_their_cap(kv, sm_cap):
         lambda s: c.call(out, check=False, workspace=ws, sm_cap=sm_cap, stream=s))
     assert len(blocks) == (1 if sm_cap == 1 else 2)
     assert max(blocks) <= sm_cap and not overlap
+
+
+def test_fp8_scale_of_zero_over_the_largest_q():
+    """With a scale of zero every visible key counts the same, whatever q is: keys and values
+    of two signs, turn about, have a mean of zero at every odd position."""
+    c = Chunk([64], [64], "fp8", H=2, H_kv=1, seed=0)
+    c.scale = 0.0
+    c.q.fill_(3e38)
+    sign = torch.arange(c.bs, device="cuda") % 2 == 0
+    code = torch.where(sign, 0x7E, 0xFE).to(torch.uint8)  # 448 and -448
+    for cache in (c.k, c.v):
+        cache[:] = code[None, :, None, None]
+    c.assert_close(c.call())
