@@ -127,18 +127,6 @@ static_assert(smem_bytes<128, false>() <= 232448 && smem_bytes<64, false>() <= 2
               "227 KB a block");
 
 // ---------------------------------------------------------------- the block's pipeline
-// A wait of a whole (converged) warp, each lane for its own barrier and parity; false for all
-// lanes after kWaitLimitNs. The vote inside the loop keeps the warp together: a loop per lane
-// with one vote behind it took a fifth longer to get through when there was nothing to wait for.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
-  const unsigned long long t0 = __shfl_sync(kFullMask, global_timer_ns(), 0);
-  while (true) {
-    if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
-    if (__shfl_sync(kFullMask, global_timer_ns(), 0) - t0 > kWaitLimitNs) return false;
-  }
-}
-
 // The ids of a piece's blocks, 32 at a time: lane l holds that of block l % nbt of tile
 // l / nbt of the current group of tiles, the next group's already under way.
 struct BlockIds {

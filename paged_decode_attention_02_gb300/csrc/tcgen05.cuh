@@ -154,6 +154,18 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
                : "memory");
 }
 
+// A wait of a whole (converged) warp, each lane for its own barrier and parity; false for all
+// lanes after kWaitLimitNs. The vote inside the loop keeps the warp together: a loop per lane
+// with one vote behind it took a fifth longer to get through when there was nothing to wait for.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = __shfl_sync(kFullMask, global_timer_ns(), 0);
+  while (true) {
+    if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+    if (__shfl_sync(kFullMask, global_timer_ns(), 0) - t0 > kWaitLimitNs) return false;
+  }
+}
+
 template <int kRegs>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));

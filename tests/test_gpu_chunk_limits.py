@@ -1,12 +1,13 @@
-"""Chunk attention at the edges of its arguments: what a call may occupy under an SM
-cap, a scale of zero."""
+"""Chunk attention at the edges of its arguments: what a call may occupy under an SM cap, a
+scale of zero, more requests than the plan numbers singly, calls on streams of their own."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
 import paged_decode_attention_02_gb300 as pda
-from chunk_common import Chunk
+from chunk_common import Chunk, i32
 from paged_decode_attention_02_gb300 import binding
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +95,56 @@ def test_fp8_scale_of_zero_over_the_largest_q():
     for cache in (c.k, c.v):
         cache[:] = code[None, :, None, None]
     c.assert_close(c.call())
+
+
+@pytest.mark.parametrize("kv", ["f32", "bf16", "f16", "fp8"])
+@pytest.mark.parametrize("B,sm_cap", [(257, 0), (700, 0), (700, 3), (1500, 0)])
+def test_more_requests_than_the_plan_numbers_singly(kv, B, sm_cap):
+    """Above 256 requests the plan counts them in chunks and walks within one; empty and padded
+    requests lie between the others."""
+    rng = np.random.RandomState(B)
+    n = rng.choice([0, 1, 1, 2, 5, 33], B)
+    past = rng.choice([0, 3, 100, 127, 128, 700], B)
+    n[100], past[100] = 300, 2500
+    c = Chunk(n, past, kv, H=4, H_kv=2, D=64, seed=B, pad_rows=2)
+    lens, ref = c.L.copy(), c.reference()
+    out_rows = []
+    for b in range(3, B, 50):
+        lens[b] = 0
+        out_rows += list(range(int(c.start_np[b]), int(c.start_np[b + 1])))
+    out = c.call(lens=i32(lens), sm_cap=sm_cap)
+    assert (out[out_rows] == 0).all() and (out[c.T:] == 7).all()
+    for t in ref:
+        t[out_rows] = 0
+    c.assert_close(out, ref)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_as_many_requests_as_a_call_takes(kv):
+    c = Chunk([1] * 8192, [b % 40 for b in range(8192)], kv, H=2, H_kv=1, D=64, seed=1)
+    c.assert_close(c.call())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_calls_on_two_streams_at_once(kv):
+    """Each stream's calls repeat bit for bit what the call gives alone. Outputs are filled on
+    the stream that writes them, and kept until both are done."""
+    a = Chunk([200, 1, 50], [800, 3000, 0], kv, seed=1)
+    b = Chunk([1] * 20, list(range(100, 2100, 100)), kv, seed=2)
+    rounds, jobs = 10, []
+    for c in (a, b):
+        ws = pda.alloc_chunk_workspace(c.B, c.T, c.H, c.H_kv, c.D, c.bs, c.k.dtype, 76)
+        alone = c.call(workspace=ws, sm_cap=76)
+        c.assert_close(alone)
+        jobs.append((c, ws, alone, [torch.empty_like(c.q) for _ in range(rounds)],
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(rounds):
+        for c, ws, _, outs, stream in jobs:
+            with torch.cuda.stream(stream):
+                outs[i].fill_(7.0)
+            c.call(outs[i], check=False, workspace=ws, sm_cap=76, stream=stream)
+    torch.cuda.synchronize()
+    for c, _, alone, outs, _ in jobs:
+        pda.check_error(c.err)
+        assert all(torch.equal(o, alone) for o in outs)
