@@ -552,7 +552,7 @@ pda_status pda_chunk_attention_workspace_size(int B, int T, int H, int H_kv, int
  *      out = sum_t softmax(s)_t * V_t[k].
  * n == 1 is pda_paged_decode_attention's row.
  *
- *  out, q         [T, H, D] in q_dtype: the step's tokens, request after request. Rows
+ *  out, q         [T, H, D], both in q_dtype: the step's tokens, request after request. Rows
  *                 outside [query_start[0], query_start[B]) are neither computed nor written.
  *  query_start    [B + 1] int32 (device), non-decreasing, within [0, T].
  *  context_lens   [B] int32 (device). L == 0 gives zero rows (a padded request). L < 0,
@@ -587,7 +587,10 @@ pda_status pda_paged_chunk_attention(void* out, const void* q, const void* k_cac
 /*
  * pda_paged_chunk_attention_fp8 -- pda_paged_chunk_attention over an FP8 E4M3 cache: stored
  * code c of K means decode(c) * k_scale, of V decode(c) * v_scale (finite per-tensor scales).
- * Codes are widened exactly; q and out are PDA_BF16, and the products run as for a bf16 cache.
+ * q and out are PDA_BF16. Both products run with fp16 operands and fp32 accumulation: the codes
+ * are widened exactly, each row of q (of a token and head) is scaled by a power of two that puts
+ * its largest element at 2^14 and rounded to fp16 (elements below 2^-28 of that largest lose
+ * bits, those below 2^-38 of it count as zero), and the probabilities are rounded to fp16.
  */
 pda_status pda_paged_chunk_attention_fp8(void* out, const void* q, const void* k_cache,
                                          const void* v_cache, const int32_t* block_tables,

@@ -6,8 +6,10 @@
 // x + 16 j of a 64-key step, of the output the columns 4 x + 64 j. Q, two K and V steps
 // (cp.async, one in flight) and the probabilities lie in shared memory; a row's maximum and
 // sum are reduced over the 16 threads that share it.
-// Bound by fp32 arithmetic and, in short batches, by rows padded to 64: two 256-token chunks on
-// 1024 of 32/8 heads run at 28.6 TFLOP/s (338 us).
+// Two 256-token chunks on 1024 of 32/8 heads run at 28.6 TFLOP/s (338 us), 38 % of the fp32
+// lanes' rate. Bound by shared-memory loads (69 % of their rate while an SM works, the multiply-
+// adds 51 %: a 4 x 4 tile loads eight 16-byte pieces for 64 of them), by SMs that end early (a
+// quarter of their time) and, in short batches, by rows padded to 64.
 #include <atomic>
 
 #include "chunk_plan.cuh"

@@ -8,11 +8,12 @@
 // m, l and O stay in fp32; the probabilities are rounded to the operands' 16-bit type for the
 // P V product (the matrix instruction takes no wider operand with 16-bit V).
 //
-// What bounds it: 4096 tokens on 12288 of 32/8 heads run at 1680 TFLOP/s (573 us, 86 % of the
-// measured GEMM rate), the tensor pipe 73 % busy: Q K's two operands come from shared memory,
-// 128 bytes a cycle, and one warp hands the pipe from group to group. 32 requests of 1 to 8
-// tokens over up to 8192 stream 5.7 TB/s (120 us, 85 % of the copy peak). Eight warps of softmax
-// with a thread per row need no shuffles; more do not fit TMEM's 512 columns.
+// What bounds it: 4096 tokens on 12288 of 32/8 heads run at 1592 TFLOP/s under the power cap (604
+// us, 90 % of the measured sustained GEMM rate) and 570 us before it sets in (86 % of the burst
+// rate), the tensor pipe 73 % busy: Q K's two operands come from shared memory, 128 bytes a cycle,
+// and one warp hands the pipe from group to group. 32 requests of 1 to 8 tokens over up to 8192
+// stream 5.7 TB/s (120 us, 85 % of the copy peak). Eight warps of softmax with a thread per row
+// need no shuffles; with score tiles of 128 keys more do not fit TMEM's 512 columns.
 //
 // One block per SM walks a contiguous range of the launch's units (chunk_plan.h). Warps:
 //   0-3, 4-7  softmax of row group 0 and 1 (a thread per row: TMEM lane = row)
@@ -23,15 +24,20 @@
 //   12-15     clean the V tiles at the diagonal and the end (see below), or, over an FP8
 //             cache, widen every K and V tile: the TMA brings the codes, these warps write
 //             them as fp16 (exact, and one instruction for two codes, where bf16 took four:
-//             365 -> 341 us on three chunks of up to 2048 tokens; 312 with K and V through
+//             365 -> 341 us on three chunks of up to 2048 tokens; 311 with K and V through
 //             one copy of the loop) where the products read them. The softmax warps then
 //             bring Q, each row scaled by a power of two that puts its largest value at
-//             2^14: what falls under fp16's smallest step is below 2^-38 of that value.
+//             2^14: elements below 2^-28 of that value are subnormal and lose bits, and
+//             what falls under fp16's smallest step is below 2^-38 of it.
 // The softmax warps take the registers that the others give back (setmaxnreg).
 // An item of more than 128 rows gives each group 128 rows; both read every K and V tile. An
 // item of fewer gives both groups the same rows and alternate tiles, merged at the end, so
 // that one group's softmax still runs under the other's products.
-// TMEM: S0 | S1 | O0 | O1, 128 columns each; P overwrites the first 64 columns of its S.
+// TMEM: S0 | S1 | O0 | O1, 128 columns each; P overwrites the first 64 columns of its S. The next
+// Q K then overwrites P, with nothing but the order of issue between it and the P V that reads P:
+// the kernel relies on matrix instructions of one thread running in that order, which PTX states
+// for equal accumulators and shapes only. A commit and a wait between them took 634 us for 562 on
+// the large chunk, 142 for 136 on ragged prompts.
 //
 // V tiles that reach past what some row may see (the diagonal ones) multiply zero
 // probabilities with later tokens' V, or with whatever lies behind the last token; 0 * NaN
@@ -453,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // never 0: masked scores are -inf times this
     const float least = __uint_as_float(1), sl_all = fmaxf(fabsf(p.scale_log2), least);
     // fp16 probabilities are kept 2^4 higher (the factor cancels in O / l): with the
-    // reference up to 2^8 below the maximum they stay below 2^13, and fewer are subnormal
+    // reference up to 2^8 below the maximum they stay below 2^13, and only those under 2^-18 of
+    // the reference are subnormal
     const float lift = kOpBf16 ? 0.f : 4.f;
     unsigned s_phase = 0, o_phase = 0, m_phase = 0;
     for (int item = 0; !timed_out; ++item) {
@@ -910,7 +917,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
-        // Group g's P V of step s and its Q K of the next, issued back to back. Their three
+        // Group g's P V of step s and its Q K of the next, issued back to back and run in that
+        // order (see TMEM above: the second writes where the first reads). Their three
         // barriers are polled at once, a lane each: one wait after the other left the tensor
         // core idle for a fifth of the time.
         auto step = [&](int g, int s, int n) {
