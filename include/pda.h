@@ -530,6 +530,77 @@ pda_status pda_kv_build_slots(int32_t* slot_mapping, int32_t* query_start,
                               cudaStream_t stream);
 
 /*
+ * pda_kv_build_slots_positions -- pda_kv_build_slots, and the position p of every new token in
+ * its request (what pda_qk_norm_rope_append turns its queries and keys by).
+ *
+ *  positions      [N] int32, written whole: 0 for rows behind the last token and for the tokens
+ *                 of a request in error or padded. Everything else as pda_kv_build_slots.
+ */
+pda_status pda_kv_build_slots_positions(int32_t* slot_mapping, int32_t* positions,
+                                        int32_t* query_start, const int32_t* query_lens,
+                                        const int32_t* context_lens, const int32_t* block_tables,
+                                        int N, int B, int max_blocks_per_seq, int block_size,
+                                        int num_blocks, int32_t* error_word,
+                                        cudaStream_t stream);
+
+/*
+ * pda_qk_norm_rope_append -- the queries and keys of a step's new tokens, normed per head and
+ * turned by their positions, and the keys and values written into their cache slots, in one pass:
+ * what comes between a layer's projections and its attention, with pda_kv_append's write.
+ *
+ * The pages give no position encoding; the shapes and slots are pda_kv_append's (page
+ * "Disaggregated LLM Serving: from PD disaggregation to attention offload", sec. 1). Each head row
+ * x [D] of q and k, in fp32 and rounded once at the end:
+ *  - with a weight w [D]:  x = x / sqrt(mean(x^2) + eps) * w   (q_weight for q, k_weight for k);
+ *  - the first R = rope_dim elements turn in pairs by the angle of the token's position p:
+ *      (a, b) -> (a c - b s, b c + a s),  c, s = attention_factor * cos, sin (2 pi p F_i / 2^64),
+ *    pair i < R / 2 being elements (i, i + R / 2), or (2 i, 2 i + 1) where `interleaved` is not 0.
+ * v is copied. k and v of token t go to slot_mapping[t] as by pda_kv_append (< 0: not written;
+ * too large: PDA_DEVERR_SLOT, not written); q_out is written for every token.
+ *
+ *  q_out          [T, H, D] in dtype, dense. May be q itself where q is dense.
+ *  q, k, v        [T, H, D], [T, H_kv, D], [T, H_kv, D] in dtype; a token's heads are dense, and
+ *                 tokens are q_stride, k_stride, v_stride elements apart (slices of one
+ *                 projection's output need no copy). Strides a multiple of 16 bytes, no smaller
+ *                 than a token.
+ *  k_cache,v_cache [num_blocks, block_size, H_kv, D] in kv_dtype, updated in place; kv_dtype is
+ *                 dtype (PDA_F32, PDA_BF16, PDA_F16), or PDA_FP8_E4M3 with dtype PDA_BF16: then
+ *                 the code nearest to x * (1 / k_scale) (v: 1 / v_scale) in fp32, no larger than
+ *                 448, is stored.
+ *  positions      [T] int32, any value.
+ *  freqs          [rope_dim / 2] uint64: F_i, turns per position as a fraction of 2^64.
+ *                 p F_i modulo 2^64 is exact, so far positions lose nothing.
+ *  q_weight, k_weight [D] in dtype, each may be NULL (no norm).
+ *  Supported: D a multiple of 8 up to 256; rope_dim a multiple of 16 up to D (0: no rotation);
+ *  H, H_kv <= 16384. Pointers 16-byte aligned. Scales and their
+ *  reciprocals finite. Inputs and outputs do not
+ *  overlap otherwise. T == 0 is a no-op.
+ */
+pda_status pda_qk_norm_rope_append(void* q_out, const void* q, const void* k, const void* v,
+                                   long long q_stride, long long k_stride, long long v_stride,
+                                   void* k_cache, void* v_cache, const int32_t* slot_mapping,
+                                   const int32_t* positions, const uint64_t* freqs, int rope_dim,
+                                   int interleaved, float attention_factor, const void* q_weight,
+                                   const void* k_weight, float eps, int T, int H, int H_kv, int D,
+                                   int block_size, int num_blocks, float k_scale, float v_scale,
+                                   pda_dtype dtype, pda_dtype kv_dtype, int32_t* error_word,
+                                   cudaStream_t stream);
+
+/*
+ * pda_qk_norm_rope -- the same norm and rotation into dense rows, without a cache (for keys that
+ * are quantised further before they are appended).
+ *
+ *  q_out, k_out   [T, H, D], [T, H_kv, D] in dtype, dense; may be q and k themselves where those
+ *                 are dense. Everything else as pda_qk_norm_rope_append.
+ */
+pda_status pda_qk_norm_rope(void* q_out, void* k_out, const void* q, const void* k,
+                            long long q_stride, long long k_stride, const int32_t* positions,
+                            const uint64_t* freqs, int rope_dim, int interleaved,
+                            float attention_factor, const void* q_weight, const void* k_weight,
+                            float eps, int T, int H, int H_kv, int D, pda_dtype dtype,
+                            cudaStream_t stream);
+
+/*
  * pda_chunk_attention_workspace_size -- bytes of device workspace pda_paged_chunk_attention
  * (or _fp8, with PDA_FP8_E4M3) needs on the current device for these sizes. The bound does
  * not depend on the lengths. Written to *bytes (host).

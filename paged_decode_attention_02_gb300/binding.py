@@ -8,6 +8,7 @@ fails to load, every call raises, and nothing falls back to another implementati
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -33,7 +34,8 @@ EXPORTED = [
     "pda_kv_append_block_scales", "pda_kv_pack_block_scales_batched",
     "pda_kv_unpack_block_scales_batched", "pda_kv_assign_blocks", "pda_kv_build_slots",
     "pda_chunk_attention_workspace_size", "pda_paged_chunk_attention",
-    "pda_paged_chunk_attention_fp8",
+    "pda_paged_chunk_attention_fp8", "pda_kv_build_slots_positions", "pda_qk_norm_rope_append",
+    "pda_qk_norm_rope",
 ]
 
 _lock = threading.Lock()
@@ -111,6 +113,17 @@ def load():
         lib.pda_kv_assign_blocks.restype = I
         lib.pda_kv_build_slots.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P]
         lib.pda_kv_build_slots.restype = I
+        lib.pda_kv_build_slots_positions.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P]
+        lib.pda_kv_build_slots_positions.restype = I
+        # q_out, q, k, v, strides, caches, slots, positions, freqs, rope_dim, interleaved,
+        # factor, weights, eps, T, H, H_kv, D, bs, NB, scales, dtypes, error_word, stream
+        LL = ctypes.c_longlong
+        lib.pda_qk_norm_rope_append.argtypes = [P, P, P, P, LL, LL, LL, P, P, P, P, P, I, I, F, P,
+                                                P, F, I, I, I, I, I, I, F, F, I, I, P, P]
+        lib.pda_qk_norm_rope_append.restype = I
+        lib.pda_qk_norm_rope.argtypes = [P, P, P, P, LL, LL, P, P, I, I, F, P, P, F, I, I, I, I, I,
+                                         P]
+        lib.pda_qk_norm_rope.restype = I
         lib.pda_chunk_attention_workspace_size.argtypes = [I, I, I, I, I, I, I, I,
                                                            ctypes.POINTER(SZ)]
         lib.pda_chunk_attention_workspace_size.restype = I
@@ -531,22 +544,148 @@ def kv_assign_blocks(block_tables, blocks_held, free_list, free_count, context_l
 
 
 def kv_build_slots(slot_mapping, query_start, query_lens, context_lens, block_tables,
-                   block_size: int, num_blocks: int, error_word=None, stream=None):
+                   block_size: int, num_blocks: int, error_word=None, stream=None,
+                   positions=None):
     """Fill ``slot_mapping`` ([N] int32, for ``kv_append``) and ``query_start`` ([B + 1], for
     ``paged_chunk_attention``) from ``query_lens`` new tokens of ``context_lens`` per request;
-    rows of ``slot_mapping`` behind the last token get -1."""
+    rows of ``slot_mapping`` behind the last token get -1. ``positions`` ([N] int32, for
+    ``qk_norm_rope_append``), where given, gets each token's position in its request."""
     _require(block_tables.dim() == 2 and slot_mapping.dim() == 1,
              "block_tables must be [B, max_blocks] and slot_mapping [N]")
     B, max_blocks = block_tables.shape
     dev, i32, b = _cuda_index(query_start), torch.int32, (B,)
-    _call(load().pda_kv_build_slots, "pda_kv_build_slots", dev, stream,
-          _addr(slot_mapping, dev, "slot_mapping", i32),
-          _addr(query_start, dev, "query_start", i32, (B + 1,)),
-          _addr(query_lens, dev, "query_lens", i32, b),
-          _addr(context_lens, dev, "context_lens", i32, b),
-          _addr(block_tables, dev, "block_tables", i32), slot_mapping.shape[0], B, max_blocks,
-          int(block_size), int(num_blocks), _addr(error_word, dev, "error_word"))
+    args = (_addr(query_start, dev, "query_start", i32, (B + 1,)),
+            _addr(query_lens, dev, "query_lens", i32, b),
+            _addr(context_lens, dev, "context_lens", i32, b),
+            _addr(block_tables, dev, "block_tables", i32), slot_mapping.shape[0], B, max_blocks,
+            int(block_size), int(num_blocks), _addr(error_word, dev, "error_word"))
+    slots = _addr(slot_mapping, dev, "slot_mapping", i32)
+    if positions is None:
+        _call(load().pda_kv_build_slots, "pda_kv_build_slots", dev, stream, slots, *args)
+    else:
+        _call(load().pda_kv_build_slots_positions, "pda_kv_build_slots_positions", dev, stream,
+              slots, _addr(positions, dev, "positions", i32, slot_mapping.shape), *args)
     return slot_mapping
+
+
+def rope_frequencies(rope_dim: int, base: float = 10000.0, stretch: float = 1.0,
+                     original_length: int | None = None, low_turns: float = 1.0,
+                     high_turns: float = 32.0, inv_freq=None, device=None) -> torch.Tensor:
+    """The frequencies ``qk_norm_rope_append`` turns by: [rope_dim / 2] int64, turns per position
+    as a 64-bit fraction of a turn. Pair i turns ``base ** (-2 i / rope_dim)`` radians a position
+    (or ``inv_freq[i]``), slowed for longer contexts by ``stretch``: all pairs alike (position
+    interpolation), or, with ``original_length``, by parts (the YaRN paper's interpolation): pairs
+    that turn less than ``low_turns`` times within it are slowed, those that turn ``high_turns``
+    times or more are kept, those between mix both linearly in their turns. (That paper's
+    ``attention_factor`` is ``0.1 * log(stretch) + 1``.)"""
+    _require(rope_dim >= 0 and rope_dim % 2 == 0, "rope_dim must be even")
+    _require(stretch > 0 and high_turns > low_turns, "stretch > 0 and high_turns > low_turns")
+    if inv_freq is None:
+        inv_freq = [float(base) ** (-2 * i / rope_dim) for i in range(rope_dim // 2)]
+    _require(len(inv_freq) == rope_dim // 2, "inv_freq must hold rope_dim / 2 values")
+    out = []
+    for f in map(float, inv_freq):
+        _require(math.isfinite(f), "frequencies must be finite")
+        keep = 0.0
+        if original_length is not None:
+            turns = original_length * f / (2 * math.pi)
+            keep = min(1.0, max(0.0, (turns - low_turns) / (high_turns - low_turns)))
+        f = f * keep + f / stretch * (1 - keep)
+        n = round(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64
+        out.append(n - 2 ** 64 if n >= 2 ** 63 else n)
+    return torch.tensor(out, dtype=torch.int64, device=device or "cuda")
+
+
+def _heads(t, dev: int, name: str, dtype, shape):
+    """Address, token stride and end of head rows [T, heads, D]: a token's heads dense, tokens
+    any distance apart."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}; all tensors must live on one CUDA device")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
+    T, n, D = shape
+    row, at = n * D, t.data_ptr()
+    if T == 0:
+        return at, row, at
+    by_token, by_head, by_element = t.stride()
+    if (D > 1 and by_element != 1) or (n > 1 and by_head != D):
+        raise ValueError(f"{name}: a token's heads must be dense")
+    if T == 1:
+        by_token = row
+    return at, by_token, at + ((T - 1) * by_token + row) * t.element_size()
+
+
+def _apart(out: int, size: int, other, name: str, may_be_same: int = -1):
+    """Refuses an output of ``size`` bytes that overlaps ``other`` (as from ``_heads``), unless it
+    is the same memory and ``other``'s tokens are ``may_be_same`` apart."""
+    at, stride, end = other
+    if out < end and at < out + size and not (out == at and stride == may_be_same):
+        raise ValueError(f"an output overlaps {name}")
+
+
+def qk_norm_rope_append(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, freqs,
+                        q_weight=None, k_weight=None, eps: float = 1e-6,
+                        interleaved: bool = False, attention_factor: float = 1.0,
+                        k_scale: float = 1.0, v_scale: float = 1.0, error_word=None, stream=None):
+    """Norm (``q_weight``, ``k_weight`` [D], each optional) and rotate the heads of ``q``
+    [T, H, D] and ``k`` [T, H_kv, D] by their ``positions``; write the queries to ``q_out``
+    (which may be ``q``) and ``k`` and ``v`` into their cache slots, as ``kv_append`` does. The
+    inputs may be slices of one projection's output. ``freqs`` come from ``rope_frequencies``;
+    the first ``2 * len(freqs)`` elements of a head turn. Over an FP8 cache, ``k / k_scale`` and
+    ``v / v_scale`` are rounded to codes."""
+    _require(q.dim() == 3 and k.dim() == 3 and k_cache.dim() == 4 and freqs.dim() == 1,
+             "q and k must be [T, heads, D], the caches [NB, bs, H_kv, D], freqs [rope_dim / 2]")
+    T, H, D = q.shape
+    NB, bs, H_kv, D2 = k_cache.shape
+    _require(D == D2, "q and the caches must agree in head size")
+    dev, dt, i32 = _cuda_index(q), q.dtype, torch.int32
+    kv = (T, H_kv, D)
+    qh = _heads(q, dev, "q", dt, (T, H, D))
+    kh, vh = _heads(k, dev, "k", dt, kv), _heads(v, dev, "v", dt, kv)
+    out = _addr(q_out, dev, "q_out", dt, q.shape)
+    size = q_out.nbytes
+    _apart(out, size, qh, "q", H * D)
+    _apart(out, size, kh, "k")
+    _apart(out, size, vh, "v")
+    _call(load().pda_qk_norm_rope_append, "pda_qk_norm_rope_append", dev, stream,
+          out, qh[0], kh[0], vh[0], qh[1], kh[1], vh[1],
+          _addr(k_cache, dev, "k_cache"),
+          _addr(v_cache, dev, "v_cache", k_cache.dtype, k_cache.shape),
+          _addr(slot_mapping, dev, "slot_mapping", i32, (T,)),
+          _addr(positions, dev, "positions", i32, (T,)),
+          _addr(freqs, dev, "freqs", torch.int64), 2 * freqs.shape[0], int(bool(interleaved)),
+          float(attention_factor), _addr(q_weight, dev, "q_weight", dt, (D,)),
+          _addr(k_weight, dev, "k_weight", dt, (D,)), float(eps), T, H, H_kv, D, bs, NB,
+          float(k_scale), float(v_scale), _dtype(q), _dtype(k_cache),
+          _addr(error_word, dev, "error_word"))
+    return q_out
+
+
+def qk_norm_rope(q_out, k_out, q, k, positions, freqs, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, interleaved: bool = False, attention_factor: float = 1.0,
+                 stream=None):
+    """``qk_norm_rope_append``'s norm and rotation into dense ``q_out`` and ``k_out`` (which may
+    be ``q`` and ``k``), without a cache."""
+    _require(q.dim() == 3 and k.dim() == 3 and freqs.dim() == 1,
+             "q and k must be [T, heads, D], freqs [rope_dim / 2]")
+    T, H, D = q.shape
+    H_kv = k.shape[1]
+    dev, dt, i32 = _cuda_index(q), q.dtype, torch.int32
+    qh, kh = _heads(q, dev, "q", dt, (T, H, D)), _heads(k, dev, "k", dt, (T, H_kv, D))
+    q_at, k_at = _addr(q_out, dev, "q_out", dt, q.shape), _addr(k_out, dev, "k_out", dt, k.shape)
+    q_size, k_size = q_out.nbytes, k_out.nbytes
+    _apart(q_at, q_size, qh, "q", H * D)
+    _apart(q_at, q_size, kh, "k")
+    _apart(k_at, k_size, qh, "q")
+    _apart(k_at, k_size, kh, "k", H_kv * D)
+    _apart(k_at, k_size, (q_at, 0, q_at + q_size), "the other output")
+    _call(load().pda_qk_norm_rope, "pda_qk_norm_rope", dev, stream, q_at, k_at, qh[0], kh[0],
+          qh[1], kh[1], _addr(positions, dev, "positions", i32, (T,)),
+          _addr(freqs, dev, "freqs", torch.int64), 2 * freqs.shape[0], int(bool(interleaved)),
+          float(attention_factor), _addr(q_weight, dev, "q_weight", dt, (D,)),
+          _addr(k_weight, dev, "k_weight", dt, (D,)), float(eps), T, H, H_kv, D, _dtype(q))
+    return q_out, k_out
 
 
 _KV_DTYPE = {torch.bfloat16: PDA_BF16, torch.float32: PDA_F32, torch.float16: PDA_F16,

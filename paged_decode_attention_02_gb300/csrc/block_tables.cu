@@ -191,7 +191,8 @@ constexpr int kSlotThreads = 256;
 constexpr int kSlotPerThread = 4;
 
 __global__ void __launch_bounds__(kSlotThreads)
-    kv_slots_kernel(int32_t* __restrict__ slots, int32_t* __restrict__ query_start,
+    kv_slots_kernel(int32_t* __restrict__ slots, int32_t* __restrict__ positions,
+                    int32_t* __restrict__ query_start,
                     const int32_t* __restrict__ query_lens, const int32_t* __restrict__ lens,
                     const int32_t* __restrict__ tables, int N, int B, int max_blocks,
                     int block_size, int num_blocks, int32_t* error_word) {
@@ -232,12 +233,13 @@ __global__ void __launch_bounds__(kSlotThreads)
         (static_cast<long long>(blockIdx.x) * kSlotPerThread + k) * kSlotThreads + tid;
     if (at >= N) break;
     const int t = static_cast<int>(at);
-    int slot = -1;
+    int slot = -1, pos = 0;
     if (t < used) {
       const int b = owner_of(end, B, t);
       const int L = lens[b], n = query_lens[b];
       if (L >= n && L <= static_cast<long long>(max_blocks) * block_size) {
         const int p = L - n + t - (b > 0 ? end[b - 1] : 0);
+        pos = p;
         const int id = tables[static_cast<size_t>(b) * max_blocks + p / block_size];
         if (id < 0 || id >= num_blocks)
           atomic_or_error(error_word, PDA_DEVERR_BLOCK_ID);
@@ -246,6 +248,7 @@ __global__ void __launch_bounds__(kSlotThreads)
       }
     }
     slots[t] = slot;
+    if (positions != nullptr) positions[t] = pos;
   }
 }
 
@@ -275,6 +278,27 @@ pda_status check_tables(int B, int max_blocks, int block_size, int num_blocks) {
       static_cast<long long>(num_blocks) * block_size >= (1ll << 31))
     return PDA_ERR_UNSUPPORTED;
   return PDA_OK;
+}
+
+pda_status build_slots(int32_t* slot_mapping, int32_t* positions, int32_t* query_start,
+                       const int32_t* query_lens, const int32_t* context_lens,
+                       const int32_t* block_tables, int N, int B, int max_blocks_per_seq,
+                       int block_size, int num_blocks, int32_t* error_word,
+                       cudaStream_t stream) {
+  if (N < 0) return PDA_ERR_INVALID_ARG;
+  if (N > (1 << 30)) return PDA_ERR_UNSUPPORTED;
+  const pda_status st = check_tables(B, max_blocks_per_seq, block_size, num_blocks);
+  if (st != PDA_OK) return st;
+  if (query_start == nullptr || (N > 0 && slot_mapping == nullptr)) return PDA_ERR_INVALID_ARG;
+  if (B > 0 && (query_lens == nullptr || context_lens == nullptr || block_tables == nullptr))
+    return PDA_ERR_INVALID_ARG;
+  const long long per = static_cast<long long>(kSlotThreads) * kSlotPerThread;
+  const long long blocks = (static_cast<long long>(N) + per - 1) / per;
+  const size_t smem = static_cast<size_t>(B) * sizeof(int);
+  kv_slots_kernel<<<static_cast<unsigned>(blocks > 0 ? blocks : 1), kSlotThreads, smem, stream>>>(
+      slot_mapping, positions, query_start, query_lens, context_lens, block_tables, N, B,
+      max_blocks_per_seq, block_size, num_blocks, error_word);
+  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }
 
 }  // namespace
@@ -309,18 +333,16 @@ extern "C" pda_status pda_kv_build_slots(int32_t* slot_mapping, int32_t* query_s
                                          const int32_t* block_tables, int N, int B,
                                          int max_blocks_per_seq, int block_size, int num_blocks,
                                          int32_t* error_word, cudaStream_t stream) {
-  if (N < 0) return PDA_ERR_INVALID_ARG;
-  if (N > (1 << 30)) return PDA_ERR_UNSUPPORTED;
-  const pda_status st = check_tables(B, max_blocks_per_seq, block_size, num_blocks);
-  if (st != PDA_OK) return st;
-  if (query_start == nullptr || (N > 0 && slot_mapping == nullptr)) return PDA_ERR_INVALID_ARG;
-  if (B > 0 && (query_lens == nullptr || context_lens == nullptr || block_tables == nullptr))
-    return PDA_ERR_INVALID_ARG;
-  const long long per = static_cast<long long>(kSlotThreads) * kSlotPerThread;
-  const long long blocks = (static_cast<long long>(N) + per - 1) / per;
-  const size_t smem = static_cast<size_t>(B) * sizeof(int);
-  kv_slots_kernel<<<static_cast<unsigned>(blocks > 0 ? blocks : 1), kSlotThreads, smem, stream>>>(
-      slot_mapping, query_start, query_lens, context_lens, block_tables, N, B,
-      max_blocks_per_seq, block_size, num_blocks, error_word);
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  return build_slots(slot_mapping, nullptr, query_start, query_lens, context_lens, block_tables, N,
+                     B, max_blocks_per_seq, block_size, num_blocks, error_word, stream);
+}
+
+extern "C" pda_status pda_kv_build_slots_positions(
+    int32_t* slot_mapping, int32_t* positions, int32_t* query_start, const int32_t* query_lens,
+    const int32_t* context_lens, const int32_t* block_tables, int N, int B,
+    int max_blocks_per_seq, int block_size, int num_blocks, int32_t* error_word,
+    cudaStream_t stream) {
+  if (N > 0 && positions == nullptr) return PDA_ERR_INVALID_ARG;
+  return build_slots(slot_mapping, positions, query_start, query_lens, context_lens, block_tables,
+                     N, B, max_blocks_per_seq, block_size, num_blocks, error_word, stream);
 }
