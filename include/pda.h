@@ -256,6 +256,33 @@ pda_status pda_paged_decode_attention_nvfp4(void* out, const void* q, const void
                                             cudaStream_t stream);
 
 /*
+ * pda_paged_window_attention -- decode attention with a sliding window: each request's query token
+ * attends over the last `window` tokens of its history (itself among them) and the first `sinks`,
+ * which stay visible:
+ *      s_t = scale * q[b,h,:] . K_t[k,:],   t < L and (t >= L - window or t < sinks).
+ * The pages describe no windowed model; this is what its layers need beside
+ * pda_paged_decode_attention (page "Disaggregated LLM Serving", sec. 1), of which everything else
+ * holds. Blocks that hold no visible token are not looked up or read: their table entries may be
+ * anything, and their memory another request's. What blocks hold in rows that are not visible does
+ * not reach the output.
+ *
+ *  window         >= 1; sinks >= 0. A window as long as the history is none.
+ *  kv_dtype       any of pda_paged_decode_attention, _fp8 and _nvfp4; q_dtype, the caches, the
+ *                 block scales (NULL but for PDA_NVFP4) and k_scale, v_scale (1 for the plain
+ *                 types) are as there.
+ *  workspace      of pda_attention_workspace_size for the same sizes.
+ *  The other sizes and the errors are those calls'.
+ */
+pda_status pda_paged_window_attention(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const void* k_block_scales, const void* v_block_scales, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* context_lens, int max_context_len, int window,
+    int sinks, int B, int H, int H_kv, int D, int block_size, int num_blocks, float scale,
+    float k_scale, float v_scale, pda_dtype q_dtype, pda_dtype kv_dtype, pda_dtype out_dtype,
+    int sm_cap, void* workspace, size_t workspace_bytes, int32_t* error_word,
+    cudaStream_t stream);
+
+/*
  * pda_paged_decode_attention_noalloc -- pda_paged_decode_attention without a workspace
  * argument, for callers that cannot allocate device memory.
  *
@@ -672,6 +699,27 @@ pda_status pda_paged_chunk_attention_fp8(void* out, const void* q, const void* k
                                          float v_scale, pda_dtype q_dtype, int sm_cap,
                                          void* workspace, size_t workspace_bytes,
                                          int32_t* error_word, cudaStream_t stream);
+
+/*
+ * pda_paged_window_chunk_attention -- chunk attention with a sliding window: token i of request b,
+ * at position p = L - n + i, attends over the last `window` tokens up to itself and the request's
+ * first `sinks`:  t <= p and (t > p - window or t < sinks).
+ * n == 1 is pda_paged_window_attention's row.
+ *
+ * Everything else is pda_paged_chunk_attention's (pda_paged_chunk_attention_fp8's with kv_dtype
+ * PDA_FP8_E4M3; k_scale and v_scale are 1 for the plain types), the workspace too. Blocks that no
+ * new token of the request sees are not looked up or read, whatever their table entries. A block
+ * id out of range gives NaN in the rows that see the block, and PDA_DEVERR_BLOCK_ID. What the cache holds in
+ * rows that a token does not see does not reach its output, NaN and infinities included.
+ *  window >= 1, sinks >= 0. A window as long as the history is none.
+ */
+pda_status pda_paged_window_chunk_attention(
+    void* out, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+    const int32_t* query_start, int max_context_len, int window, int sinks, int B, int T, int H,
+    int H_kv, int D, int block_size, int num_blocks, float scale, float k_scale, float v_scale,
+    pda_dtype q_dtype, pda_dtype kv_dtype, int sm_cap, void* workspace, size_t workspace_bytes,
+    int32_t* error_word, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

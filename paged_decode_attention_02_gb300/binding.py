@@ -35,7 +35,8 @@ EXPORTED = [
     "pda_kv_unpack_block_scales_batched", "pda_kv_assign_blocks", "pda_kv_build_slots",
     "pda_chunk_attention_workspace_size", "pda_paged_chunk_attention",
     "pda_paged_chunk_attention_fp8", "pda_kv_build_slots_positions", "pda_qk_norm_rope_append",
-    "pda_qk_norm_rope",
+    "pda_qk_norm_rope", "pda_paged_window_attention",
+    "pda_paged_window_chunk_attention",
 ]
 
 _lock = threading.Lock()
@@ -113,6 +114,16 @@ def load():
         lib.pda_kv_assign_blocks.restype = I
         lib.pda_kv_build_slots.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P]
         lib.pda_kv_build_slots.restype = I
+        # out, q, k, v, block scales, tables, max_blocks, lens, max_context_len, window, sinks, B,
+        # H, H_kv, D, bs, NB, scales, dtypes, sm_cap, workspace, bytes, error_word, stream
+        lib.pda_paged_window_attention.argtypes = [P, P, P, P, P, P, P, I, P, I, I, I, I, I, I, I,
+                                                   I, I, F, F, F, I, I, I, I, P, SZ, P, P]
+        lib.pda_paged_window_attention.restype = I
+        # out, q, k, v, tables, max_blocks, lens, query_start, max_context_len, window, sinks, B, T,
+        # H, H_kv, D, bs, NB, scales, dtypes, sm_cap, workspace, bytes, error_word, stream
+        lib.pda_paged_window_chunk_attention.argtypes = [P, P, P, P, P, I, P, P, I, I, I, I, I, I,
+                                                         I, I, I, I, F, F, F, I, I, I, P, SZ, P, P]
+        lib.pda_paged_window_chunk_attention.restype = I
         lib.pda_kv_build_slots_positions.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P]
         lib.pda_kv_build_slots_positions.restype = I
         # q_out, q, k, v, strides, caches, slots, positions, freqs, rope_dim, interleaved,
@@ -239,10 +250,34 @@ def alloc_workspace(B, H, H_kv, D, block_size=16, kv_dtype=torch.bfloat16, sm_ca
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
 
 
+def _windowed(window: int, sinks: int) -> bool:
+    _require(window >= 0 and sinks >= 0, "window and sinks must not be negative")
+    _require(window > 0 or sinks == 0, "sinks are the first tokens beside a window")
+    return window > 0
+
+
+def _window_attention(out, q, k_cache, v_cache, block_scales, block_tables, context_lens,
+                      max_context_len, window, sinks, scales, kv_dtype, sm_cap, workspace,
+                      error_word, stream):
+    B, H, D = q.shape
+    NB, bs, H_kv, _ = k_cache.shape
+    _check(load().pda_paged_window_attention(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_scales[0]),
+        _ptr(block_scales[1]), _ptr(block_tables),
+        block_tables.shape[1] if block_tables.dim() == 2 else 0, _ptr(context_lens),
+        int(max_context_len), int(window), int(sinks), B, H, H_kv, D, bs, NB, *scales, _dtype(q),
+        kv_dtype, _dtype(out), int(sm_cap), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(error_word), _stream(stream)),
+        "pda_paged_window_attention")
+    return out
+
+
 def paged_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens,
                            max_context_len: int, scale: float, sm_cap: int = 0, workspace=None,
-                           error_word=None, stream=None):
-    """``out[b,h] = softmax(scale q[b,h] K^T) V`` over request b's paged history."""
+                           error_word=None, stream=None, window: int = 0, sinks: int = 0):
+    """``out[b,h] = softmax(scale q[b,h] K^T) V`` over request b's paged history, or, with a
+    ``window``, over its last ``window`` tokens and its first ``sinks`` (blocks without any of
+    them are not read)."""
     B, H, D = q.shape
     NB, bs, H_kv, D2 = k_cache.shape
     assert D == D2 and v_cache.shape == k_cache.shape and out.shape == q.shape
@@ -250,6 +285,12 @@ def paged_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens,
     max_blocks = block_tables.shape[1] if block_tables.dim() == 2 else 0
     if workspace is None:
         workspace = alloc_workspace(B, H, H_kv, D, bs, k_cache.dtype, sm_cap, q.device)
+    if _windowed(window, sinks):
+        _require(_dtype(k_cache) != PDA_FP8_E4M3, "an FP8 cache needs its scales: the _fp8 call")
+        return _window_attention(out, q, k_cache, v_cache, (None, None), block_tables,
+                                 context_lens, max_context_len, window, sinks,
+                                 (float(scale), 1.0, 1.0), _dtype(k_cache), sm_cap, workspace,
+                                 error_word, stream)
     _check(load().pda_paged_decode_attention(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks,
         _ptr(context_lens), int(max_context_len), B, H, H_kv, D, bs, NB, float(scale),
@@ -262,8 +303,9 @@ def paged_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens,
 def paged_decode_attention_fp8(out, q, k_cache, v_cache, block_tables, context_lens,
                                max_context_len: int, scale: float, k_scale: float,
                                v_scale: float, sm_cap: int = 0, workspace=None, error_word=None,
-                               stream=None):
-    """Attention over an FP8 E4M3 cache: stored code c of K means decode(c) * k_scale."""
+                               stream=None, window: int = 0, sinks: int = 0):
+    """Attention over an FP8 E4M3 cache: stored code c of K means decode(c) * k_scale.
+    ``window`` and ``sinks`` as in ``paged_decode_attention``."""
     B, H, D = q.shape
     NB, bs, H_kv, D2 = k_cache.shape
     assert D == D2 and v_cache.shape == k_cache.shape and out.shape == q.shape
@@ -272,6 +314,11 @@ def paged_decode_attention_fp8(out, q, k_cache, v_cache, block_tables, context_l
     max_blocks = block_tables.shape[1] if block_tables.dim() == 2 else 0
     if workspace is None:
         workspace = alloc_workspace(B, H, H_kv, D, bs, torch.uint8, sm_cap, q.device)
+    if _windowed(window, sinks):
+        return _window_attention(out, q, k_cache, v_cache, (None, None), block_tables,
+                                 context_lens, max_context_len, window, sinks,
+                                 (float(scale), float(k_scale), float(v_scale)), PDA_FP8_E4M3,
+                                 sm_cap, workspace, error_word, stream)
     _check(load().pda_paged_decode_attention_fp8(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks,
         _ptr(context_lens), int(max_context_len), B, H, H_kv, D, bs, NB, float(scale),
@@ -284,10 +331,10 @@ def paged_decode_attention_fp8(out, q, k_cache, v_cache, block_tables, context_l
 def paged_decode_attention_nvfp4(out, q, k_data, v_data, k_block_scales, v_block_scales,
                                  block_tables, context_lens, max_context_len: int, scale: float,
                                  k_scale: float, v_scale: float, sm_cap: int = 0, workspace=None,
-                                 error_word=None, stream=None):
+                                 error_word=None, stream=None, window: int = 0, sinks: int = 0):
     """Attention over an NVFP4 cache: data [NB, bs, H_kv, D/2] uint8 (two E2M1 codes per
     byte, even element low), block scales [NB, H_kv, bs, D/16] uint8 (E4M3, per block and
-    head-major)."""
+    head-major). ``window`` and ``sinks`` as in ``paged_decode_attention``."""
     B, H, D = q.shape
     NB, bs, H_kv, half = k_data.shape
     assert 2 * half == D and v_data.shape == k_data.shape and out.shape == q.shape
@@ -300,6 +347,11 @@ def paged_decode_attention_nvfp4(out, q, k_data, v_data, k_block_scales, v_block
         _check(load().pda_attention_workspace_size(B, H, H_kv, D, bs, PDA_NVFP4, sm_cap,
                                                    ctypes.byref(n)), "workspace size")
         workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=q.device)
+    if _windowed(window, sinks):
+        return _window_attention(out, q, k_data, v_data, (k_block_scales, v_block_scales),
+                                 block_tables, context_lens, max_context_len, window, sinks,
+                                 (float(scale), float(k_scale), float(v_scale)), PDA_NVFP4,
+                                 sm_cap, workspace, error_word, stream)
     _check(load().pda_paged_decode_attention_nvfp4(
         _ptr(out), _ptr(q), _ptr(k_data), _ptr(v_data), _ptr(k_block_scales),
         _ptr(v_block_scales), _ptr(block_tables), max_blocks, _ptr(context_lens),
@@ -712,7 +764,7 @@ def alloc_chunk_workspace(B, T, H, H_kv, D, block_size=16, kv_dtype=torch.bfloat
 
 
 def _chunk(fn, what, scales, out, q, k_cache, v_cache, block_tables, context_lens, query_start,
-           max_context_len, sm_cap, workspace, error_word, stream, dtypes):
+           max_context_len, sm_cap, workspace, error_word, stream, dtypes, window, sinks):
     _require(q.dim() == 3 and k_cache.dim() == 4 and block_tables.dim() == 2,
              "q must be [T, H, D], the caches [NB, bs, H_kv, D], block_tables [B, max_blocks]")
     T, H, D = q.shape
@@ -724,37 +776,46 @@ def _chunk(fn, what, scales, out, q, k_cache, v_cache, block_tables, context_len
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             workspace = alloc_chunk_workspace(B, T, H, H_kv, D, bs, k_cache.dtype, sm_cap,
                                               q.device)
+    windows = ()
+    if _windowed(window, sinks):
+        fn, what = load().pda_paged_window_chunk_attention, "pda_paged_window_chunk_attention"
+        windows = (int(window), int(sinks))
+        scales = (*scales, 1.0, 1.0)[:3]
+        dtypes = (dtypes[0], _dtype(k_cache))
     _call(fn, what, dev, stream, _addr(out, dev, "out", q.dtype, q.shape), _addr(q, dev, "q"),
           _addr(k_cache, dev, "k_cache"),
           _addr(v_cache, dev, "v_cache", k_cache.dtype, k_cache.shape),
           _addr(block_tables, dev, "block_tables", i32), max_blocks,
           _addr(context_lens, dev, "context_lens", i32, (B,)),
-          _addr(query_start, dev, "query_start", i32, (B + 1,)), int(max_context_len), B, T, H,
-          H_kv, D, bs, NB, *scales, *dtypes, int(sm_cap), _addr(workspace, dev, "workspace"),
+          _addr(query_start, dev, "query_start", i32, (B + 1,)), int(max_context_len), *windows,
+          B, T, H, H_kv, D, bs, NB, *scales, *dtypes, int(sm_cap), _addr(workspace, dev, "workspace"),
           workspace.numel() * workspace.element_size(), _addr(error_word, dev, "error_word"))
     return out
 
 
 def paged_chunk_attention(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
                           max_context_len: int, scale: float, sm_cap: int = 0, workspace=None,
-                          error_word=None, stream=None):
+                          error_word=None, stream=None, window: int = 0, sinks: int = 0):
     """Attention of each request's new tokens (rows ``query_start[b]:query_start[b + 1]`` of
     ``q`` [T, H, D], the last of its ``context_lens[b]``) over its paged history up to and
-    including themselves."""
+    including themselves; with a ``window``, over the last ``window`` tokens up to and including
+    themselves and the first ``sinks``."""
+    _require(not window or _dtype(k_cache) != PDA_FP8_E4M3,
+             "an FP8 cache needs its scales: the _fp8 call")
     return _chunk(load().pda_paged_chunk_attention, "pda_paged_chunk_attention",
                   (float(scale),), out, q, k_cache, v_cache, block_tables, context_lens,
                   query_start, max_context_len, sm_cap, workspace, error_word, stream,
-                  (_dtype(q), _dtype(k_cache)))
+                  (_dtype(q), _dtype(k_cache)), window, sinks)
 
 
 def paged_chunk_attention_fp8(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
                               max_context_len: int, scale: float, k_scale: float,
                               v_scale: float, sm_cap: int = 0, workspace=None, error_word=None,
-                              stream=None):
+                              stream=None, window: int = 0, sinks: int = 0):
     """``paged_chunk_attention`` over an FP8 E4M3 cache: stored code c of K means
     decode(c) * k_scale."""
     _require(_dtype(k_cache) == PDA_FP8_E4M3, "the caches must hold FP8 E4M3 codes")
     return _chunk(load().pda_paged_chunk_attention_fp8, "pda_paged_chunk_attention_fp8",
                   (float(scale), float(k_scale), float(v_scale)), out, q, k_cache, v_cache,
                   block_tables, context_lens, query_start, max_context_len, sm_cap, workspace,
-                  error_word, stream, (_dtype(q),))
+                  error_word, stream, (_dtype(q),), window, sinks)

@@ -17,17 +17,18 @@
 namespace pda {
 namespace {
 
-using CutsOf = Cuts<6, 4, 6>;  // 64-row items
+template <bool kWindow>
+using CutsOf = Cuts<6, 4, 6, kWindow>;  // 64-row items
 constexpr int kRows = 64, kKeys = 64;
 
-template <int D>
+template <int D, typename C>
 struct Smem {
   float q[kRows][D + 4];
   float k[2][kKeys][D + 4];  // padded: eight keys' 16-byte pieces lie in different banks
   float v[2][kKeys][D];
   float p[kKeys][kRows + 4];  // key-major, so a thread's four rows are one piece
   PlanMemory plan;
-  Where first;
+  Where<C> first;
   int range[2];
 };
 
@@ -42,23 +43,24 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
-template <int D>
+template <int D, bool kWindow>
 __global__ void __launch_bounds__(256, 1)
     chunk_f32_kernel(const ChunkParams p, int g_shift, float* partial) {
+  using C = CutsOf<kWindow>;
   constexpr int kCols = D / 16;  // output columns of a thread, four side by side
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
+  Smem<D, C>& sm = *reinterpret_cast<Smem<D, C>*>(smem_raw);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int x = tid & 15, y = tid >> 4;
-  const int lt = CutsOf::kRowsLog2 - g_shift;
-  const Plan pl = make_plan<CutsOf>(p, lt, gridDim.x, &sm.plan);
+  const int lt = C::kRowsLog2 - g_shift;
+  const Plan pl = make_plan<C>(p, lt, gridDim.x, &sm.plan);
 
   // requests without work whose rows are written all the same: padded (zeros) or in error (NaN)
   if (!pl.ok && blockIdx.x == 0 && tid == 0) atomic_or_error(p.error_word, PDA_DEVERR_QUERY);
   for (int b = pl.ok ? blockIdx.x : p.B; b < p.B; b += gridDim.x) {
     const int q0 = p.query_start[b], q1 = p.query_start[b + 1], L = p.context_lens[b];
-    if (q0 == q1 || chunk_req(p, b, lt).r.n > 0) continue;
+    if (q0 == q1 || chunk_req<C>(p, b, lt).r.n > 0) continue;
     if (L != 0 && tid == 0) atomic_or_error(p.error_word, PDA_DEVERR_CONTEXT_LEN);
     const float f = L == 0 ? 0.f : NAN;
     float4* rows = reinterpret_cast<float4*>(p.out) + static_cast<size_t>(q0) * p.H * (D / 4);
@@ -67,10 +69,10 @@ __global__ void __launch_bounds__(256, 1)
   }
 
   if (warp == 0) {
-    Where w{};
+    Where<C> w{};
     int u = 0, u_end = 0;
     if (static_cast<int>(blockIdx.x) < pl.workers && pl.units > 0) {
-      u = cut_of<CutsOf>(p, pl, lt, blockIdx.x + (lane & 1), &w);
+      u = cut_of<C>(p, pl, lt, blockIdx.x + (lane & 1), &w);
       u_end = __shfl_sync(kFullMask, u, 1);
       u = __shfl_sync(kFullMask, u, 0);
       // lane 0's item is the block's; the others' are not
@@ -84,14 +86,14 @@ __global__ void __launch_bounds__(256, 1)
     }
   }
   __syncthreads();
-  Where w = sm.first;
+  Where<C> w = sm.first;
   int u = sm.range[0];
   const int u_end = sm.range[1];
   const float* k_cache = static_cast<const float*>(p.k_cache);
   const float* v_cache = static_cast<const float*>(p.v_cache);
 
   while (u < u_end) {
-    const ChunkReq r = w.q.r;
+    const typename C::Request r = w.q.r;
     const int tiles = r.tiles(w.i);
     const int end = w.start + tiles + kItemUnits;
     const int tok0 = w.i << lt, tokens = min(1 << lt, r.n - tok0);
@@ -99,19 +101,32 @@ __global__ void __launch_bounds__(256, 1)
     const int jb = u_end >= end ? tiles : u_end - w.start - kItemUnits;
     const int pos0 = r.L - r.n + tok0, kv_end = pos0 + tokens;
     const int32_t* table = p.block_tables + static_cast<size_t>(w.b) * p.max_blocks;
-    const int first_key = ja * kChunkKeys, last_key = min(kv_end, jb * kChunkKeys);
+    // with a window the item's keys are numbered without the tiles it skips: key_of gives the
+    // key behind such a number
+    int gap = 0, lowest = 0, last_lowest = 0;
+    if constexpr (kWindow) {
+      gap = r.skipped(w.i) * kChunkKeys;
+      lowest = r.lowest(w.i);
+      last_lowest = max(0, kv_end - p.window);
+    }
+    auto key_of = [&](int at) {
+      return kWindow && at >= p.sink_tiles * kChunkKeys ? at + gap : at;
+    };
+    const int first_key = ja * kChunkKeys, last_key = min(kv_end - gap, jb * kChunkKeys);
     const int steps = (last_key - first_key + kKeys - 1) / kKeys;
-    int bad_from = 0x7fffffff;  // first key of a block with an id out of range
+    int bad_from = 0x7fffffff;  // first key of a block with an id out of range (window: 0)
 
     // a warp loads every eighth row; ids are the same for all its lanes
     auto load = [&](int s) {
       const int buf = s & 1, key0 = first_key + s * kKeys;
       for (int i = warp; i < kKeys; i += 8) {
-        const int key = key0 + i;
-        bool there = key < last_key;
+        const int key = key_of(key0 + i);
+        bool there = key0 + i < last_key;
+        if (kWindow) there = there && (key < p.sinks || key >= lowest);
         int id = there ? table[key / p.block_size] : 0;
         if (id < 0 || id >= p.num_blocks) {
-          bad_from = min(bad_from, max(key / p.block_size * p.block_size, first_key));
+          bad_from = kWindow ? 0
+                             : min(bad_from, max(key / p.block_size * p.block_size, first_key));
           if (lane == 0) atomic_or_error(p.error_word, PDA_DEVERR_BLOCK_ID);
           there = false;
           id = 0;
@@ -145,7 +160,7 @@ __global__ void __launch_bounds__(256, 1)
       for (int e = 0; e < kCols; ++e) o[a][e] = 0.f;
     }
     for (int s = 0; s < steps; ++s) {
-      const int buf = s & 1, key0 = first_key + s * kKeys;
+      const int buf = s & 1, at0 = first_key + s * kKeys, key0 = key_of(at0);
       if (s + 1 < steps) {
         load(s + 1);
         cp_async_wait<1>();
@@ -173,13 +188,18 @@ __global__ void __launch_bounds__(256, 1)
           }
       }
       // some row does not see the whole step: its V may not even be multiplied by zero
-      const bool edge = key0 + kKeys - 1 > pos0;
+      const bool edge = key0 + kKeys - 1 > pos0 ||
+                        (kWindow && key0 < last_lowest && key0 + kKeys - 1 >= p.sinks);
+      auto sees = [&](int a, int key) {
+        if (kWindow && key >= p.sinks && key <= pos[a] - p.window) return false;
+        return key <= pos[a];
+      };
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
         float top = m[a];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          sc[a][b] = key0 + x + 16 * b <= pos[a] ? sc[a][b] * p.scale_log2 : -INFINITY;
+          sc[a][b] = sees(a, key0 + x + 16 * b) ? sc[a][b] * p.scale_log2 : -INFINITY;
           top = fmaxf(top, sc[a][b]);
         }
 #pragma unroll
@@ -201,7 +221,7 @@ __global__ void __launch_bounds__(256, 1)
         *reinterpret_cast<float4*>(&sm.p[x + 16 * b][4 * y]) =
             make_float4(sc[0][b], sc[1][b], sc[2][b], sc[3][b]);
       __syncwarp();  // a warp reads back its own rows only
-      const int keys = min(kKeys, last_key - key0);
+      const int keys = min(kKeys, last_key - at0);
       auto accumulate = [&](int j, bool masked) {
         const float4 pr = *reinterpret_cast<const float4*>(&sm.p[j][4 * y]);
         const float pa[4] = {pr.x, pr.y, pr.z, pr.w};
@@ -210,7 +230,7 @@ __global__ void __launch_bounds__(256, 1)
           const float4 v = *reinterpret_cast<const float4*>(&sm.v[buf][j][16 * e + 4 * x]);
 #pragma unroll
           for (int a = 0; a < 4; ++a) {
-            if (masked && key0 + j > pos[a]) continue;
+            if (masked && !sees(a, key0 + j)) continue;
             o[a][e] = fmaf(pa[a], v.x, o[a][e]);
             o[a][e + 1] = fmaf(pa[a], v.y, o[a][e + 1]);
             o[a][e + 2] = fmaf(pa[a], v.z, o[a][e + 2]);
@@ -242,7 +262,8 @@ __global__ void __launch_bounds__(256, 1)
       for (int i = 1; i < 16; i <<= 1) l[a] += __shfl_xor_sync(kFullMask, l[a], i);
       const int row = 4 * y + a, tok = row >> g_shift;
       if (tok >= tokens) continue;
-      const bool dead = pos[a] >= bad_from;
+      bool dead = pos[a] >= bad_from;
+      if (kWindow && dead) dead = sees_bad_block(p, table, pos[a]);
       if (part >= 0) {
         if (x == 0) part_ml(partial, part, D)[row] = make_float2(m[a], dead ? NAN : l[a]);
 #pragma unroll
@@ -266,24 +287,24 @@ __global__ void __launch_bounds__(256, 1)
   }
 }
 
-template <int D>
+template <int D, bool kWindow>
 pda_status launch(const ChunkParams& p, int dev, int sms, bool capped, float* partial,
                   cudaStream_t stream) {
-  constexpr int smem = static_cast<int>(sizeof(Smem<D>));
+  constexpr int smem = static_cast<int>(sizeof(Smem<D, CutsOf<kWindow>>));
   static_assert(smem <= 232448, "227 KB a block");
   static std::atomic<bool> raised[64];
   if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(chunk_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(chunk_f32_kernel<D, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem) != cudaSuccess)
       return PDA_ERR_CUDA;
     if (dev < 64) raised[dev].store(true, std::memory_order_release);
   }
   int g_shift = 0;
   while ((1 << g_shift) < p.G) ++g_shift;
-  const int grid = chunk_grid<CutsOf>(p, g_shift, sms);
-  chunk_f32_kernel<D><<<grid, 256, smem, stream>>>(p, g_shift, partial);
+  const int grid = chunk_grid<CutsOf<kWindow>>(p, g_shift, sms);
+  chunk_f32_kernel<D, kWindow><<<grid, 256, smem, stream>>>(p, g_shift, partial);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
-  return launch_merge<D, float, CutsOf>(p, g_shift, partial, grid, capped, stream);
+  return launch_merge<D, float, CutsOf<kWindow>>(p, g_shift, partial, grid, capped, stream);
 }
 
 }  // namespace
@@ -291,8 +312,11 @@ pda_status launch(const ChunkParams& p, int dev, int sms, bool capped, float* pa
 pda_status launch_chunk_f32(const ChunkParams& p, int D, int dev, int sms, bool capped,
                             void* workspace, cudaStream_t stream) {
   float* partial = static_cast<float*>(workspace);
-  return D == 128 ? launch<128>(p, dev, sms, capped, partial, stream)
-                  : launch<64>(p, dev, sms, capped, partial, stream);
+  if (p.window > 0)
+    return D == 128 ? launch<128, true>(p, dev, sms, capped, partial, stream)
+                    : launch<64, true>(p, dev, sms, capped, partial, stream);
+  return D == 128 ? launch<128, false>(p, dev, sms, capped, partial, stream)
+                  : launch<64, false>(p, dev, sms, capped, partial, stream);
 }
 
 }  // namespace pda

@@ -17,6 +17,9 @@ struct ChunkParams {
   float scale_log2;  // softmax scale times log2 e (and the cache's K scale)
   float v_scale;
   int B, T, H, H_kv, G, max_blocks, max_context_len, block_size, num_blocks;
+  // sliding window (window 0: none): a token sees the last `window` keys up to itself and the
+  // first `sinks`, which lie in sink_tiles key tiles
+  int window, sinks, sink_tiles;
 };
 
 // Workspace bytes on `sms` SMs: two cut items' partial results a block.
@@ -26,6 +29,9 @@ size_t chunk_workspace(int sms, int D);
 // where it is `capped` to them.
 pda_status launch_chunk_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int dev, int sms,
                            bool capped, void* workspace, cudaStream_t stream);
+// The same with a sliding window, compiled in a unit of its own.
+pda_status launch_chunk_window_tc(const ChunkParams& p, int D, pda_dtype kv_dtype, int dev,
+                                  int sms, bool capped, void* workspace, cudaStream_t stream);
 // fp32 caches.
 pda_status launch_chunk_f32(const ChunkParams& p, int D, int dev, int sms, bool capped,
                             void* workspace, cudaStream_t stream);

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "chunk_internal.h"
 #include "chunk_plan.h"
@@ -11,20 +12,23 @@
 namespace pda {
 
 // How a kernel cuts its work: log2 of an item's rows, the fewest key tiles of a cut item's
-// piece, and the fewest units of a worker's range.
-template <int rows_log2, int piece_tiles, int worker_units>
+// piece, the fewest units of a worker's range, and whether there is a sliding window.
+template <int rows_log2, int piece_tiles, int worker_units, bool window = false>
 struct Cuts {
   static constexpr int kRowsLog2 = rows_log2, kPieceTiles = piece_tiles,
                        kWorkerUnits = worker_units;
+  static constexpr bool kWindow = window;
+  using Request = std::conditional_t<window, WindowReq, ChunkReq>;
 };
 
 // ---------------------------------------------------------------- plan
 // Units of the requests [0, c * per) for every c, built by all threads of the block.
 constexpr int kPlanChunks = 256;
 
+template <typename C>
 struct Req {
   int row0;  // first row of q and out
-  ChunkReq r;
+  typename C::Request r;
 };
 
 struct PlanMemory {
@@ -38,17 +42,27 @@ struct Plan {
   bool ok;  // query_start never decreases and stays within [0, T]; otherwise there is no work
 };
 
+template <typename C>
 struct Where {
   int b, kh, i, start;  // start: a unit
-  Req q;
+  Req<C> q;
 };
 
+template <typename C>
+__device__ __forceinline__ typename C::Request request(const ChunkParams& p, int n, int L, int lt) {
+  if constexpr (C::kWindow)
+    return WindowReq{{n, L, lt}, p.window, p.sink_tiles};
+  else
+    return ChunkReq{n, L, lt};
+}
+
 // A request with work to do; n = 0 for one without (empty, padded or in error).
-__device__ __forceinline__ Req chunk_req(const ChunkParams& p, int b, int lt) {
+template <typename C>
+__device__ __forceinline__ Req<C> chunk_req(const ChunkParams& p, int b, int lt) {
   const int q0 = p.query_start[b], q1 = p.query_start[b + 1], L = p.context_lens[b];
   const bool ok = q0 >= 0 && q1 <= p.T && q0 < q1 && L >= q1 - q0 && L <= p.max_context_len &&
                   L <= static_cast<long long>(p.max_blocks) * p.block_size;
-  return Req{q0, ChunkReq{ok ? q1 - q0 : 0, ok ? L : 0, lt}};
+  return Req<C>{q0, request<C>(p, ok ? q1 - q0 : 0, ok ? L : 0, lt)};
 }
 
 // Called by all threads of a block of at least 256.
@@ -63,7 +77,7 @@ __device__ __forceinline__ Plan make_plan(const ChunkParams& p, int lt, int work
   bool bad = false;
   if (c < kPlanChunks)
     for (int b = c * pl.per; b < min(p.B, (c + 1) * pl.per); ++b) {
-      const Req q = chunk_req(p, b, lt);
+      const Req<C> q = chunk_req<C>(p, b, lt);
       bad |= q.row0 < 0 || q.row0 > p.query_start[b + 1] || p.query_start[b + 1] > p.T;
       x += q.r.units();
       if (pl.per == 1) mem->req[b] = make_int3(q.row0, q.r.n, q.r.L);
@@ -90,7 +104,8 @@ __device__ __forceinline__ Plan make_plan(const ChunkParams& p, int lt, int work
 }
 
 // The item that holds unit u < units. Valid while the plan's memory is.
-__device__ __forceinline__ Where locate(const ChunkParams& p, const Plan& pl, int lt, int u) {
+template <typename C>
+__device__ __forceinline__ Where<C> locate(const ChunkParams& p, const Plan& pl, int lt, int u) {
   int lo = 0, hi = kPlanChunks - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -101,45 +116,59 @@ __device__ __forceinline__ Where locate(const ChunkParams& p, const Plan& pl, in
   }
   int at = pl.mem->prefix[lo];
   int b = lo * pl.per;
-  Req q;
+  Req<C> q;
   if (pl.per == 1) {
     const int3 v = pl.mem->req[b];
-    q = Req{v.x, ChunkReq{v.y, v.z, lt}};
+    q = Req<C>{v.x, request<C>(p, v.y, v.z, lt)};
   } else {
-    q = chunk_req(p, b, lt);
+    q = chunk_req<C>(p, b, lt);
   }
   int one = q.r.units();
   while (at + one * p.H_kv <= u) {
     at += one * p.H_kv;
-    q = chunk_req(p, ++b, lt);
+    q = chunk_req<C>(p, ++b, lt);
     one = q.r.units();
   }
   const int kh = static_cast<unsigned>(u - at) / static_cast<unsigned>(one);
   at += kh * one;
   const int i = q.r.item_of(u - at);
-  return Where{b, kh, i, at + q.r.units_before(i), q};
+  return Where<C>{b, kh, i, at + q.r.units_before(i), q};
 }
 
 // Moves on to the item behind, of a batch that has one.
-__device__ __forceinline__ void next_item(const ChunkParams& p, int lt, Where* w) {
+template <typename C>
+__device__ __forceinline__ void next_item(const ChunkParams& p, int lt, Where<C>* w) {
   w->start += w->q.r.tiles(w->i) + kItemUnits;
   if (++w->i < w->q.r.items()) return;
   w->i = 0;
   if (++w->kh < p.H_kv) return;
   w->kh = 0;
   do {
-    w->q = chunk_req(p, ++w->b, lt);
+    w->q = chunk_req<C>(p, ++w->b, lt);
   } while (w->q.r.n == 0 && w->b + 1 < p.B);
 }
 
 // The cut before worker c, snapped; *w: the item it falls into (for a cut below `units`).
 template <typename C>
 __device__ __forceinline__ int cut_of(const ChunkParams& p, const Plan& pl, int lt, int c,
-                                      Where* w) {
+                                      Where<C>* w) {
   const int u = chunk_cut(pl.units, pl.workers, c);
   if (u >= pl.units) return pl.units;
-  *w = locate(p, pl, lt, u);
+  *w = locate<C>(p, pl, lt, u);
   return chunk_snap(u, w->start, w->q.r.tiles(w->i), C::kPieceTiles);
+}
+
+// Whether the row at position pos, under a window, sees a block whose id is out of range.
+__device__ __forceinline__ bool sees_bad_block(const ChunkParams& p, const int32_t* table,
+                                               int pos) {
+  const int bs = p.block_size, first = max(0, pos - p.window + 1) / bs;
+  bool bad = false;
+  auto look = [&](int from, int to) {
+    for (int i = from; i < to; ++i) bad |= table[i] < 0 || table[i] >= p.num_blocks;
+  };
+  if (p.sinks > 0) look(0, min(first, min(p.sinks - 1, pos) / bs + 1));
+  look(first, pos / bs + 1);
+  return bad;
 }
 
 // ---------------------------------------------------------------- partial results
@@ -194,7 +223,7 @@ __global__ void __launch_bounds__(1024)
   const int sets = static_cast<int>(blockDim.x) / kMergeThreads;
   const int first = (blockIdx.y * sets + threadIdx.x / kMergeThreads) * kMergeRows;
   int pieces = 0, rows = 0;
-  Where w{};
+  Where<C> w{};
   if (c < pl.workers) {
     // the cut and, on the odd lanes, the one before it
     const int s = cut_of<C>(p, pl, lt, c - (lane & 1), &w);
@@ -257,12 +286,22 @@ inline int chunk_tiles(const ChunkParams& p) {
   const long long keys = std::min<long long>(p.max_context_len, cap);
   return static_cast<int>((keys + kChunkKeys - 1) / kChunkKeys);
 }
+// The same with a window: the first tokens' tiles and those of an item's windows, one more where
+// they start inside a tile.
+template <typename C>
+int item_tiles(const ChunkParams& p, int g_shift) {
+  const int all = chunk_tiles(p);
+  if (!C::kWindow) return all;
+  const long long keys = static_cast<long long>(p.window) + (1 << (C::kRowsLog2 - g_shift));
+  return static_cast<int>(
+      std::min<long long>(all, p.sink_tiles + (keys + kChunkKeys - 1) / kChunkKeys + 1));
+}
 // Blocks of a launch: no more than that bound can keep busy.
 template <typename C>
 long long chunk_units(const ChunkParams& p, int g_shift) {
   const long long items =
       ((static_cast<long long>(p.T) >> (C::kRowsLog2 - g_shift)) + p.B) * p.H_kv;
-  return items * (chunk_tiles(p) + kItemUnits);
+  return items * (item_tiles<C>(p, g_shift) + kItemUnits);
 }
 template <typename C>
 int chunk_grid(const ChunkParams& p, int g_shift, int sms) {
@@ -275,7 +314,7 @@ int chunk_grid(const ChunkParams& p, int g_shift, int sms) {
 template <int D, typename Out, typename C>
 pda_status launch_merge(const ChunkParams& p, int g_shift, float* partial, int grid, bool capped,
                         cudaStream_t stream) {
-  if (grid == 1 || chunk_tiles(p) < 2 * C::kPieceTiles) return PDA_OK;
+  if (grid == 1 || item_tiles<C>(p, g_shift) < 2 * C::kPieceTiles) return PDA_OK;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

@@ -76,6 +76,61 @@ struct ChunkReq {
   }
 };
 
+// The same with a sliding window: an item attends to the first tokens' tiles and to those from its
+// first token's window on, tiles between are left out, so its tile j is key tile j, or
+// j + skipped(i) behind the first tokens'.
+struct WindowReq : ChunkReq {
+  int window;      // keys a token sees up to itself, >= 1
+  int sink_tiles;  // key tiles that hold first tokens
+  // first key of the window of item i's first token
+  PDA_CHUNK_HD int lowest(int i) const {
+    const int a = L - n + static_cast<int>(static_cast<unsigned>(i) << lt) - window + 1;
+    return a > 0 ? a : 0;
+  }
+  PDA_CHUNK_HD int skipped(int i) const {
+    const int s = (lowest(i) >> 7) - sink_tiles;
+    return s > 0 ? s : 0;
+  }
+  PDA_CHUNK_HD int tiles(int i) const { return ChunkReq::tiles(i) - skipped(i); }
+  // skipped tiles of items [0, i): of those from the first item on whose window starts behind the
+  // first tokens' tiles, floors of an arithmetic progression again
+  PDA_CHUNK_HD unsigned skipped_before(int i) const {
+    const int a = L - n - window + 1;
+    const int from = (sink_tiles + 1) << 7;  // the window's start where the first tile is skipped
+    const unsigned up = from > a ? static_cast<unsigned>(from) - static_cast<unsigned>(a) : 0u;
+    const unsigned j0 = (up >> lt) + ((up & ((1u << lt) - 1)) != 0);
+    const unsigned m = i;
+    if (j0 >= m) return 0;
+    unsigned sum;
+    if (lt >= 7) {
+      sum = (m - j0) * static_cast<unsigned>(a >> 7) + ((pairs(m) - pairs(j0)) << (lt - 7));
+    } else {
+      const unsigned x0 = static_cast<unsigned>(a >> lt);
+      sum = floor_sum(x0 + m, 7 - lt) - floor_sum(x0 + j0, 7 - lt);
+    }
+    return sum - (m - j0) * static_cast<unsigned>(sink_tiles);
+  }
+  PDA_CHUNK_HD int units_before(int i) const {
+    return static_cast<int>(static_cast<unsigned>(ChunkReq::units_before(i)) - skipped_before(i));
+  }
+  PDA_CHUNK_HD int units() const {
+    if (n == 0) return 0;
+    const int last = items() - 1;
+    return units_before(last) + tiles(last) + kItemUnits;
+  }
+  PDA_CHUNK_HD int item_of(int w) const {
+    int lo = 0, hi = items() - 1;
+    while (lo < hi) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if (units_before(mid) <= w)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+};
+
 // Where a cut at unit u of an item that starts at unit `start` really falls: before key tile
 // u - start - kItemUnits, or at the item's start or end where that leaves a piece of fewer than
 // `least` tiles.

@@ -43,6 +43,35 @@
 
 namespace pda {
 
+// Which of a tile's 16 rows count: the first n, or those of a mask.
+struct FirstRows {
+  int n;
+  __device__ __forceinline__ bool all() const { return n == 16; }
+  __device__ __forceinline__ bool operator()(int t) const { return t < n; }
+  // Row t's values and scale, zeroed where it does not count.
+  template <int N>
+  __device__ __forceinline__ void keep(int t, float* v, float& scale) const {
+    if (t >= n) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = 0.f;
+      scale = 0.f;
+    }
+  }
+};
+struct RowMask {
+  int bits;
+  __device__ __forceinline__ bool all() const { return bits == 0xffff; }
+  __device__ __forceinline__ bool operator()(int t) const { return (bits >> t & 1) != 0; }
+  // by arithmetic: a tile's 16 answers together take more predicates than there are
+  template <int N>
+  __device__ __forceinline__ void keep(int t, float* v, float& scale) const {
+    const uint32_t all = static_cast<uint32_t>(-(bits >> t & 1));
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = __uint_as_float(__float_as_uint(v[e]) & all);
+    scale = __uint_as_float(__float_as_uint(scale) & all);
+  }
+};
+
 // The per-head products, shared by the single- and two-head steps. Lane = 4 g + t4.
 template <typename KV, int D>
 struct TCOps {
@@ -127,10 +156,11 @@ struct TCOps {
 
   // Per token half of this lane's V pairs: which of (token 2t4 [+8], token 2t4+1 [+8]) are
   // valid; the masks clear the invalid token's bytes (FP8) or fp16 halves (NVFP4).
-  static __device__ __forceinline__ void keep_masks(int t4, int n_valid, uint32_t& keep_lo,
+  template <typename Valid>
+  static __device__ __forceinline__ void keep_masks(int t4, Valid valid, uint32_t& keep_lo,
                                                     uint32_t& keep_hi) {
-    const bool a = 2 * t4 < n_valid, b = 2 * t4 + 1 < n_valid;
-    const bool c = 8 + 2 * t4 < n_valid, d = 9 + 2 * t4 < n_valid;
+    const bool a = valid(2 * t4), b = valid(2 * t4 + 1);
+    const bool c = valid(8 + 2 * t4), d = valid(9 + 2 * t4);
     if constexpr (FP4) {
       keep_lo = (a ? 0x0000ffffu : 0u) | (b ? 0xffff0000u : 0u);
       keep_hi = (c ? 0x0000ffffu : 0u) | (d ? 0xffff0000u : 0u);
@@ -336,9 +366,9 @@ struct WarpAttnTC {
   }
 
   // ks/vs: the tile's K and V rows (swizzled); ksc/vsc: NVFP4 block scales, [16][D/16].
-  template <bool kPartial>
+  template <bool kPartial, typename Valid>
   __device__ __forceinline__ void tile(const KV* ks, const KV* vs, const uint8_t* ksc,
-                                       const uint8_t* vsc, int n_valid) {
+                                       const uint8_t* vsc, Valid valid) {
     float sc[2][4] = {};
     Ops::qk(sc, qa, reinterpret_cast<const unsigned char*>(ks), ksc, ROW_SCALES, g, t4);
     float x[4] = {sc[0][0] * c, sc[0][1] * c, sc[1][0] * c, sc[1][1] * c};
@@ -346,7 +376,7 @@ struct WarpAttnTC {
       const int tok[4] = {2 * t4, 2 * t4 + 1, 8 + 2 * t4, 9 + 2 * t4};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (tok[e] >= n_valid) x[e] = -INFINITY;
+        if (!valid(tok[e])) x[e] = -INFINITY;
     }
     bool grow;
     const float alpha = Ops::softmax(x, m_run, l_run, grow);
@@ -368,7 +398,7 @@ struct WarpAttnTC {
     Ops::split_p(x[0], x[1], pb0, pl0);
     Ops::split_p(x[2], x[3], pb1, pl1);
     uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
-    if (kPartial) Ops::keep_masks(t4, n_valid, keep_lo, keep_hi);
+    if (kPartial) Ops::keep_masks(t4, valid, keep_lo, keep_hi);
     Ops::pv(o, reinterpret_cast<const unsigned char*>(vs), vsc, ROW_SCALES, v_off, g, t4, pb0,
             pb1, pl0, pl1, keep_lo, keep_hi);
   }
@@ -455,9 +485,9 @@ struct WarpAttnTCPair {
     }
   }
 
-  template <bool kPartial>
+  template <bool kPartial, typename Valid>
   __device__ __forceinline__ void tile(const KV* ks_, const KV* vs_, const uint8_t* ksc,
-                                       const uint8_t* vsc, int n_valid) {
+                                       const uint8_t* vsc, Valid valid) {
     const unsigned char* ks = reinterpret_cast<const unsigned char*>(ks_);
     const unsigned char* vs = reinterpret_cast<const unsigned char*>(vs_);
     float sc[2][2][4] = {};  // head, n-tile
@@ -478,7 +508,7 @@ struct WarpAttnTCPair {
         const int tok[4] = {2 * t4, 2 * t4 + 1, 8 + 2 * t4, 9 + 2 * t4};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (tok[e] >= n_valid) x[u][e] = -INFINITY;
+          if (!valid(tok[e])) x[u][e] = -INFINITY;
       }
       alpha[u] = Ops::softmax(x[u], m_run[u], l_run[u], grow[u]);
     }
@@ -516,7 +546,7 @@ struct WarpAttnTCPair {
       pB[k] = low ? 0u : from;
     }
     uint32_t keep_lo = 0xffffffffu, keep_hi = 0xffffffffu;
-    if (kPartial) Ops::keep_masks(t4, n_valid, keep_lo, keep_hi);
+    if (kPartial) Ops::keep_masks(t4, valid, keep_lo, keep_hi);
     Ops::pv(o, vs, vsc, ROW_SCALES, v_off, g, t4, pA[0], pA[1], pA[2], pA[3], keep_lo,
             keep_hi);
     Ops::pv(o, vs + Ops::TILE_BYTES, vsc + HEAD_SCALES, ROW_SCALES, v_off, g, t4, pB[0],

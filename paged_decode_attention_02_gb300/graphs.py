@@ -32,7 +32,8 @@ def bucket_sizes(max_n: int, interval: int, with_zero: bool) -> list:
 class DecodeStepGraphs:
     def __init__(self, k_cache: torch.Tensor, v_cache: torch.Tensor, H: int, max_blocks: int,
                  max_local: int, max_remote: int, interval: int, scale: float,
-                 remote_sm_cap: int, dtype=None):
+                 remote_sm_cap: int, dtype=None, window: int = 0, sinks: int = 0):
+        self.window = dict(window=window, sinks=sinks)  # of a sliding-window layer
         self.k_cache, self.v_cache = k_cache, v_cache
         NB, bs, H_kv, D = k_cache.shape
         self.H, self.H_kv, self.D, self.bs, self.max_blocks = H, H_kv, D, bs, max_blocks
@@ -90,13 +91,14 @@ class DecodeStepGraphs:
                 self.out[rows_r], self.q[rows_r], self.k_cache, self.v_cache,
                 self.tables[rows_r], self.lens[rows_r], max_ctx, self.scale,
                 sm_cap=self.remote_cap, workspace=self._workspace("remote", br, self.remote_cap),
-                error_word=self.err, stream=self.side)
+                error_word=self.err, stream=self.side, **self.window)
         if bl:
             cap = self.local_cap if br else 0
             binding.paged_decode_attention(
                 self.out[rows_l], self.q[rows_l], self.k_cache, self.v_cache,
                 self.tables[rows_l], self.lens[rows_l], max_ctx, self.scale, sm_cap=cap,
-                workspace=self._workspace("local", bl, cap), error_word=self.err, stream=main)
+                workspace=self._workspace("local", bl, cap), error_word=self.err, stream=main,
+                **self.window)
         if br:
             main.wait_stream(self.side)
 
