@@ -76,6 +76,8 @@ typedef enum {
 #define PDA_DEVERR_TIMEOUT 0x8     /* a pipeline wait passed its time limit; results invalid */
 #define PDA_DEVERR_QUERY 0x10      /* query_lens / query_start negative, decreasing or beyond T */
 #define PDA_DEVERR_NO_BLOCKS 0x20  /* free_count out of range, or too few free blocks */
+#define PDA_DEVERR_TOKEN 0x40      /* a drafted token outside [0, V) */
+#define PDA_DEVERR_PROBS 0x80      /* a row to draw from has no positive, finite weight */
 
 /* Bytes of the fixed device scratch behind pda_paged_decode_attention_noalloc. */
 #define PDA_NOALLOC_SCRATCH_BYTES (8u << 20)
@@ -720,6 +722,46 @@ pda_status pda_paged_window_chunk_attention(
     int H_kv, int D, int block_size, int num_blocks, float scale, float k_scale, float v_scale,
     pda_dtype q_dtype, pda_dtype kv_dtype, int sm_cap, void* workspace, size_t workspace_bytes,
     int32_t* error_word, cudaStream_t stream);
+
+/*
+ * pda_verify_drafts -- how many of each request's drafted tokens the target model keeps, and the
+ * token that comes after them: what follows the chunk attention of drafted tokens.
+ *
+ * The pages describe no drafting; the rule is the published one of speculative sampling (accept a
+ * draft x of probability q(x) with probability min(1, p(x) / q(x)); at the first one turned down,
+ * draw from what p has over q), whose tokens are distributed as the target's own. Request b has
+ * the step's rows query_start[b] .. query_start[b + 1): its last token, then d drafts. Row r
+ * holds the target's probabilities p_r of the token behind row r's, and judges row r + 1's:
+ *  - accepted[b] = a, the number of leading drafts with
+ *      accept_u[r] * q_r(tokens[r + 1]) < p_r(tokens[r + 1])     (in fp32);
+ *  - next_tokens[b]: with weights max(p_r - q_r, 0) at the row r that turned its draft down (p_r
+ *    if none of them is positive), or p_r at the request's last row, the first token t whose
+ *    sum of weights up to t exceeds sample_u[b] times their sum.
+ * So the request goes on with its first a drafts and next_tokens[b], and its length falls by
+ * d - a.
+ *
+ *  accepted, next_tokens [B] int32, written.
+ *  target_probs   [T, V] in dtype (PDA_F32, PDA_BF16, PDA_F16), rows target_stride elements apart
+ *                 (>= V). They need not sum to one. A weight that is not positive counts as zero.
+ *  draft_probs    [T, V] in dtype, row r: what the token of row r + 1 was drawn from; rows
+ *                 draft_stride apart; a request's last row is not read. NULL: the drafts were
+ *                 certain (q = 1 at the draft, 0 elsewhere).
+ *  tokens         [T] int32, the step's tokens; a request's first is not read.
+ *  query_start    [B + 1] int32, non-decreasing, within [0, T].
+ *  accept_u       [T] fp32, sample_u [B] fp32: uniform in [0, 1); a request's last accept_u is not
+ *                 read.
+ *  A request without rows gets accepted 0 and token -1; so does one whose query_start decreases or
+ *  leaves [0, T], with PDA_DEVERR_QUERY. A draft outside [0, V) is turned down
+ *  (PDA_DEVERR_TOKEN). Where no weight is positive, or their sum is not finite, next_tokens[b] is
+ *  -1 (PDA_DEVERR_PROBS). Probabilities aligned to their type; rows aligned to 16 bytes are read
+ *  faster. V <= 2^20, B <= 8192, else PDA_ERR_UNSUPPORTED. B == 0 is a no-op.
+ */
+pda_status pda_verify_drafts(int32_t* accepted, int32_t* next_tokens, const void* target_probs,
+                             const void* draft_probs, long long target_stride,
+                             long long draft_stride, const int32_t* tokens,
+                             const int32_t* query_start, const float* accept_u,
+                             const float* sample_u, int T, int B, int V, pda_dtype dtype,
+                             int32_t* error_word, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -12,7 +12,7 @@ from .binding import (PdaDeviceError, PdaError, alloc_chunk_workspace, alloc_wor
                       paged_decode_attention,
                       paged_decode_attention_fp8, paged_decode_attention_nvfp4,
                       paged_decode_attention_noalloc, qk_norm_rope, qk_norm_rope_append,
-                      rope_frequencies, status_string)
+                      rope_frequencies, status_string, verify_drafts)
 
 __all__ = ["PdaDeviceError", "PdaError", "alloc_workspace", "check_error", "attention_workspace_size", "device_sm_count",
            "kv_append", "kv_append_block_scales", "kv_pack_block_scales_batched",
@@ -21,4 +21,5 @@ __all__ = ["PdaDeviceError", "PdaError", "alloc_workspace", "check_error", "atte
            "paged_decode_attention_nvfp4", "paged_decode_attention_noalloc",
            "alloc_chunk_workspace", "chunk_attention_workspace_size", "kv_assign_blocks",
            "kv_build_slots", "paged_chunk_attention", "paged_chunk_attention_fp8",
-           "qk_norm_rope", "qk_norm_rope_append", "rope_frequencies", "status_string"]
+           "qk_norm_rope", "qk_norm_rope_append", "rope_frequencies", "status_string",
+           "verify_drafts"]

@@ -21,6 +21,7 @@ from . import build_lib
 PDA_F32, PDA_BF16, PDA_FP8_E4M3, PDA_NVFP4, PDA_F16 = 0, 1, 2, 3, 4
 PDA_DEVERR_CONTEXT_LEN, PDA_DEVERR_BLOCK_ID, PDA_DEVERR_SLOT, PDA_DEVERR_TIMEOUT = 1, 2, 4, 8
 PDA_DEVERR_QUERY, PDA_DEVERR_NO_BLOCKS = 0x10, 0x20
+PDA_DEVERR_TOKEN, PDA_DEVERR_PROBS = 0x40, 0x80
 PDA_PACK_MAX_BATCH = 64
 PDA_PACK_MAX_LAYERS = 256
 PDA_NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -36,7 +37,7 @@ EXPORTED = [
     "pda_chunk_attention_workspace_size", "pda_paged_chunk_attention",
     "pda_paged_chunk_attention_fp8", "pda_kv_build_slots_positions", "pda_qk_norm_rope_append",
     "pda_qk_norm_rope", "pda_paged_window_attention",
-    "pda_paged_window_chunk_attention",
+    "pda_paged_window_chunk_attention", "pda_verify_drafts",
 ]
 
 _lock = threading.Lock()
@@ -146,6 +147,10 @@ def load():
         lib.pda_paged_chunk_attention_fp8.argtypes = [P, P, P, P, P, I, P, P, I, I, I, I, I, I,
                                                       I, I, F, F, F, I, I, P, SZ, P, P]
         lib.pda_paged_chunk_attention_fp8.restype = I
+        # accepted, next, target, draft, strides, tokens, query_start, uniforms, T, B, V, dtype,
+        # error_word, stream
+        lib.pda_verify_drafts.argtypes = [P, P, P, P, LL, LL, P, P, P, P, I, I, I, I, P, P]
+        lib.pda_verify_drafts.restype = I
         _lib = lib
         return lib
 
@@ -162,7 +167,9 @@ class PdaDeviceError(RuntimeError):
              PDA_DEVERR_SLOT: "slot out of range",
              PDA_DEVERR_TIMEOUT: "pipeline wait timed out",
              PDA_DEVERR_QUERY: "query lengths out of range",
-             PDA_DEVERR_NO_BLOCKS: "too few free blocks"}
+             PDA_DEVERR_NO_BLOCKS: "too few free blocks",
+             PDA_DEVERR_TOKEN: "token out of range",
+             PDA_DEVERR_PROBS: "no probability to draw from"}
 
     def __init__(self, bits: int):
         self.bits = bits
@@ -819,3 +826,40 @@ def paged_chunk_attention_fp8(out, q, k_cache, v_cache, block_tables, context_le
                   (float(scale), float(k_scale), float(v_scale)), out, q, k_cache, v_cache,
                   block_tables, context_lens, query_start, max_context_len, sm_cap, workspace,
                   error_word, stream, (_dtype(q),), window, sinks)
+
+
+def _rows(t, dev: int, name: str, dtype, shape):
+    """Address and row stride of [T, V] rows, dense within a row."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}; all tensors must live on one CUDA device")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
+    by_row, by_element = t.stride()
+    if shape[1] > 1 and by_element != 1:
+        raise ValueError(f"{name}: rows must be dense")
+    return t.data_ptr(), by_row if shape[0] > 1 else shape[1]
+
+
+def verify_drafts(accepted, next_tokens, target_probs, draft_probs, tokens, query_start, accept_u,
+                  sample_u, error_word=None, stream=None):
+    """Per request (rows ``query_start[b]:query_start[b + 1]`` of the step's ``tokens`` [T], its
+    last token and then its drafts), how many leading drafts the target keeps (``accepted`` [B])
+    and the token after them (``next_tokens`` [B]), by speculative sampling from the given
+    uniforms. Row r of ``target_probs`` [T, V] (of ``draft_probs``, which may be None for certain
+    drafts) is the target's (the draft model's) distribution of the token behind row r's."""
+    _require(target_probs.dim() == 2 and accepted.dim() == 1,
+             "target_probs must be [T, V] and accepted [B]")
+    T, V = target_probs.shape
+    B = accepted.shape[0]
+    dev, dt, i32, f32 = _cuda_index(target_probs), target_probs.dtype, torch.int32, torch.float32
+    p, p_stride = _rows(target_probs, dev, "target_probs", dt, (T, V))
+    q, q_stride = ((None, 0) if draft_probs is None else
+                   _rows(draft_probs, dev, "draft_probs", dt, (T, V)))
+    _call(load().pda_verify_drafts, "pda_verify_drafts", dev, stream,
+          _addr(accepted, dev, "accepted", i32), _addr(next_tokens, dev, "next_tokens", i32, (B,)),
+          p, q, p_stride, q_stride, _addr(tokens, dev, "tokens", i32, (T,)),
+          _addr(query_start, dev, "query_start", i32, (B + 1,)),
+          _addr(accept_u, dev, "accept_u", f32, (T,)), _addr(sample_u, dev, "sample_u", f32, (B,)),
+          T, B, V, _dtype(target_probs), _addr(error_word, dev, "error_word"))
+    return accepted, next_tokens
