@@ -12,6 +12,7 @@ import math
 import os
 import threading
 
+import numpy as np
 import torch
 
 from . import build_lib
@@ -267,15 +268,32 @@ def _window_attention(out, q, k_cache, v_cache, block_scales, block_tables, cont
                       max_context_len, window, sinks, scales, kv_dtype, sm_cap, workspace,
                       error_word, stream):
     B, H, D = q.shape
-    NB, bs, H_kv, _ = k_cache.shape
-    _check(load().pda_paged_window_attention(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_scales[0]),
-        _ptr(block_scales[1]), _ptr(block_tables),
-        block_tables.shape[1] if block_tables.dim() == 2 else 0, _ptr(context_lens),
-        int(max_context_len), int(window), int(sinks), B, H, H_kv, D, bs, NB, *scales, _dtype(q),
-        kv_dtype, _dtype(out), int(sm_cap), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(error_word), _stream(stream)),
-        "pda_paged_window_attention")
+    NB, bs, H_kv, row = k_cache.shape
+    _require(block_tables.dim() == 2, "block_tables must be [B, max_blocks]")
+    _require(row == (D // 2 if kv_dtype == PDA_NVFP4 else D),
+             "q and the caches must agree in head size")
+    dev, i32, cache = _cuda_index(q), torch.int32, k_cache.dtype
+    k_bs, v_bs = block_scales
+    if kv_dtype == PDA_NVFP4:
+        _require(k_bs.shape == v_bs.shape == (NB, H_kv, bs, D // 16),
+                 "the block scales must be [NB, H_kv, bs, D / 16]")
+    else:
+        _require(_dtype(k_cache) == kv_dtype, "the caches must hold FP8 E4M3 codes")
+    if workspace is None:  # from the launching stream's pool: reused there only
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            n = ctypes.c_size_t(0)
+            _check(load().pda_attention_workspace_size(B, H, H_kv, D, bs, kv_dtype, int(sm_cap),
+                                                       ctypes.byref(n)), "workspace size")
+            workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=q.device)
+    _call(load().pda_paged_window_attention, "pda_paged_window_attention", dev, stream,
+          _addr(out, dev, "out", None, q.shape), _addr(q, dev, "q"),
+          _addr(k_cache, dev, "k_cache"), _addr(v_cache, dev, "v_cache", cache, k_cache.shape),
+          _addr(k_bs, dev, "k_block_scales"), _addr(v_bs, dev, "v_block_scales"),
+          _addr(block_tables, dev, "block_tables", i32), block_tables.shape[1],
+          _addr(context_lens, dev, "context_lens", i32, (B,)), int(max_context_len), int(window),
+          int(sinks), B, H, H_kv, D, bs, NB, *scales, _dtype(q), kv_dtype, _dtype(out),
+          int(sm_cap), _addr(workspace, dev, "workspace"), workspace.nbytes,
+          _addr(error_word, dev, "error_word"))
     return out
 
 
@@ -285,6 +303,12 @@ def paged_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens,
     """``out[b,h] = softmax(scale q[b,h] K^T) V`` over request b's paged history, or, with a
     ``window``, over its last ``window`` tokens and its first ``sinks`` (blocks without any of
     them are not read)."""
+    if _windowed(window, sinks):
+        _require(_dtype(k_cache) != PDA_FP8_E4M3, "an FP8 cache needs its scales: the _fp8 call")
+        return _window_attention(out, q, k_cache, v_cache, (None, None), block_tables,
+                                 context_lens, max_context_len, window, sinks,
+                                 (float(scale), 1.0, 1.0), _dtype(k_cache), sm_cap, workspace,
+                                 error_word, stream)
     B, H, D = q.shape
     NB, bs, H_kv, D2 = k_cache.shape
     assert D == D2 and v_cache.shape == k_cache.shape and out.shape == q.shape
@@ -292,12 +316,6 @@ def paged_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens,
     max_blocks = block_tables.shape[1] if block_tables.dim() == 2 else 0
     if workspace is None:
         workspace = alloc_workspace(B, H, H_kv, D, bs, k_cache.dtype, sm_cap, q.device)
-    if _windowed(window, sinks):
-        _require(_dtype(k_cache) != PDA_FP8_E4M3, "an FP8 cache needs its scales: the _fp8 call")
-        return _window_attention(out, q, k_cache, v_cache, (None, None), block_tables,
-                                 context_lens, max_context_len, window, sinks,
-                                 (float(scale), 1.0, 1.0), _dtype(k_cache), sm_cap, workspace,
-                                 error_word, stream)
     _check(load().pda_paged_decode_attention(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks,
         _ptr(context_lens), int(max_context_len), B, H, H_kv, D, bs, NB, float(scale),
@@ -313,6 +331,11 @@ def paged_decode_attention_fp8(out, q, k_cache, v_cache, block_tables, context_l
                                stream=None, window: int = 0, sinks: int = 0):
     """Attention over an FP8 E4M3 cache: stored code c of K means decode(c) * k_scale.
     ``window`` and ``sinks`` as in ``paged_decode_attention``."""
+    if _windowed(window, sinks):
+        return _window_attention(out, q, k_cache, v_cache, (None, None), block_tables,
+                                 context_lens, max_context_len, window, sinks,
+                                 (float(scale), float(k_scale), float(v_scale)), PDA_FP8_E4M3,
+                                 sm_cap, workspace, error_word, stream)
     B, H, D = q.shape
     NB, bs, H_kv, D2 = k_cache.shape
     assert D == D2 and v_cache.shape == k_cache.shape and out.shape == q.shape
@@ -321,11 +344,6 @@ def paged_decode_attention_fp8(out, q, k_cache, v_cache, block_tables, context_l
     max_blocks = block_tables.shape[1] if block_tables.dim() == 2 else 0
     if workspace is None:
         workspace = alloc_workspace(B, H, H_kv, D, bs, torch.uint8, sm_cap, q.device)
-    if _windowed(window, sinks):
-        return _window_attention(out, q, k_cache, v_cache, (None, None), block_tables,
-                                 context_lens, max_context_len, window, sinks,
-                                 (float(scale), float(k_scale), float(v_scale)), PDA_FP8_E4M3,
-                                 sm_cap, workspace, error_word, stream)
     _check(load().pda_paged_decode_attention_fp8(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks,
         _ptr(context_lens), int(max_context_len), B, H, H_kv, D, bs, NB, float(scale),
@@ -342,6 +360,11 @@ def paged_decode_attention_nvfp4(out, q, k_data, v_data, k_block_scales, v_block
     """Attention over an NVFP4 cache: data [NB, bs, H_kv, D/2] uint8 (two E2M1 codes per
     byte, even element low), block scales [NB, H_kv, bs, D/16] uint8 (E4M3, per block and
     head-major). ``window`` and ``sinks`` as in ``paged_decode_attention``."""
+    if _windowed(window, sinks):
+        return _window_attention(out, q, k_data, v_data, (k_block_scales, v_block_scales),
+                                 block_tables, context_lens, max_context_len, window, sinks,
+                                 (float(scale), float(k_scale), float(v_scale)), PDA_NVFP4,
+                                 sm_cap, workspace, error_word, stream)
     B, H, D = q.shape
     NB, bs, H_kv, half = k_data.shape
     assert 2 * half == D and v_data.shape == k_data.shape and out.shape == q.shape
@@ -354,11 +377,6 @@ def paged_decode_attention_nvfp4(out, q, k_data, v_data, k_block_scales, v_block
         _check(load().pda_attention_workspace_size(B, H, H_kv, D, bs, PDA_NVFP4, sm_cap,
                                                    ctypes.byref(n)), "workspace size")
         workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=q.device)
-    if _windowed(window, sinks):
-        return _window_attention(out, q, k_data, v_data, (k_block_scales, v_block_scales),
-                                 block_tables, context_lens, max_context_len, window, sinks,
-                                 (float(scale), float(k_scale), float(v_scale)), PDA_NVFP4,
-                                 sm_cap, workspace, error_word, stream)
     _check(load().pda_paged_decode_attention_nvfp4(
         _ptr(out), _ptr(q), _ptr(k_data), _ptr(v_data), _ptr(k_block_scales),
         _ptr(v_block_scales), _ptr(block_tables), max_blocks, _ptr(context_lens),
@@ -640,19 +658,18 @@ def rope_frequencies(rope_dim: int, base: float = 10000.0, stretch: float = 1.0,
     _require(rope_dim >= 0 and rope_dim % 2 == 0, "rope_dim must be even")
     _require(stretch > 0 and high_turns > low_turns, "stretch > 0 and high_turns > low_turns")
     if inv_freq is None:
-        inv_freq = [float(base) ** (-2 * i / rope_dim) for i in range(rope_dim // 2)]
+        inv_freq = float(base) ** (-np.arange(0, rope_dim, 2) / max(rope_dim, 1))
     _require(len(inv_freq) == rope_dim // 2, "inv_freq must hold rope_dim / 2 values")
-    out = []
-    for f in map(float, inv_freq):
-        _require(math.isfinite(f), "frequencies must be finite")
-        keep = 0.0
-        if original_length is not None:
-            turns = original_length * f / (2 * math.pi)
-            keep = min(1.0, max(0.0, (turns - low_turns) / (high_turns - low_turns)))
-        f = f * keep + f / stretch * (1 - keep)
-        n = round(f / (2 * math.pi) * 2.0 ** 64) % 2 ** 64
-        out.append(n - 2 ** 64 if n >= 2 ** 63 else n)
-    return torch.tensor(out, dtype=torch.int64, device=device or "cuda")
+    f = np.asarray(inv_freq, np.float64)
+    _require(np.isfinite(f).all(), "frequencies must be finite")
+    keep = 0.0
+    if original_length is not None:
+        turns = original_length * f / (2 * math.pi)
+        keep = np.clip((turns - low_turns) / (high_turns - low_turns), 0.0, 1.0)
+    f = (f * keep + f / stretch * (1 - keep)) / (2 * math.pi)
+    fixed = np.rint(np.abs(f) % 1.0 * 2.0 ** 64).astype(np.uint64).view(np.int64)
+    fixed = np.where(f < 0, -fixed, fixed)
+    return torch.from_numpy(fixed).to(device or "cuda")
 
 
 def _heads(t, dev: int, name: str, dtype, shape):

@@ -415,6 +415,13 @@ __device__ __forceinline__ void clean_tile(unsigned char* tile, int part, int ke
   }
 }
 
+// A mask of the n lowest bits (none where n < 0, 32 at most).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  uint32_t r;
+  asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(r) : "r"(max(n, 0)));
+  return r;
+}
+
 // Lane q of each quad gives v[c] = its 16 bytes number c and gets v[r] = bytes number q of
 // the quad's lane r.
 __device__ __forceinline__ void quad_transpose(uint4* v) {
@@ -542,6 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = packed >> g_shift;
       const int pos = d.pos0 + min(tok, d.tokens - 1);  // this row's position
       const int first_pos = d.pos0 + ((single ? 0 : g * 128) >> g_shift);
+      // of this warp's first and last row
+      const int warp_pos = kWindow ? __shfl_sync(kFullMask, pos, 0) : 0;
+      const int warp_end = kWindow ? __shfl_sync(kFullMask, pos, 31) : 0;
       float sl = sl_all;  // of a score, in log2 units
       if (kFp8) {
         // this row of Q; where the groups share their rows, group 0's warps store it
@@ -577,19 +587,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < kChunkKeys; k += 32) tmem_arrived32(x + k);
-        if (key0 + kChunkKeys - 1 > first_pos) {
+        if constexpr (kWindow) {
+          // masked where some row of this warp does not see the whole tile, by a bit per key
+          if (key0 + kChunkKeys - 1 > warp_pos ||
+              (key0 <= warp_end - p.window && key0 + kChunkKeys > p.sinks)) {
+#pragma unroll
+            for (int k0 = 0; k0 < kChunkKeys; k0 += 32) {
+              const int at = key0 + k0;
+              const uint32_t seen = low_bits(pos + 1 - at) &
+                                    (~low_bits(pos - p.window + 1 - at) | low_bits(p.sinks - at));
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(seen >> k & 1)) x[k0 + k] = -INFINITY;
+            }
+          }
+        } else if (key0 + kChunkKeys - 1 > first_pos) {
           const int seen = pos - key0;
 #pragma unroll
           for (int k = 0; k < kChunkKeys; ++k)
             if (k > seen) x[k] = -INFINITY;
-        }
-        if constexpr (kWindow) {
-          if (key0 < d.last_lowest && key0 + kChunkKeys - 1 >= p.sinks) {
-            const int from = pos - p.window + 1 - key0, first = p.sinks - key0;
-#pragma unroll
-            for (int k = 0; k < kChunkKeys; ++k)
-              if (k < from && k >= first) x[k] = -INFINITY;
-          }
         }
         float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll

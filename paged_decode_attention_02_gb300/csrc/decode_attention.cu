@@ -288,7 +288,8 @@ pda_status launch_attention(void* out, const void* q, const void* k_cache, const
       per_row = std::min(per_row, (static_cast<long long>(sinks) + kBS - 1) / kBS +
                                       (static_cast<long long>(window) + kBS - 1) / kBS + 1);
     const long long tiles = static_cast<long long>(B) * tiling.H_u * per_row;
-    const long long per_block = static_cast<long long>(pl.nwarps) * PDA_MIN_TILES_PER_WARP;
+    const long long per_block = static_cast<long long>(pl.nwarps) *
+                                (windowed ? kWindowMinTiles : PDA_MIN_TILES_PER_WARP);
     const long long blocks = (tiles + per_block - 1) / per_block;
     if (blocks < pl.grid) {
       pl.grid = static_cast<int>(std::max<long long>(1, blocks));

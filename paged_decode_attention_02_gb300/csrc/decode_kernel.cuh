@@ -70,6 +70,16 @@ namespace pda {
 #define PDA_MIN_TILES_PER_WARP 8
 #endif
 
+// With a window, whose launches are short, a warp takes as few as two tiles, and more where a
+// segment has many: with T tiles over n warps, the tiles take T / n and the merge n, so n follows
+// sqrt(T). 16 requests of 16/2 heads of 64 in bf16: 128 keys 17 us at two tiles and 19 at four,
+// 1024 keys 25 and 23, 4096 keys (one request) 46 and 31.
+constexpr int kWindowMinTiles = 2;
+__device__ __forceinline__ int window_tiles_per_warp(int tiles, int segments) {
+  const float mean = static_cast<float>(tiles) / static_cast<float>(max(segments, 1));
+  return max(kWindowMinTiles, static_cast<int>(sqrtf(mean) * 0.25f));
+}
+
 #ifndef PDA_TC_WARPS
 #define PDA_TC_WARPS 12        // warps (workers) per block of the tensor-core tile step
 #endif
@@ -497,6 +507,15 @@ __device__ __forceinline__ void register_claims(unsigned long long* c, unsigned 
   }
 }
 
+// The same for a window, whose segments' pieces arrive together: the counter is made this call's
+// first, then counted up by additions. (Exchanges that fail and start again take an L2 round trip
+// a piece.)
+__device__ __forceinline__ unsigned arrive_add(unsigned long long* counter,
+                                               unsigned long long call) {
+  register_claims(counter, call);
+  return (static_cast<unsigned>(atomicAdd(counter, 1ull)) & 0xffffu) + 1u;
+}
+
 // Claims the next pool chunk and returns its index (NW k or more once the pool is used up).
 // The tag mix leaves the low 16 bits alone, so the count adds without unmixing; a call makes
 // at most NW k + NW claims, below 2^16.
@@ -615,6 +634,116 @@ __device__ void merge_segment(const AttnParams& p, int b, int h, int w0, int w1,
 #pragma unroll 1
   for (int j0 = 0; j0 < G; j0 += HP)
     merge_heads<D, G, HP>(p, b, h, j0, w0, w1, w0_tail, un, lane);
+}
+
+// The same merge for a window, whose launches are short and a good part of their time the
+// merge's: a lane takes four columns of a head, and eight loads of a lane are in flight at once
+// (with a piece's after the other's, each an L2 round trip, 33 pieces of 8 heads took 50 us).
+template <int D, int G>
+__device__ __forceinline__ void merge_segment_wide(const AttnParams& p, int b, int h, int w0,
+                                                   int w1, bool w0_tail, const Units un,
+                                                   int lane) {
+  constexpr int kHeads = 128 / D;                               // heads of a warp's load
+  constexpr int kSets = (G + kHeads - 1) / kHeads;              // loads of a piece
+  constexpr int kHere = kSets < 4 ? kSets : 4;                  // of them at once
+  constexpr int kBatch = 8 / kHere;                             // pieces at once
+  const int sub = lane / (D / 4);                               // this lane's head of a load
+  auto slot_of = [&](int w) { return 2 * w + ((w == w0 && w0_tail) ? 1 : 0); };
+  const float2* ml = reinterpret_cast<const float2*>(p.ws_ml);
+  // lane i looks at unit w0 + i, w0 + i + 32, ...
+  float M[G], L[G];
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    M[j] = -INFINITY;
+    L[j] = 0.f;
+  }
+  for (int w = w0 + lane; w <= w1; w += 32)
+    if (un.live(w))
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+        M[j] = fmaxf(M[j], __ldcg(ml + static_cast<size_t>(slot_of(w)) * G + j).x);
+#pragma unroll
+  for (int j = 0; j < G; ++j)
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) M[j] = fmaxf(M[j], __shfl_xor_sync(kFullMask, M[j], m));
+  float4 acc[kSets];
+#pragma unroll
+  for (int s = 0; s < kSets; ++s) acc[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int base = w0; base <= w1; base += 32) {
+    const int w = base + lane;
+    const bool mine = w <= w1 && un.live(w);
+    const unsigned live_mask = __ballot_sync(kFullMask, mine);
+    float f[G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      f[j] = 0.f;
+      if (mine) {
+        const float2 v = __ldcg(ml + static_cast<size_t>(slot_of(w)) * G + j);
+        f[j] = ex2(v.x - M[j]);
+        L[j] = fmaf(v.y, f[j], L[j]);
+      }
+    }
+#pragma unroll
+    for (int s0 = 0; s0 < kSets; s0 += kHere) {
+      unsigned rest = live_mask;  // the same on every lane
+#pragma unroll 1
+      while (rest != 0u) {
+        float4 o[kBatch][kHere];
+        int from[kBatch];
+        unsigned todo = rest;
+        // a missing piece of the last batch reads one that is there, and counts nothing
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          from[u] = todo != 0u ? __ffs(todo) - 1 : -1;
+          todo &= todo - 1u;
+          const size_t row = static_cast<size_t>(slot_of(from[u] >= 0 ? base + from[u] : w0)) * G;
+#pragma unroll
+          for (int s = 0; s < kHere; ++s) {
+            const int j = min((s0 + s) * kHeads + sub, G - 1);
+            o[u][s] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + (row + j) * D) +
+                             lane % (D / 4));
+          }
+        }
+        rest = todo;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          if (from[u] < 0) continue;
+#pragma unroll
+          for (int s = 0; s < kHere; ++s) {
+            const int j = (s0 + s) * kHeads;
+            float g = __shfl_sync(kFullMask, f[j], from[u]);
+            if (kHeads == 2 && j + 1 < G) {
+              const float g1 = __shfl_sync(kFullMask, f[j + 1 < G ? j + 1 : j], from[u]);
+              if (sub == 1) g = g1;
+            }
+            float4& to = acc[s0 + s];
+            to.x = fmaf(o[u][s].x, g, to.x);
+            to.y = fmaf(o[u][s].y, g, to.y);
+            to.z = fmaf(o[u][s].z, g, to.z);
+            to.w = fmaf(o[u][s].w, g, to.w);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < G; ++j)
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) L[j] += __shfl_xor_sync(kFullMask, L[j], m);
+#pragma unroll
+  for (int s = 0; s < kSets; ++s) {
+    const int j = s * kHeads + sub;
+    const float l = kHeads == 2 && sub == 1 ? L[s * kHeads + 1 < G ? s * kHeads + 1 : 0]
+                                            : L[s * kHeads];
+    if (j >= G) continue;
+    const float inv = p.v_scale / l;
+    const float v[4] = {acc[s].x * inv, acc[s].y * inv, acc[s].z * inv, acc[s].w * inv};
+    const size_t at = (static_cast<size_t>(b) * p.H + static_cast<size_t>(h) * G + j) * D +
+                      4 * (lane % (D / 4));
+    store_out(p.out, at, v, 2, p.out_kind);
+    store_out(p.out, at + 2, v + 2, 2, p.out_kind);
+  }
 }
 
 // Tiles of the first n >= 0 tokens.
@@ -736,8 +865,8 @@ __global__ void __launch_bounds__(warps_for_mode(G, MODE, std::is_same<KV, nvfp4
   // this launch (the host sized the grid by its bound on the lengths; the lengths on the
   // device may be shorter). The others leave here. Only the CUDA-core step leaves a pool
   // (see make_plan); the tensor-core steps compile without it.
-  const int nw = max(1, min(p.num_workers,
-                            (W_tiles + PDA_MIN_TILES_PER_WARP - 1) / PDA_MIN_TILES_PER_WARP));
+  const int least = kWindow ? window_tiles_per_warp(W_tiles, B * H_kv) : PDA_MIN_TILES_PER_WARP;
+  const int nw = max(1, min(p.num_workers, (W_tiles + least - 1) / least));
   const int wi = blockIdx.x * nwarps + warp;
   if (wi >= nw) return;
   const Units un = make_units(W_tiles, nw, MODE == kModeCuda ? p.pool_k : 0);
@@ -899,6 +1028,7 @@ __global__ void __launch_bounds__(warps_for_mode(G, MODE, std::is_same<KV, nvfp4
     int cb, ch, cblk, cnb;
     locate(t_begin, cb, ch, cblk, cnb);
     bool seg_bad = false;
+    int head_seg = -1, tail_seg = -1;  // segments to merge
 
     for (int x = t_begin; x < t_end; ++x) {
       const bool ready = __all_sync(kFullMask, mbar_wait_bounded(&my_bar[stage], phase));
@@ -975,7 +1105,9 @@ __global__ void __launch_bounds__(warps_for_mode(G, MODE, std::is_same<KV, nvfp4
           __syncwarp();
           const int seg = cb * H_kv + ch;
           unsigned arrived = 0;
-          if (lane == 0) arrived = arrive(p.ws_arrive + seg, p.call);
+          if (lane == 0)
+            arrived = kWindow ? arrive_add(p.ws_arrive + seg, p.call)
+                              : arrive(p.ws_arrive + seg, p.call);
           arrived = __shfl_sync(kFullMask, arrived, 0);
           const int w0 = un.owner(seg_start);
           const int w1 = un.owner(seg_end - 1);
@@ -985,9 +1117,16 @@ __global__ void __launch_bounds__(warps_for_mode(G, MODE, std::is_same<KV, nvfp4
             pieces += __popc(__ballot_sync(kFullMask, ww <= w1 && un.live(ww)));
           }
           if (arrived == pieces) {
-            __threadfence();  // see the other pieces' stores
-            merge_segment<D, G>(p, cb, ch, w0, w1, seg_start != un.start(w0), un, lane);
-            if (lane == 0) atomicExch(p.ws_arrive + seg, arrival_reset(p.call));
+            if constexpr (kWindow) {  // merged behind the unit's tiles
+              if (seg_start <= t_begin)
+                head_seg = seg;
+              else
+                tail_seg = seg;
+            } else {
+              __threadfence();  // see the other pieces' stores
+              merge_segment<D, G>(p, cb, ch, w0, w1, seg_start != un.start(w0), un, lane);
+              if (lane == 0) atomicExch(p.ws_arrive + seg, arrival_reset(p.call));
+            }
           }
         }
       }
@@ -1001,6 +1140,22 @@ __global__ void __launch_bounds__(warps_for_mode(G, MODE, std::is_same<KV, nvfp4
           } while (cb < B && s_pre[cb + 1] == s_pre[cb]);
         }
         if (cb < B) cnb = s_pre[cb + 1] - s_pre[cb];
+      }
+    }
+    if constexpr (kWindow) {
+      // Segments whose last piece this unit brought: at most its first and its last. Behind the
+      // loop, so that the merge's registers are not held beside the tiles' (within it, it spilled
+      // them: 690 us for 633 on 256 requests over 4100 keys).
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        const int seg = k == 0 ? head_seg : tail_seg;
+        if (seg < 0) continue;
+        const int mb = seg / H_kv, mh = seg - mb * H_kv, nb = s_pre[mb + 1] - s_pre[mb];
+        const int seg_start = s_pre[mb] * H_kv + mh * nb;
+        const int w0 = un.owner(seg_start), w1 = un.owner(seg_start + nb - 1);
+        __threadfence();  // see the other pieces' stores
+        merge_segment_wide<D, G>(p, mb, mh, w0, w1, seg_start != un.start(w0), un, lane);
+        if (lane == 0) atomicExch(p.ws_arrive + seg, arrival_reset(p.call));
       }
     }
     claimed = __shfl_sync(kFullMask, next_claim, 0);

@@ -43,7 +43,7 @@ struct RopeParams {
   const void* k_weight;
   int32_t* error_word;
   int T, H, H_kv, D, R;
-  int parts, steps_per_warp;  // warps of a token
+  int group_rows, groups_per_warp, parts;  // parts: warps of a token
   long long num_slots;
   float eps, factor, per_k, per_v;  // codes: 1 / scale
 };
@@ -111,12 +111,14 @@ __device__ __forceinline__ void store8(fp8e4m3* p, const float* x) {
   *reinterpret_cast<uint2*>(p) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-// A warp takes one token's steps [part * steps_per_warp, + 1): a step is 32 / LPR head rows of
-// one kind, queries first, then keys, then values. LPR lanes share a row, eight elements each
-// (those behind D idle). With y the pair's other element, the weights folded into the angle:
+// A step is 32 / LPR head rows of one kind (queries, then keys, then values), LPR lanes sharing a
+// row, eight elements each (kWhole: D = 8 LPR; otherwise those behind D idle); up to kRopeSteps
+// steps of a kind make a group, whose loads are in flight together and under the group before. A
+// warp takes one token's groups [part * groups_per_warp, + 1). With y the pair's other element, the
+// weights folded into the angle:
 //   out = rsqrt(mean x^2 + eps) (x (w c) + y (+- w_y s)).
-template <typename E, typename KV, int LPR, bool kHalf>
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeParams p) {
+template <typename E, typename KV, int LPR, bool kHalf, bool kWhole>
+__global__ void __launch_bounds__(kRopeThreads, 5) qk_rope_kernel(const RopeParams p) {
   constexpr int kRows = 32 / LPR;                                  // rows of a step
   __shared__ float2 trig[kRopeThreads / 32][kRopeMaxHead / 2];     // (cos, sin) of the pairs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -125,45 +127,46 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeParams 
   const unsigned t = task / static_cast<unsigned>(p.parts);
   if (t >= static_cast<unsigned>(p.T)) return;
   const int part = static_cast<int>(task - t * p.parts);
-  const size_t token = t;
+  const int D = kWhole ? LPR * kRopeVec : p.D;
   const int half_lanes = p.R / (2 * kRopeVec);
-  const bool live = d0 < p.D, turns = d0 < p.R, first_half = cl < half_lanes;
+  const bool live = kWhole || d0 < D, turns = d0 < p.R, first_half = cl < half_lanes;
   const int partner = turns ? (first_half ? lane + half_lanes : lane - half_lanes) : lane;
-  const int q_steps = (p.H + kRows - 1) / kRows, k_steps = (p.H_kv + kRows - 1) / kRows;
-  const int all = q_steps + (p.v != nullptr ? 2 : 1) * k_steps;
-  const int s0 = part * p.steps_per_warp, s1 = min(all, s0 + p.steps_per_warp);
-  if (s0 >= s1) return;
+  const int q_groups = (p.H + p.group_rows - 1) / p.group_rows;
+  const int k_groups = (p.H_kv + p.group_rows - 1) / p.group_rows;
+  const int all = q_groups + (p.v != nullptr ? 2 : 1) * k_groups;
+  const int g0 = part * p.groups_per_warp, g1 = min(all, g0 + p.groups_per_warp);
+  if (g0 >= g1) return;
 
-  // this lane's place in step s's row (nullptr: none), and the row's head
-  auto source = [&](int s, int* head) -> const E* {
-    const int h_k = s - q_steps, h_v = h_k - k_steps;
-    const E* base;
-    long long stride;
-    int h, n;
-    if (h_k < 0) {
-      base = static_cast<const E*>(p.q), stride = p.q_stride, h = s * kRows + sub, n = p.H;
-    } else if (h_v < 0) {
-      base = static_cast<const E*>(p.k), stride = p.k_stride, h = h_k * kRows + sub, n = p.H_kv;
-    } else {
-      base = static_cast<const E*>(p.v), stride = p.v_stride, h = h_v * kRows + sub, n = p.H_kv;
-    }
-    *head = h;
-    return live && h < n ? base + token * stride + h * p.D + d0 : nullptr;
+  // group g's kind (0 queries, 1 keys, 2 values), this lane's first row and the end of its rows
+  struct Group {
+    int kind, row, end;
+  };
+  auto group = [&](int g) {
+    Group r;
+    r.kind = g < q_groups ? 0 : g < q_groups + k_groups ? 1 : 2;
+    const int first = (g - (r.kind == 0 ? 0 : q_groups) - (r.kind == 2 ? k_groups : 0)) *
+                      p.group_rows;
+    r.row = first + sub;
+    r.end = min(first + p.group_rows, r.kind == 0 ? p.H : p.H_kv);
+    return r;
   };
   Raw<E> x[kRopeSteps];
-  auto load = [&](int s) {
+  auto load = [&](const Group& g) {
+    const E* base = static_cast<const E*>(g.kind == 0 ? p.q : g.kind == 1 ? p.k : p.v) +
+                    static_cast<long long>(t) *
+                        (g.kind == 0 ? p.q_stride : g.kind == 1 ? p.k_stride : p.v_stride) +
+                    g.row * D + d0;
 #pragma unroll
     for (int u = 0; u < kRopeSteps; ++u) {
-      int h;
-      const E* at = s + u < s1 ? source(s + u, &h) : nullptr;
-      if (at != nullptr)
-        x[u].load(at);
+      if (live && g.row + u * kRows < g.end)
+        x[u].load(base + u * kRows * D);
       else
 #pragma unroll
         for (int i = 0; i < Raw<E>::kWords; ++i) x[u].w[i] = 0;
     }
   };
-  load(s0);
+  Group next = group(g0);
+  load(next);
   const long long slot = p.slots != nullptr ? p.slots[t] : static_cast<long long>(t);
   const unsigned long long pos =
       static_cast<unsigned long long>(static_cast<long long>(p.positions[t]));
@@ -174,9 +177,9 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeParams 
     trig[warp][i] = make_float2(cs * p.factor, sn * p.factor);
   }
   __syncwarp();
-  const float inv_d = 1.f / static_cast<float>(p.D);
-  float c[kRopeVec], s_[kRopeVec];
-  // c, s_ of a kind's rows
+  const float inv_d = 1.f / static_cast<float>(D);
+  float c[kRopeVec], s[kRopeVec];
+  // c, s of a kind's rows
   auto angles = [&](const void* weight) {
     float w[kRopeVec], wy[kRopeVec];
 #pragma unroll
@@ -194,38 +197,43 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeParams 
         v = trig[warp][kHalf ? d0 + e - (first_half ? 0 : p.R / 2) : (d0 + e) / 2];
       c[e] = w[e] * v.x;
       if (kHalf)
-        s_[e] = first_half ? -(wy[e] * v.y) : wy[e] * v.y;
+        s[e] = first_half ? -(wy[e] * v.y) : wy[e] * v.y;
       else
-        s_[e] = (e & 1) == 0 ? -(w[e + 1] * v.y) : w[e - 1] * v.y;
+        s[e] = (e & 1) == 0 ? -(w[e + 1] * v.y) : w[e - 1] * v.y;
     }
   };
-  int kind = -1;  // of c and s_: 0 queries, 1 keys
-  bool bad_slot = false;
-  for (int s = s0; s < s1; s += kRopeSteps) {
-    Raw<E> now[kRopeSteps];
+  int kind = -1;  // of c and s
+  for (int g = g0; g < g1; ++g) {
+    const Group now = next;
+    Raw<E> in[kRopeSteps];
 #pragma unroll
-    for (int u = 0; u < kRopeSteps; ++u) now[u] = x[u];
-    if (s + kRopeSteps < s1) load(s + kRopeSteps);
+    for (int u = 0; u < kRopeSteps; ++u) in[u] = x[u];
+    if (g + 1 < g1) {
+      next = group(g + 1);
+      load(next);
+    }
+    const void* weight = now.kind == 0 ? p.q_weight : p.k_weight;
+    if (now.kind != 2 && now.kind != kind) {
+      kind = now.kind;
+      angles(weight);
+    }
+    // where the group's rows go; nothing is written where a slot is not one
+    const bool write = now.kind == 0 || (slot >= 0 && slot < p.num_slots);
+    const size_t to = (now.kind == 0 ? static_cast<size_t>(t) * p.H
+                                     : static_cast<size_t>(write ? slot : 0) * p.H_kv) * D +
+                      now.row * D + d0;
 #pragma unroll
     for (int u = 0; u < kRopeSteps; ++u) {
-      if (s + u >= s1) break;
-      int h;
-      const bool there = source(s + u, &h) != nullptr;
-      const bool is_q = s + u < q_steps, is_v = s + u >= q_steps + k_steps;
+      if (now.row - sub + u * kRows >= now.end) break;
       float o[kRopeVec];
-      now[u].widen(o);
-      if (!is_v) {
-        const void* weight = is_q ? p.q_weight : p.k_weight;
-        if (kind != (is_q ? 0 : 1)) {
-          kind = is_q ? 0 : 1;
-          angles(weight);
-        }
+      in[u].widen(o);
+      if (now.kind != 2) {
         float y[kRopeVec];
         if (kHalf) {
           Raw<E> other;
 #pragma unroll
           for (int i = 0; i < Raw<E>::kWords; ++i) {
-            other.w[i] = __shfl_sync(kFullMask, now[u].w[i], partner);
+            other.w[i] = __shfl_sync(kFullMask, in[u].w[i], partner);
             if (!turns) other.w[i] = 0;
           }
           other.widen(y);
@@ -250,38 +258,38 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeParams 
 #pragma unroll
         for (int e = 0; e < kRopeVec; e += 2) {
           float2 v = __fmul2_rn(make_float2(o[e], o[e + 1]), make_float2(c[e], c[e + 1]));
-          v = __ffma2_rn(make_float2(y[e], y[e + 1]), make_float2(s_[e], s_[e + 1]), v);
+          v = __ffma2_rn(make_float2(y[e], y[e + 1]), make_float2(s[e], s[e + 1]), v);
           v = __fmul2_rn(v, rs2);
           o[e] = v.x;
           o[e + 1] = v.y;
         }
       }
-      if (!there) continue;
-      if (is_q) {
-        store8(static_cast<E*>(p.q_out) + (token * p.H + h) * p.D + d0, o);
-      } else if (slot >= p.num_slots) {
-        bad_slot = true;
-      } else if (slot >= 0) {
+      if (!write || !live || now.row + u * kRows >= now.end) continue;
+      const size_t at = to + u * kRows * D;
+      if (now.kind == 0) {
+        store8(static_cast<E*>(p.q_out) + at, o);
+      } else {
         if constexpr (std::is_same<KV, fp8e4m3>::value) {
-          const float per = is_v ? p.per_v : p.per_k;
+          const float per = now.kind == 2 ? p.per_v : p.per_k;
 #pragma unroll
           for (int e = 0; e < kRopeVec; ++e) o[e] *= per;
         }
-        store8(static_cast<KV*>(is_v ? p.v_out : p.k_out) +
-                   (static_cast<size_t>(slot) * p.H_kv + h) * p.D + d0,
-               o);
+        store8(static_cast<KV*>(now.kind == 2 ? p.v_out : p.k_out) + at, o);
       }
     }
   }
-  if (bad_slot) atomic_or_error(p.error_word, PDA_DEVERR_SLOT);
+  if (slot >= p.num_slots && lane == 0) atomic_or_error(p.error_word, PDA_DEVERR_SLOT);
 }
 
 template <typename E, typename KV, int LPR>
 void launch_layout(const RopeParams& p, bool interleaved, dim3 grid, cudaStream_t stream) {
+  const bool whole = p.D == LPR * kRopeVec;
   if (interleaved)
-    qk_rope_kernel<E, KV, LPR, false><<<grid, kRopeThreads, 0, stream>>>(p);
+    (whole ? qk_rope_kernel<E, KV, LPR, false, true> : qk_rope_kernel<E, KV, LPR, false, false>)
+        <<<grid, kRopeThreads, 0, stream>>>(p);
   else
-    qk_rope_kernel<E, KV, LPR, true><<<grid, kRopeThreads, 0, stream>>>(p);
+    (whole ? qk_rope_kernel<E, KV, LPR, true, true> : qk_rope_kernel<E, KV, LPR, true, false>)
+        <<<grid, kRopeThreads, 0, stream>>>(p);
 }
 
 template <typename E, typename KV>
@@ -323,13 +331,20 @@ pda_status launch_rope(RopeParams p, pda_dtype dtype, pda_dtype kv_dtype, bool i
   int dev, sms;
   const pda_status st = current_device_sms(&dev, &sms);
   if (st != PDA_OK) return st;
-  // A warp takes a token; with few tokens their steps are spread over several, down to one each.
+  // A warp takes a token; with few tokens their groups are spread over several warps, down to
+  // groups of one step each.
   const int rows = p.D <= 64 ? 4 : p.D <= 128 ? 2 : 1;  // of a step
-  const int steps = (p.H + rows - 1) / rows + (p.H_kv + rows - 1) / rows * (p.v != nullptr ? 2 : 1);
-  const long long want = static_cast<long long>(sms) * kRopeWarpsPerSm;
-  const long long parts = std::min<long long>(steps, std::max<long long>(1, want / p.T));
-  p.steps_per_warp = static_cast<int>((steps + parts - 1) / parts);
-  p.parts = (steps + p.steps_per_warp - 1) / p.steps_per_warp;
+  const long long want = static_cast<long long>(sms) * kRopeWarpsPerSm / p.T;  // warps of a token
+  int groups = 0;
+  for (int steps = kRopeSteps; steps >= 1; steps >>= 1) {
+    p.group_rows = rows * steps;
+    groups = (p.H + p.group_rows - 1) / p.group_rows +
+             (p.H_kv + p.group_rows - 1) / p.group_rows * (p.v != nullptr ? 2 : 1);
+    if (groups >= want) break;
+  }
+  const long long parts = std::min<long long>(groups, std::max<long long>(1, want));
+  p.groups_per_warp = static_cast<int>((groups + parts - 1) / parts);
+  p.parts = (groups + p.groups_per_warp - 1) / p.groups_per_warp;
   const long long blocks =
       (static_cast<long long>(p.T) * p.parts + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   const dim3 grid(static_cast<unsigned>(blocks));
@@ -359,7 +374,7 @@ extern "C" pda_status pda_qk_norm_rope_append(
     cudaStream_t stream) {
   RopeParams p{q_out, q, k, v, q_stride, k_stride, v_stride, k_cache, v_cache, slot_mapping,
                positions, reinterpret_cast<const unsigned long long*>(freqs), q_weight, k_weight,
-               error_word, T, H, H_kv, D, rope_dim, 0, 0,
+               error_word, T, H, H_kv, D, rope_dim, 0, 0, 0,
                static_cast<long long>(num_blocks) * block_size, eps, attention_factor,
                1.f / k_scale, 1.f / v_scale};
   if (block_size <= 0 || num_blocks <= 0 || !dtype_ok(kv_dtype) || !isfinite(k_scale) ||
@@ -384,7 +399,7 @@ extern "C" pda_status pda_qk_norm_rope(void* q_out, void* k_out, const void* q, 
                                        cudaStream_t stream) {
   const RopeParams p{q_out, q, k, nullptr, q_stride, k_stride, 0, k_out, nullptr, nullptr,
                      positions, reinterpret_cast<const unsigned long long*>(freqs), q_weight,
-                     k_weight, nullptr, T, H, H_kv, D, rope_dim, 0, 0, T, eps, attention_factor,
+                     k_weight, nullptr, T, H, H_kv, D, rope_dim, 0, 0, 0, T, eps, attention_factor,
                      1.f, 1.f};
   const pda_status st = check_rope(p, dtype);
   if (st != PDA_OK) return st;

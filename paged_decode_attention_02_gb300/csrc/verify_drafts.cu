@@ -11,13 +11,15 @@
 // elsewhere.
 //
 // Sums. The answer is a whole number that depends on sums over the whole vocabulary, so a sum is
-// kept to about 2^-46: a lane adds its eight values in 32 bits with the error of every addition
-// kept (the two-sum of Knuth), everything above that in 64 bits.
+// kept to about 2^-44, as a 32-bit value and what its additions lost (the two-sum of Knuth). An SM
+// does two 64-bit additions a cycle, each a long wait for the next: sums of that type took 36 us
+// for 64 requests of 131072 tokens.
 //
 // What bounds it: the two rows that a request draws from, read once (the accepted drafts cost a
-// few loads each). A cluster of blocks shares a request's vocabulary; each keeps the sums of its
-// own tiles of 256 tokens in shared memory, their totals meet over the cluster's shared memory,
-// and the one warp whose tile holds the answer reads that tile again: one launch, no workspace.
+// few loads each), after a chain of three loads that finds them. A cluster of blocks shares a
+// request's vocabulary; each keeps the sums of its own tiles in shared memory, their totals meet
+// over the cluster's shared memory, and the one warp whose tile holds the answer reads that tile
+// again: one launch, no workspace.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -31,10 +33,10 @@ namespace {
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kLaneTokens = 8;                  // consecutive tokens of a lane
-constexpr int kTileTokens = 32 * kLaneTokens;   // of a warp's step
+constexpr int kStepTokens = 32 * kLaneTokens;   // of a warp's step; a tile is 1, 2 or 4 of them
 constexpr int kVerifyCluster = 8;               // blocks of a request
 constexpr int kMaxVocab = 1 << 20;
-constexpr int kMaxTiles = kMaxVocab / kTileTokens / kVerifyCluster;  // of a block
+constexpr int kMaxTiles = kMaxVocab / kStepTokens / kVerifyCluster;  // of a block
 
 struct VerifyParams {
   int32_t* accepted;
@@ -55,54 +57,116 @@ __device__ __forceinline__ float widen1(E v) {
   return static_cast<float>(v);
 }
 
-// Eight probabilities from token v on (zeros behind V). kWide: rows are 16-byte aligned.
-template <typename E, bool kWide>
+// Eight probabilities, of tokens v, v + kApart, ... (zeros behind V). kWide: rows are 16-byte
+// aligned.
+template <typename E, bool kWide, int kApart>
 __device__ __forceinline__ void load_row(const E* row, int v, int V, float* x) {
-  if (kWide && v + kLaneTokens <= V) {
+  if (kWide && kApart == 1 && v + kLaneTokens <= V) {
     load_elems<E, kLaneTokens>(row + v, x);
     return;
   }
 #pragma unroll
-  for (int e = 0; e < kLaneTokens; ++e) x[e] = v + e < V ? widen1(row[v + e]) : 0.f;
+  for (int e = 0; e < kLaneTokens; ++e)
+    x[e] = v + e * kApart < V ? widen1(row[v + e * kApart]) : 0.f;
 }
 
-// The weight of each of a lane's eight tokens; a weight that is no positive number counts as zero.
-template <typename E, bool kWide>
+// The weights of a lane's eight tokens; one that is no positive number counts as zero.
+template <typename E, bool kWide, int kApart>
 __device__ __forceinline__ void weights(const E* p_row, const E* q_row, int without, int v, int V,
                                         float* r) {
-  load_row<E, kWide>(p_row, v, V, r);
+  load_row<E, kWide, kApart>(p_row, v, V, r);
   if (q_row != nullptr) {
     float q[kLaneTokens];
-    load_row<E, kWide>(q_row, v, V, q);
+    load_row<E, kWide, kApart>(q_row, v, V, q);
 #pragma unroll
     for (int e = 0; e < kLaneTokens; ++e) r[e] -= q[e];
   }
 #pragma unroll
   for (int e = 0; e < kLaneTokens; ++e) {
-    if (v + e == without) r[e] = 0.f;
+    if (v + e * kApart == without) r[e] = 0.f;
     r[e] = fmaxf(r[e], 0.f);  // NaN gives 0
   }
 }
 
-// The sum of eight values and what its additions lost, in 64 bits.
-__device__ __forceinline__ double sum8(const float* r) {
-  float s = r[0], lost = 0.f;
-#pragma unroll
-  for (int e = 1; e < kLaneTokens; ++e) {
-    const float t = s + r[e], back = t - s;
-    lost += (s - (t - back)) + (r[e] - back);
+// A sum and what its additions lost.
+struct Sum {
+  float s, lost;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, back = t - s;
+    lost += (s - (t - back)) + (x - back);
     s = t;
   }
-  return static_cast<double>(s) + static_cast<double>(lost);
+  __device__ __forceinline__ void add(Sum o) {
+    lost += o.lost;
+    add(o.s);
+  }
+  __device__ __forceinline__ Sum minus(Sum o) const {
+    Sum d = *this;
+    d.add(Sum{-o.s, -o.lost});
+    return d;
+  }
+  __device__ __forceinline__ bool above(Sum o) const { return (s - o.s) + (lost - o.lost) > 0.f; }
+  __device__ __forceinline__ bool positive() const { return s + lost > 0.f; }
+};
+
+// The sum of eight values, in two chains.
+__device__ __forceinline__ Sum sum8(const float* r) {
+  Sum a{r[0], 0.f}, b{r[1], 0.f};
+#pragma unroll
+  for (int e = 2; e < kLaneTokens; e += 2) {
+    a.add(r[e]);
+    b.add(r[e + 1]);
+  }
+  a.add(b);
+  return a;
 }
 
-template <typename E, bool kWide>
-__global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerifyThreads)
+__device__ __forceinline__ Sum from_lane(Sum x, int lane) {
+  return Sum{__shfl_sync(kFullMask, x.s, lane), __shfl_sync(kFullMask, x.lost, lane)};
+}
+
+// On every lane, the sum over the lanes.
+__device__ __forceinline__ Sum over_lanes(Sum x) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1)
+    x.add(Sum{__shfl_xor_sync(kFullMask, x.s, o), __shfl_xor_sync(kFullMask, x.lost, o)});
+  return x;
+}
+
+// The sum over this lane and those below.
+__device__ __forceinline__ Sum up_to_lane(Sum x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sum y{__shfl_up_sync(kFullMask, x.s, o), __shfl_up_sync(kFullMask, x.lost, o)};
+    if (lane >= o) x.add(y);
+  }
+  return x;
+}
+
+// Lanes hold consecutive stretches of sum x. Finds the first past `goal` (else the last positive
+// one; -1: there is none) and takes what lies before it off the goal.
+struct Found {
+  int lane;
+  bool past;
+};
+__device__ __forceinline__ Found find(Sum x, Sum* goal) {
+  const Sum end = up_to_lane(x);
+  const unsigned over = __ballot_sync(kFullMask, x.positive() && end.above(*goal));
+  const unsigned some = __ballot_sync(kFullMask, x.positive());
+  const int lane = over != 0 ? __ffs(over) - 1 : 31 - __clz(some);
+  const Sum before = from_lane(end, lane > 0 ? lane - 1 : 0);
+  if (lane > 0) *goal = goal->minus(before);
+  return Found{lane, over != 0};
+}
+
+template <typename E, bool kWide, int kSteps>
+__global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerifyThreads, 4)
     verify_kernel(const VerifyParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ double tile_sum[kMaxTiles];
-  __shared__ double total[2][kVerifyCluster];  // of each block of the cluster, in each pass
+  __shared__ Sum tile_sum[kMaxTiles];
+  __shared__ Sum total[2][kVerifyCluster];  // of each block of the cluster, in each pass
   __shared__ int first_rejected;
   const int rank = static_cast<int>(cluster.block_rank());
   const int b = static_cast<int>(blockIdx.x) / kVerifyCluster;
@@ -156,124 +220,146 @@ __global__ void __cluster_dims__(kVerifyCluster, 1, 1) __launch_bounds__(kVerify
   int pass = 0;
   const E* q_row = nullptr;
   int without = -1;
-  double all = 0.0, before = 0.0;
+  Sum mine, all;  // lane k: block k's total; every lane: the cluster's
   for (;; ++pass) {
     const bool rest = pass == 0 && a < drafts;
     q_row = rest && p.draft != nullptr
                 ? static_cast<const E*>(p.draft) + row * p.draft_stride
                 : nullptr;
     without = rest && p.draft == nullptr ? rejected : -1;
+    // rows of odd alignment are read a token a lane
+    constexpr int kApart = kWide ? 1 : 32;
     for (int t = warp; t < p.tiles; t += kVerifyWarps) {
-      const int v = (tile0 + t) * kTileTokens + lane * kLaneTokens;
-      float r[kLaneTokens];
-      weights<E, kWide>(p_row, q_row, without, v, p.V, r);
-      double s = sum8(r);
+      Sum sum{0.f, 0.f};
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
-      if (lane == 0) tile_sum[t] = s;
+      for (int k = 0; k < kSteps; ++k) {
+        const int v = ((tile0 + t) * kSteps + k) * kStepTokens + lane * (kWide ? kLaneTokens : 1);
+        float r[kLaneTokens];
+        weights<E, kWide, kApart>(p_row, q_row, without, v, p.V, r);
+        sum.add(sum8(r));
+      }
+      sum = over_lanes(sum);
+      if (lane == 0) tile_sum[t] = sum;
     }
     __syncthreads();
     if (pass == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (warp == 0) {
-      double s = 0.0;
-      for (int t = lane; t < p.tiles; t += 32) s += tile_sum[t];
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
+      Sum s{0.f, 0.f};
+      for (int t = lane; t < p.tiles; t += 32) s.add(tile_sum[t]);
+      s = over_lanes(s);
       if (lane < kVerifyCluster) *cluster.map_shared_rank(&total[pass][rank], lane) = s;
     }
     cluster.sync();
-    all = before = 0.0;
-    for (int k = 0; k < kVerifyCluster; ++k) {
-      if (k == rank) before = all;
-      all += total[pass][k];
-    }
-    if (all > 0.0 || !rest) break;  // the second pass is never `rest`
+    mine = lane < kVerifyCluster ? total[pass][lane] : Sum{0.f, 0.f};
+    all = over_lanes(mine);
+    if (all.positive() || !rest) break;  // the second pass is never `rest`
   }
-  if (rank == 0 && tid == 0) {
+  if (warp != 0) return;
+
+  const bool usable = all.positive() && isfinite(all.s) && isfinite(all.lost);
+  if (rank == 0 && lane == 0) {
     p.accepted[b] = a;
-    if (!(all > 0.0 && isfinite(all))) {
+    if (!usable) {
       p.next_tokens[b] = -1;
       atomic_or_error(p.error_word, PDA_DEVERR_PROBS);
     }
   }
-  if (!(all > 0.0 && isfinite(all))) return;
-  // ---- the block, the tile and the lane that the answer lies in
-  const double u = fmin(fmax(static_cast<double>(p.sample_u[b]), 0.0), 1.0);
-  double goal = u * all;
-  // u = 1, or sums in another order: the last token with a weight
-  int last_block = 0;
-  {
-    double run = 0.0;
-    int found = -1;
-    for (int k = 0; k < kVerifyCluster; ++k) {
-      const double s = total[pass][k];
-      if (s > 0.0) last_block = k;
-      run += s;
-      if (found < 0 && run > goal) found = k;
+  if (!usable) return;
+  // ---- the block, the tile, the step and the lane that the answer lies in; where sums in another
+  // order leave none past the goal (or u = 1), the last with a weight
+  const float u = fminf(fmaxf(p.sample_u[b], 0.f), 1.f);
+  Sum goal{u * all.s, 0.f};
+  goal.lost = fmaf(u, all.s, -goal.s) + u * all.lost;
+  const Found block = find(mine, &goal);
+  if (block.lane != rank) return;
+  bool past = block.past;
+  if (!past) goal.s = INFINITY;
+  int tile = -1;
+  for (int t0 = 0; t0 < p.tiles; t0 += 32) {
+    const Sum s = t0 + lane < p.tiles ? tile_sum[t0 + lane] : Sum{0.f, 0.f};
+    Sum left = goal;
+    const Found f = find(s, &left);
+    if (f.lane >= 0) tile = t0 + f.lane;
+    if (f.past) {
+      goal = left;
+      break;
     }
-    const bool none = found < 0;
-    if (none) found = last_block;
-    if (found != rank || warp != 0) return;
-    goal = none ? INFINITY : goal - before;
+    past = past && t0 + 32 < p.tiles;
+    goal = goal.minus(over_lanes(s));
   }
-  double run = 0.0;
-  int tile = -1, last_tile = 0;
-  double tile_goal = INFINITY;
-  for (int t0 = 0; t0 < p.tiles && tile < 0; t0 += 32) {
-    const double s = t0 + lane < p.tiles ? tile_sum[t0 + lane] : 0.0;
-    double end = s;
+  if (!past) goal.s = INFINITY;
+  float r[kSteps][kLaneTokens];
+  Sum step[kSteps];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(kFullMask, end, o);
-      if (lane >= o) end += y;
-    }
-    const unsigned over = __ballot_sync(kFullMask, run + end > goal);
-    const unsigned some = __ballot_sync(kFullMask, s > 0.0);
-    if (over != 0) {
-      const int l = __ffs(over) - 1;
-      tile = t0 + l;
-      tile_goal = goal - (run + __shfl_sync(kFullMask, end - s, l));
-    } else if (some != 0) {
-      last_tile = t0 + 31 - __clz(some);
-    }
-    run += __shfl_sync(kFullMask, end, 31);
-  }
-  if (tile < 0) tile = last_tile;
-  const int v = (tile0 + tile) * kTileTokens + lane * kLaneTokens;
-  float r[kLaneTokens];
-  weights<E, kWide>(p_row, q_row, without, v, p.V, r);
-  const double s = sum8(r);
-  double end = s;
+  for (int k = 0; k < kSteps; ++k)
+    weights<E, kWide, 1>(p_row, q_row, without,
+                         ((tile0 + tile) * kSteps + k) * kStepTokens + lane * kLaneTokens, p.V,
+                         r[k]);
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(kFullMask, end, o);
-    if (lane >= o) end += y;
+  for (int k = 0; k < kSteps; ++k) step[k] = sum8(r[k]);
+  int at = 0;  // the step
+  if (kSteps > 1) {
+    Sum whole{0.f, 0.f};  // lane k: step k's
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const Sum s = over_lanes(step[k]);
+      if (lane == k) whole = s;
+    }
+    const Found f = find(whole, &goal);
+    at = f.lane;
+    if (!f.past) goal.s = INFINITY;
   }
-  // this lane's first token past the goal, and its last with a weight
-  double at = end - s;
-  int hit = -1, last = -1;
+#pragma unroll
+  for (int k = 1; k < kSteps; ++k)
+    if (k == at) {
+      step[0] = step[k];
+#pragma unroll
+      for (int e = 0; e < kLaneTokens; ++e) r[0][e] = r[k][e];
+    }
+  const Found f = find(step[0], &goal);
+  if (!f.past) goal.s = INFINITY;
+  if (lane != f.lane) return;
+  Sum end{0.f, 0.f};
+  int hit = -1, last = 0;
 #pragma unroll
   for (int e = 0; e < kLaneTokens; ++e) {
-    at += static_cast<double>(r[e]);
-    if (r[e] > 0.f) {
-      last = v + e;
-      if (hit < 0 && at > tile_goal) hit = v + e;
+    end.add(r[0][e]);
+    if (r[0][e] > 0.f) {
+      last = e;
+      if (hit < 0 && end.above(goal)) hit = e;
     }
   }
-  const unsigned hits = __ballot_sync(kFullMask, hit >= 0);
-  const unsigned lasts = __ballot_sync(kFullMask, last >= 0);
-  const int from = hits != 0 ? __ffs(hits) - 1 : lasts != 0 ? 31 - __clz(lasts) : 0;
-  const int token = __shfl_sync(kFullMask, hits != 0 ? hit : last, from);
-  if (lane == 0) p.next_tokens[b] = token;
+  p.next_tokens[b] = ((tile0 + tile) * kSteps + at) * kStepTokens + lane * kLaneTokens +
+                     (hit >= 0 ? hit : last);
+}
+
+template <typename E, bool kWide>
+void launch_steps(VerifyParams p, int B, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(B) * kVerifyCluster);
+  const int steps = (p.V + kStepTokens - 1) / kStepTokens;
+  auto tiles = [&](int of) {
+    return ((steps + of - 1) / of + kVerifyCluster - 1) / kVerifyCluster;
+  };
+  // the longest tile that still gives every warp of the cluster one: a tile's sum over the lanes
+  // costs about as much as a step of it
+  if (steps >= 4 * kVerifyCluster * kVerifyWarps) {
+    p.tiles = tiles(4);
+    verify_kernel<E, kWide, 4><<<grid, kVerifyThreads, 0, stream>>>(p);
+  } else if (steps >= kVerifyCluster * kVerifyWarps) {
+    p.tiles = tiles(2);
+    verify_kernel<E, kWide, 2><<<grid, kVerifyThreads, 0, stream>>>(p);
+  } else {
+    p.tiles = tiles(1);
+    verify_kernel<E, kWide, 1><<<grid, kVerifyThreads, 0, stream>>>(p);
+  }
 }
 
 template <typename E>
 void launch_verify(const VerifyParams& p, int B, bool wide, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(B) * kVerifyCluster);
   if (wide)
-    verify_kernel<E, true><<<grid, kVerifyThreads, 0, stream>>>(p);
+    launch_steps<E, true>(p, B, stream);
   else
-    verify_kernel<E, false><<<grid, kVerifyThreads, 0, stream>>>(p);
+    launch_steps<E, false>(p, B, stream);
 }
 
 }  // namespace
@@ -303,10 +389,8 @@ extern "C" pda_status pda_verify_drafts(int32_t* accepted, int32_t* next_tokens,
   const bool wide = aligned16(target_probs) && aligned16(draft_probs) &&
                     target_stride * e % 16 == 0 &&
                     (draft_probs == nullptr || draft_stride * e % 16 == 0);
-  const int tiles = (V + kTileTokens - 1) / kTileTokens;
   const VerifyParams p{accepted, next_tokens, target_probs, draft_probs, target_stride,
-                       draft_stride, tokens, query_start, accept_u, sample_u, error_word, T, V,
-                       (tiles + kVerifyCluster - 1) / kVerifyCluster};
+                       draft_stride, tokens, query_start, accept_u, sample_u, error_word, T, V, 0};
   if (dtype == PDA_F32)
     launch_verify<float>(p, B, wide, stream);
   else if (dtype == PDA_BF16)
