@@ -180,24 +180,16 @@ static_assert(kFits<false> && kFits<true>, "227 KB a block");
 // ---------------------------------------------------------------- the block's pipeline
 // The ids of a piece's blocks, 32 at a time: lane l holds that of block l % nbt of tile
 // l / nbt of the current group of tiles, the next group's already under way.
-template <bool kWindow>
-struct BlockIds : DescWindow<kWindow> {
+struct BlockIds {
   const int32_t* table;
   int bs, nbt, per_group;  // block size, blocks of a tile, tiles of a group
   int ja, nt, end, num_blocks;
-  int sinks, sink_tiles;
   int group, ids, next;
-
-  __device__ __forceinline__ int key_tile(int t) const {
-    if constexpr (kWindow) return ja + t + (ja + t >= sink_tiles ? this->skip : 0);
-    return ja + t;
-  }
 
   __device__ __forceinline__ int block_of(int gr, bool* used) const {
     const int lane = threadIdx.x & 31, t = gr * per_group + lane / nbt;
-    const long long key = static_cast<long long>(key_tile(t)) * kChunkKeys + (lane % nbt) * bs;
+    const long long key = static_cast<long long>(ja + t) * kChunkKeys + (lane % nbt) * bs;
     *used = t < nt && key < end;
-    if constexpr (kWindow) *used = *used && (key < sinks || key + bs > this->lowest);
     return *used ? static_cast<int>(key / bs) : 0;
   }
   __device__ __forceinline__ int fetch(int gr) const {
@@ -205,13 +197,7 @@ struct BlockIds : DescWindow<kWindow> {
     const int blk = block_of(gr, &used);
     return used ? table[blk] : 0;
   }
-  __device__ __forceinline__ void start(const ChunkParams& p, const Desc<kWindow>& d) {
-    if constexpr (kWindow) {
-      this->skip = d.skip;
-      this->lowest = d.lowest;
-      sinks = p.sinks;
-      sink_tiles = p.sink_tiles;
-    }
+  __device__ __forceinline__ void start(const ChunkParams& p, const Desc<false>& d) {
     bs = p.block_size;
     nbt = bs >= kChunkKeys ? 1 : kChunkKeys / bs;
     per_group = 32 / nbt;
@@ -224,7 +210,7 @@ struct BlockIds : DescWindow<kWindow> {
     next = fetch(0);
   }
   // Makes tile t's group current; *bad_from falls to the first key of a block whose id is out
-  // of range (any block stands in: the rows that see it become NaN), or, with a window, to 0.
+  // of range (any block stands in: the rows that see it become NaN).
   __device__ __forceinline__ void advance(int t, int* bad_from, int32_t* error_word) {
     if (t / per_group == group) return;
     group = t / per_group;
@@ -234,7 +220,7 @@ struct BlockIds : DescWindow<kWindow> {
         bool used;
         const int blk = block_of(group, &used);
         const int tile = ja + group * per_group + (threadIdx.x & 31) / nbt;
-        atomicMin(bad_from, kWindow ? 0 : max(blk * bs, tile * kChunkKeys));
+        atomicMin(bad_from, max(blk * bs, tile * kChunkKeys));
         atomic_or_error(error_word, PDA_DEVERR_BLOCK_ID);
         __threadfence_block();
       }
@@ -243,10 +229,70 @@ struct BlockIds : DescWindow<kWindow> {
     __syncwarp();
     next = fetch(group + 1);
   }
+  // Tiles of the piece; the key tile behind tile t, its blocks, and the keys from its first on
+  // that some row may see.
+  __device__ __forceinline__ int tiles() const { return nt; }
+  __device__ __forceinline__ int blocks() const { return nbt; }
+  __device__ __forceinline__ int keys(int t) const { return end - (ja + t) * kChunkKeys; }
   // Cache row of block `blk` of tile t (all lanes call).
   __device__ __forceinline__ int row(int t, int blk) const {
     const int id = __shfl_sync(kFullMask, ids, ((t - group * per_group) * nbt + blk) & 31);
-    return id * bs + (bs > kChunkKeys ? (key_tile(t) * kChunkKeys) % bs : 0);
+    return id * bs + (bs > kChunkKeys ? ((ja + t) * kChunkKeys) % bs : 0);
+  }
+};
+
+// The same with a window: tiles behind the first tokens' are `skip` key tiles further, and blocks
+// that no row of the item sees are not looked up (block 0 stands in). *bad_from falls to 0 where
+// an id is out of range: the rows look for themselves. Few registers: what the plan gives is read
+// where it is used (with it in registers of their own, the loading warps spilled, and every tile
+// took a seventh longer).
+struct WindowIds {
+  const ChunkParams& p;
+  const Desc<true>* d;
+  int group, ids, next;
+
+  __device__ __forceinline__ int bs_log2() const { return __ffs(p.block_size) - 1; }
+  __device__ __forceinline__ int nbt_log2() const { return max(0, 7 - bs_log2()); }
+  __device__ __forceinline__ int group_log2() const { return 5 - nbt_log2(); }
+  __device__ __forceinline__ int fetch(int gr) const {
+    const int lane = threadIdx.x & 31, n = nbt_log2();
+    const int t = (gr << (5 - n)) + (lane >> n), j = d->ja + t;
+    if (j >= d->jb) return 0;
+    const int key = d->key_tile(p, j) * kChunkKeys + ((lane & ((1 << n) - 1)) << bs_log2());
+    const bool used = key < d->end && (key < p.sinks || key + p.block_size > d->lowest);
+    return used ? p.block_tables[d->table + (key >> bs_log2())] : 0;
+  }
+  __device__ __forceinline__ void start(const ChunkParams&, const Desc<true>& piece) {
+    d = &piece;
+    group = -1;
+    next = fetch(0);
+  }
+  __device__ __forceinline__ void advance(int t, int* bad_from, int32_t* error_word) {
+    const int g = t >> group_log2();
+    if (g == group) return;
+    group = g;
+    ids = next;
+    if (ids < 0 || ids >= p.num_blocks) {
+      if (bad_from != nullptr) {
+        atomicMin(bad_from, 0);
+        atomic_or_error(error_word, PDA_DEVERR_BLOCK_ID);
+        __threadfence_block();
+      }
+      ids = 0;
+    }
+    __syncwarp();
+    next = fetch(g + 1);
+  }
+  __device__ __forceinline__ int tiles() const { return d->jb - d->ja; }
+  __device__ __forceinline__ int blocks() const { return 1 << nbt_log2(); }
+  __device__ __forceinline__ int keys(int t) const {
+    return d->end - d->key_tile(p, d->ja + t) * kChunkKeys;
+  }
+  __device__ __forceinline__ int row(int t, int blk) const {
+    const int id = __shfl_sync(
+        kFullMask, ids, (((t - (group << group_log2())) << nbt_log2()) + blk) & 31);
+    const int r = id << bs_log2();
+    return p.block_size > kChunkKeys && (d->key_tile(p, d->ja + t) & 1) != 0 ? r + kChunkKeys : r;
   }
 };
 
@@ -459,6 +505,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D, kFp8>;
   using Cuts = CutsOf<kWindow>;
   using Piece = Desc<kWindow>;
+  using Ids = std::conditional_t<kWindow, WindowIds, BlockIds>;
+  auto new_ids = [&] {
+    if constexpr (kWindow)
+      return WindowIds{p};
+    else
+      return BlockIds{};
+  };
   constexpr int kDescs = kDescsOf<kWindow>, kEdges = kEdgesOf<kWindow>;
   constexpr int NK = C::kK, NV = C::kV;
   extern __shared__ unsigned char smem_raw[];
@@ -549,9 +602,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = packed >> g_shift;
       const int pos = d.pos0 + min(tok, d.tokens - 1);  // this row's position
       const int first_pos = d.pos0 + ((single ? 0 : g * 128) >> g_shift);
-      // of this warp's first and last row
-      const int warp_pos = kWindow ? __shfl_sync(kFullMask, pos, 0) : 0;
-      const int warp_end = kWindow ? __shfl_sync(kFullMask, pos, 31) : 0;
       float sl = sl_all;  // of a score, in log2 units
       if (kFp8) {
         // this row of Q; where the groups share their rows, group 0's warps store it
@@ -574,13 +624,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m = -INFINITY, l = 0.f;
       for (int s = 0; s < steps; ++s) {
+        const int key0 = d.key_tile(p, ja + (single ? 2 * s + g : s)) * kChunkKeys;
         if (!warp_wait(&ms.s_full[g], s_phase)) {
           timed_out = true;
           break;
         }
         s_phase ^= 1;
         tc_fence_after();
-        const int key0 = d.key_tile(p, ja + (single ? 2 * s + g : s)) * kChunkKeys;
         float x[kChunkKeys];
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_ld32(x + 32 * k, tS + 32 * k);
@@ -589,6 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kChunkKeys; k += 32) tmem_arrived32(x + k);
         if constexpr (kWindow) {
           // masked where some row of this warp does not see the whole tile, by a bit per key
+          const int warp_pos = __shfl_sync(kFullMask, pos, 0);
+          const int warp_end = __shfl_sync(kFullMask, pos, 31);
           if (key0 + kChunkKeys - 1 > warp_pos ||
               (key0 <= warp_end - p.window && key0 + kChunkKeys > p.sinks)) {
 #pragma unroll
@@ -898,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // K: a box of a block's rows (128 at most), for each 64-element half of a row, or of codes
         const int nt = jb - ja;
         const int box_rows = min(p.block_size, kChunkKeys);
-        BlockIds<kWindow> ids;
+        Ids ids = new_ids();
         ids.start(p, d);
         for (int t = 0; t < nt; ++t) {
           ids.advance(t, &d.bad_from, p.error_word);
@@ -907,8 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             timed_out = true;
             break;
           }
-          const int keys = kv_end - ids.key_tile(t) * kChunkKeys;
-          const int boxes = min(ids.nbt, (keys + box_rows - 1) / box_rows);
+          const int keys = ids.keys(t);
+          const int boxes = min(ids.blocks(), (keys + box_rows - 1) / box_rows);
           if (lane == 0)
             mbar_arrive_expect_tx(full, boxes * box_rows * (kFp8 ? D : 2 * D));
           __syncwarp();
@@ -1105,17 +1157,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!d.valid) break;
         const int box_rows = min(p.block_size, kChunkKeys);
         const int kh = d.kh;
-        BlockIds<kWindow> ids;
+        Ids ids = new_ids();
         ids.start(p, d);
-        for (int t = 0; t < ids.nt; ++t) {
+        for (int t = 0; t < ids.tiles(); ++t) {
           ids.advance(t, nullptr, nullptr);
           uint64_t* full = kFp8 ? &ms.raw_full[1] : &ms.v_full[v_at];
           if (!warp_wait(kFp8 ? &ms.raw_empty[1] : &ms.v_empty[v_at], v_turn ^ 1)) {
             timed_out = true;
             break;
           }
-          const int keys = ids.end - ids.key_tile(t) * kChunkKeys;
-          const int boxes = min(ids.nbt, (keys + box_rows - 1) / box_rows);
+          const int keys = ids.keys(t);
+          const int boxes = min(ids.blocks(), (keys + box_rows - 1) / box_rows);
           if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_rows * (kFp8 ? D : 2 * D));
           __syncwarp();
           const int row = ids.row(t, lane);
