@@ -259,7 +259,8 @@ def alloc_workspace(B, H, H_kv, D, block_size=16, kv_dtype=torch.bfloat16, sm_ca
 
 
 def _windowed(window: int, sinks: int) -> bool:
-    _require(window >= 0 and sinks >= 0, "window and sinks must not be negative")
+    _require(0 <= window < 1 << 31 and 0 <= sinks < 1 << 31,
+             "window and sinks must not be negative, nor pass 31 bits")
     _require(window > 0 or sinks == 0, "sinks are the first tokens beside a window")
     return window > 0
 

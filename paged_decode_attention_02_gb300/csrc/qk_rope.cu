@@ -25,7 +25,7 @@ namespace {
 constexpr int kRopeThreads = 128;
 constexpr int kRopeVec = 8;        // elements of a lane
 constexpr int kRopeMaxHead = 256;  // largest D
-constexpr int kRopeWarpsPerSm = 32;  // spread few tokens over this many
+constexpr int kRopeWarpsPerSm = 16;  // spread few tokens over this many
 constexpr int kRopeSteps = 4;      // rows of a lane in flight
 
 struct RopeParams {
@@ -56,7 +56,7 @@ struct Raw {
   __device__ __forceinline__ void load(const E* p) {
 #pragma unroll
     for (int i = 0; i < kWords; i += 4) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i / 4);
+      const uint4 v = *(reinterpret_cast<const uint4*>(p) + i / 4);
       w[i] = v.x;
       w[i + 1] = v.y;
       w[i + 2] = v.z;

@@ -208,7 +208,8 @@ def test_two_streams_and_replays():
 
 def test_refusals():
     s = Window([3], [40], 8, 0, seed=12)
-    for kw in (dict(window=-1), dict(sinks=-1), dict(window=0, sinks=2)):
+    for kw in (dict(window=-1), dict(sinks=-1), dict(window=0, sinks=2),
+               dict(window=(1 << 32) + 4), dict(sinks=1 << 31)):
         with pytest.raises(ValueError):
             s.call(**kw)
     f = Window([3], [40], 8, 0, kv="fp8", seed=12)

@@ -189,7 +189,8 @@ def test_nvfp4_is_the_plain_call_on_the_visible_blocks():
 
 def test_refusals():
     s = Window([1], [40], 8, 0, seed=12)
-    for kw in (dict(window=-1), dict(sinks=-1), dict(window=0, sinks=2)):
+    for kw in (dict(window=-1), dict(sinks=-1), dict(window=0, sinks=2),
+               dict(window=(1 << 32) + 4), dict(sinks=1 << 31)):
         with pytest.raises(ValueError):
             s.decode(**kw)
     f = Window([1], [40], 8, 0, kv="fp8", seed=12)
