@@ -1,8 +1,9 @@
 """Thin ctypes binding over ``libpda.so`` (declared in ``include/pda.h``).
 
 Argument marshalling only: shapes, dtypes and devices are read off torch tensors and
-passed as plain pointers and sizes; every step of the computation runs in the library's
-CUDA kernels. The library must be built (``build_lib.build()``); if it is missing or
+passed as plain pointers and sizes (by ``ctypes``, or for the calls whose kernels are shorter
+than that by the extension module ``_marshal``); every step of the computation runs in the
+library's CUDA kernels. Both must be built (``build_lib.build()``); if one is missing or
 fails to load, every call raises, and nothing falls back to another implementation.
 """
 from __future__ import annotations
@@ -43,6 +44,7 @@ EXPORTED = [
 
 _lock = threading.Lock()
 _lib = None
+_marshal = None
 
 
 class PdaError(RuntimeError):
@@ -57,7 +59,7 @@ def lib_path() -> str:
 
 def load():
     """Load libpda.so and declare its C signatures. Raises if the library is not built."""
-    global _lib
+    global _lib, _marshal
     if _lib is not None:
         return _lib
     with _lock:
@@ -66,6 +68,9 @@ def load():
         path = lib_path()
         if not os.path.exists(path):
             raise RuntimeError(f"libpda.so is not built ({path}); run build_lib.build() first")
+        if not os.path.exists(build_lib.MARSHAL_PATH):
+            raise RuntimeError(f"the extension module is not built ({build_lib.MARSHAL_PATH}); "
+                               "run build_lib.build() first")
         lib = ctypes.CDLL(path)
         P, I, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
         lib.pda_status_string.argtypes = [I]
@@ -152,6 +157,11 @@ def load():
         # error_word, stream
         lib.pda_verify_drafts.argtypes = [P, P, P, P, LL, LL, P, P, P, P, I, I, I, I, P, P]
         lib.pda_verify_drafts.restype = I
+        from . import _marshal as marshal
+        marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.pda_qk_norm_rope_append, lib.pda_qk_norm_rope, lib.pda_paged_window_attention,
+            lib.pda_paged_window_chunk_attention, lib.pda_verify_drafts)))
+        _marshal = marshal
         _lib = lib
         return lib
 
@@ -258,43 +268,38 @@ def alloc_workspace(B, H, H_kv, D, block_size=16, kv_dtype=torch.bfloat16, sm_ca
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
 
 
-def _windowed(window: int, sinks: int) -> bool:
-    _require(0 <= window < 1 << 31 and 0 <= sinks < 1 << 31,
-             "window and sinks must not be negative, nor pass 31 bits")
-    _require(window > 0 or sinks == 0, "sinks are the first tokens beside a window")
-    return window > 0
-
-
-def _window_attention(out, q, k_cache, v_cache, block_scales, block_tables, context_lens,
-                      max_context_len, window, sinks, scales, kv_dtype, sm_cap, workspace,
-                      error_word, stream):
-    B, H, D = q.shape
-    NB, bs, H_kv, row = k_cache.shape
-    _require(block_tables.dim() == 2, "block_tables must be [B, max_blocks]")
-    _require(row == (D // 2 if kv_dtype == PDA_NVFP4 else D),
-             "q and the caches must agree in head size")
-    dev, i32, cache = _cuda_index(q), torch.int32, k_cache.dtype
-    k_bs, v_bs = block_scales
-    if kv_dtype == PDA_NVFP4:
-        _require(k_bs.shape == v_bs.shape == (NB, H_kv, bs, D // 16),
-                 "the block scales must be [NB, H_kv, bs, D / 16]")
+def _marshalled(name: str, dev: int, stream, *args):
+    """``_marshal``'s call ``name`` on device ``dev``, on ``stream`` or the device's current one."""
+    if dev < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    if _marshal is None:
+        load()
+    fn = getattr(_marshal, name)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        status = fn(dev, raw, *args)
     else:
-        _require(_dtype(k_cache) == kv_dtype, "the caches must hold FP8 E4M3 codes")
-    if workspace is None:  # from the launching stream's pool: reused there only
+        with torch.cuda.device(dev):
+            status = fn(dev, raw, *args)
+    if status != PDA_OK:
+        raise PdaError(status, "pda_" + name)
+
+
+def _window_attention(out, q, k_cache, v_cache, k_block_scales, v_block_scales, block_tables,
+                      context_lens, max_context_len, window, sinks, scale, k_scale, v_scale,
+                      kv_dtype, sm_cap, workspace, error_word, stream):
+    dev = q.get_device()
+    if workspace is None and dev >= 0:  # from the launching stream's pool: reused there only
+        B, H, D = q.shape
+        _, bs, H_kv, _ = k_cache.shape
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             n = ctypes.c_size_t(0)
             _check(load().pda_attention_workspace_size(B, H, H_kv, D, bs, kv_dtype, int(sm_cap),
                                                        ctypes.byref(n)), "workspace size")
             workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=q.device)
-    _call(load().pda_paged_window_attention, "pda_paged_window_attention", dev, stream,
-          _addr(out, dev, "out", None, q.shape), _addr(q, dev, "q"),
-          _addr(k_cache, dev, "k_cache"), _addr(v_cache, dev, "v_cache", cache, k_cache.shape),
-          _addr(k_bs, dev, "k_block_scales"), _addr(v_bs, dev, "v_block_scales"),
-          _addr(block_tables, dev, "block_tables", i32), block_tables.shape[1],
-          _addr(context_lens, dev, "context_lens", i32, (B,)), int(max_context_len), int(window),
-          int(sinks), B, H, H_kv, D, bs, NB, *scales, _dtype(q), kv_dtype, _dtype(out),
-          int(sm_cap), _addr(workspace, dev, "workspace"), workspace.nbytes,
-          _addr(error_word, dev, "error_word"))
+    _marshalled("paged_window_attention", dev, stream, out, q, k_cache, v_cache, k_block_scales,
+                v_block_scales, block_tables, context_lens, max_context_len, window, sinks, scale,
+                k_scale, v_scale, kv_dtype, sm_cap, workspace, error_word)
     return out
 
 
@@ -304,12 +309,12 @@ def paged_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens,
     """``out[b,h] = softmax(scale q[b,h] K^T) V`` over request b's paged history, or, with a
     ``window``, over its last ``window`` tokens and its first ``sinks`` (blocks without any of
     them are not read)."""
-    if _windowed(window, sinks):
-        _require(_dtype(k_cache) != PDA_FP8_E4M3, "an FP8 cache needs its scales: the _fp8 call")
-        return _window_attention(out, q, k_cache, v_cache, (None, None), block_tables,
-                                 context_lens, max_context_len, window, sinks,
-                                 (float(scale), 1.0, 1.0), _dtype(k_cache), sm_cap, workspace,
-                                 error_word, stream)
+    if window or sinks:
+        kv = _dtype(k_cache)
+        _require(kv != PDA_FP8_E4M3, "an FP8 cache needs its scales: the _fp8 call")
+        return _window_attention(out, q, k_cache, v_cache, None, None, block_tables, context_lens,
+                                 max_context_len, window, sinks, scale, 1.0, 1.0, kv, sm_cap,
+                                 workspace, error_word, stream)
     B, H, D = q.shape
     NB, bs, H_kv, D2 = k_cache.shape
     assert D == D2 and v_cache.shape == k_cache.shape and out.shape == q.shape
@@ -332,11 +337,10 @@ def paged_decode_attention_fp8(out, q, k_cache, v_cache, block_tables, context_l
                                stream=None, window: int = 0, sinks: int = 0):
     """Attention over an FP8 E4M3 cache: stored code c of K means decode(c) * k_scale.
     ``window`` and ``sinks`` as in ``paged_decode_attention``."""
-    if _windowed(window, sinks):
-        return _window_attention(out, q, k_cache, v_cache, (None, None), block_tables,
-                                 context_lens, max_context_len, window, sinks,
-                                 (float(scale), float(k_scale), float(v_scale)), PDA_FP8_E4M3,
-                                 sm_cap, workspace, error_word, stream)
+    if window or sinks:
+        return _window_attention(out, q, k_cache, v_cache, None, None, block_tables, context_lens,
+                                 max_context_len, window, sinks, scale, k_scale, v_scale,
+                                 PDA_FP8_E4M3, sm_cap, workspace, error_word, stream)
     B, H, D = q.shape
     NB, bs, H_kv, D2 = k_cache.shape
     assert D == D2 and v_cache.shape == k_cache.shape and out.shape == q.shape
@@ -361,11 +365,11 @@ def paged_decode_attention_nvfp4(out, q, k_data, v_data, k_block_scales, v_block
     """Attention over an NVFP4 cache: data [NB, bs, H_kv, D/2] uint8 (two E2M1 codes per
     byte, even element low), block scales [NB, H_kv, bs, D/16] uint8 (E4M3, per block and
     head-major). ``window`` and ``sinks`` as in ``paged_decode_attention``."""
-    if _windowed(window, sinks):
-        return _window_attention(out, q, k_data, v_data, (k_block_scales, v_block_scales),
+    if window or sinks:
+        return _window_attention(out, q, k_data, v_data, k_block_scales, v_block_scales,
                                  block_tables, context_lens, max_context_len, window, sinks,
-                                 (float(scale), float(k_scale), float(v_scale)), PDA_NVFP4,
-                                 sm_cap, workspace, error_word, stream)
+                                 scale, k_scale, v_scale, PDA_NVFP4, sm_cap, workspace,
+                                 error_word, stream)
     B, H, D = q.shape
     NB, bs, H_kv, half = k_data.shape
     assert 2 * half == D and v_data.shape == k_data.shape and out.shape == q.shape
@@ -673,34 +677,6 @@ def rope_frequencies(rope_dim: int, base: float = 10000.0, stretch: float = 1.0,
     return torch.from_numpy(fixed).to(device or "cuda")
 
 
-def _heads(t, dev: int, name: str, dtype, shape):
-    """Address, token stride and end of head rows [T, heads, D]: a token's heads dense, tokens
-    any distance apart."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}; all tensors must live on one CUDA device")
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, "
-                         f"not {t.dtype} {tuple(t.shape)}")
-    T, n, D = shape
-    row, at = n * D, t.data_ptr()
-    if T == 0:
-        return at, row, at
-    by_token, by_head, by_element = t.stride()
-    if (D > 1 and by_element != 1) or (n > 1 and by_head != D):
-        raise ValueError(f"{name}: a token's heads must be dense")
-    if T == 1:
-        by_token = row
-    return at, by_token, at + ((T - 1) * by_token + row) * t.element_size()
-
-
-def _apart(out: int, size: int, other, name: str, may_be_same: int = -1):
-    """Refuses an output of ``size`` bytes that overlaps ``other`` (as from ``_heads``), unless it
-    is the same memory and ``other``'s tokens are ``may_be_same`` apart."""
-    at, stride, end = other
-    if out < end and at < out + size and not (out == at and stride == may_be_same):
-        raise ValueError(f"an output overlaps {name}")
-
-
 def qk_norm_rope_append(q_out, q, k, v, k_cache, v_cache, slot_mapping, positions, freqs,
                         q_weight=None, k_weight=None, eps: float = 1e-6,
                         interleaved: bool = False, attention_factor: float = 1.0,
@@ -711,31 +687,9 @@ def qk_norm_rope_append(q_out, q, k, v, k_cache, v_cache, slot_mapping, position
     inputs may be slices of one projection's output. ``freqs`` come from ``rope_frequencies``;
     the first ``2 * len(freqs)`` elements of a head turn. Over an FP8 cache, ``k / k_scale`` and
     ``v / v_scale`` are rounded to codes."""
-    _require(q.dim() == 3 and k.dim() == 3 and k_cache.dim() == 4 and freqs.dim() == 1,
-             "q and k must be [T, heads, D], the caches [NB, bs, H_kv, D], freqs [rope_dim / 2]")
-    T, H, D = q.shape
-    NB, bs, H_kv, D2 = k_cache.shape
-    _require(D == D2, "q and the caches must agree in head size")
-    dev, dt, i32 = _cuda_index(q), q.dtype, torch.int32
-    kv = (T, H_kv, D)
-    qh = _heads(q, dev, "q", dt, (T, H, D))
-    kh, vh = _heads(k, dev, "k", dt, kv), _heads(v, dev, "v", dt, kv)
-    out = _addr(q_out, dev, "q_out", dt, q.shape)
-    size = q_out.nbytes
-    _apart(out, size, qh, "q", H * D)
-    _apart(out, size, kh, "k")
-    _apart(out, size, vh, "v")
-    _call(load().pda_qk_norm_rope_append, "pda_qk_norm_rope_append", dev, stream,
-          out, qh[0], kh[0], vh[0], qh[1], kh[1], vh[1],
-          _addr(k_cache, dev, "k_cache"),
-          _addr(v_cache, dev, "v_cache", k_cache.dtype, k_cache.shape),
-          _addr(slot_mapping, dev, "slot_mapping", i32, (T,)),
-          _addr(positions, dev, "positions", i32, (T,)),
-          _addr(freqs, dev, "freqs", torch.int64), 2 * freqs.shape[0], int(bool(interleaved)),
-          float(attention_factor), _addr(q_weight, dev, "q_weight", dt, (D,)),
-          _addr(k_weight, dev, "k_weight", dt, (D,)), float(eps), T, H, H_kv, D, bs, NB,
-          float(k_scale), float(v_scale), _dtype(q), _dtype(k_cache),
-          _addr(error_word, dev, "error_word"))
+    _marshalled("qk_norm_rope_append", q.get_device(), stream, q_out, q, k, v, k_cache, v_cache,
+                slot_mapping, positions, freqs, q_weight, k_weight, eps, interleaved,
+                attention_factor, k_scale, v_scale, error_word)
     return q_out
 
 
@@ -744,24 +698,8 @@ def qk_norm_rope(q_out, k_out, q, k, positions, freqs, q_weight=None, k_weight=N
                  stream=None):
     """``qk_norm_rope_append``'s norm and rotation into dense ``q_out`` and ``k_out`` (which may
     be ``q`` and ``k``), without a cache."""
-    _require(q.dim() == 3 and k.dim() == 3 and freqs.dim() == 1,
-             "q and k must be [T, heads, D], freqs [rope_dim / 2]")
-    T, H, D = q.shape
-    H_kv = k.shape[1]
-    dev, dt, i32 = _cuda_index(q), q.dtype, torch.int32
-    qh, kh = _heads(q, dev, "q", dt, (T, H, D)), _heads(k, dev, "k", dt, (T, H_kv, D))
-    q_at, k_at = _addr(q_out, dev, "q_out", dt, q.shape), _addr(k_out, dev, "k_out", dt, k.shape)
-    q_size, k_size = q_out.nbytes, k_out.nbytes
-    _apart(q_at, q_size, qh, "q", H * D)
-    _apart(q_at, q_size, kh, "k")
-    _apart(k_at, k_size, qh, "q")
-    _apart(k_at, k_size, kh, "k", H_kv * D)
-    _apart(k_at, k_size, (q_at, 0, q_at + q_size), "the other output")
-    _call(load().pda_qk_norm_rope, "pda_qk_norm_rope", dev, stream, q_at, k_at, qh[0], kh[0],
-          qh[1], kh[1], _addr(positions, dev, "positions", i32, (T,)),
-          _addr(freqs, dev, "freqs", torch.int64), 2 * freqs.shape[0], int(bool(interleaved)),
-          float(attention_factor), _addr(q_weight, dev, "q_weight", dt, (D,)),
-          _addr(k_weight, dev, "k_weight", dt, (D,)), float(eps), T, H, H_kv, D, _dtype(q))
+    _marshalled("qk_norm_rope", q.get_device(), stream, q_out, k_out, q, k, positions, freqs,
+                q_weight, k_weight, eps, interleaved, attention_factor)
     return q_out, k_out
 
 
@@ -789,7 +727,7 @@ def alloc_chunk_workspace(B, T, H, H_kv, D, block_size=16, kv_dtype=torch.bfloat
 
 
 def _chunk(fn, what, scales, out, q, k_cache, v_cache, block_tables, context_lens, query_start,
-           max_context_len, sm_cap, workspace, error_word, stream, dtypes, window, sinks):
+           max_context_len, sm_cap, workspace, error_word, stream, dtypes):
     _require(q.dim() == 3 and k_cache.dim() == 4 and block_tables.dim() == 2,
              "q must be [T, H, D], the caches [NB, bs, H_kv, D], block_tables [B, max_blocks]")
     T, H, D = q.shape
@@ -801,20 +739,30 @@ def _chunk(fn, what, scales, out, q, k_cache, v_cache, block_tables, context_len
         with torch.cuda.device(dev), torch.cuda.stream(stream):
             workspace = alloc_chunk_workspace(B, T, H, H_kv, D, bs, k_cache.dtype, sm_cap,
                                               q.device)
-    windows = ()
-    if _windowed(window, sinks):
-        fn, what = load().pda_paged_window_chunk_attention, "pda_paged_window_chunk_attention"
-        windows = (int(window), int(sinks))
-        scales = (*scales, 1.0, 1.0)[:3]
-        dtypes = (dtypes[0], _dtype(k_cache))
     _call(fn, what, dev, stream, _addr(out, dev, "out", q.dtype, q.shape), _addr(q, dev, "q"),
           _addr(k_cache, dev, "k_cache"),
           _addr(v_cache, dev, "v_cache", k_cache.dtype, k_cache.shape),
           _addr(block_tables, dev, "block_tables", i32), max_blocks,
           _addr(context_lens, dev, "context_lens", i32, (B,)),
-          _addr(query_start, dev, "query_start", i32, (B + 1,)), int(max_context_len), *windows,
-          B, T, H, H_kv, D, bs, NB, *scales, *dtypes, int(sm_cap), _addr(workspace, dev, "workspace"),
+          _addr(query_start, dev, "query_start", i32, (B + 1,)), int(max_context_len), B, T, H,
+          H_kv, D, bs, NB, *scales, *dtypes, int(sm_cap), _addr(workspace, dev, "workspace"),
           workspace.numel() * workspace.element_size(), _addr(error_word, dev, "error_word"))
+    return out
+
+
+def _window_chunk(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                  max_context_len, window, sinks, scale, k_scale, v_scale, codes, sm_cap, workspace,
+                  error_word, stream):
+    dev = q.get_device()
+    if workspace is None and dev >= 0:  # from the launching stream's pool: reused there only
+        T, H, D = q.shape
+        _, bs, H_kv, _ = k_cache.shape
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            workspace = alloc_chunk_workspace(block_tables.shape[0], T, H, H_kv, D, bs,
+                                              k_cache.dtype, sm_cap, q.device)
+    _marshalled("paged_window_chunk_attention", dev, stream, out, q, k_cache, v_cache, block_tables,
+                context_lens, query_start, max_context_len, window, sinks, scale, k_scale, v_scale,
+                codes, sm_cap, workspace, error_word)
     return out
 
 
@@ -825,12 +773,14 @@ def paged_chunk_attention(out, q, k_cache, v_cache, block_tables, context_lens, 
     ``q`` [T, H, D], the last of its ``context_lens[b]``) over its paged history up to and
     including themselves; with a ``window``, over the last ``window`` tokens up to and including
     themselves and the first ``sinks``."""
-    _require(not window or _dtype(k_cache) != PDA_FP8_E4M3,
-             "an FP8 cache needs its scales: the _fp8 call")
+    if window or sinks:
+        return _window_chunk(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                             max_context_len, window, sinks, scale, 1.0, 1.0, False, sm_cap,
+                             workspace, error_word, stream)
     return _chunk(load().pda_paged_chunk_attention, "pda_paged_chunk_attention",
                   (float(scale),), out, q, k_cache, v_cache, block_tables, context_lens,
                   query_start, max_context_len, sm_cap, workspace, error_word, stream,
-                  (_dtype(q), _dtype(k_cache)), window, sinks)
+                  (_dtype(q), _dtype(k_cache)))
 
 
 def paged_chunk_attention_fp8(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
@@ -839,24 +789,15 @@ def paged_chunk_attention_fp8(out, q, k_cache, v_cache, block_tables, context_le
                               stream=None, window: int = 0, sinks: int = 0):
     """``paged_chunk_attention`` over an FP8 E4M3 cache: stored code c of K means
     decode(c) * k_scale."""
+    if window or sinks:
+        return _window_chunk(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                             max_context_len, window, sinks, scale, k_scale, v_scale, True, sm_cap,
+                             workspace, error_word, stream)
     _require(_dtype(k_cache) == PDA_FP8_E4M3, "the caches must hold FP8 E4M3 codes")
     return _chunk(load().pda_paged_chunk_attention_fp8, "pda_paged_chunk_attention_fp8",
                   (float(scale), float(k_scale), float(v_scale)), out, q, k_cache, v_cache,
                   block_tables, context_lens, query_start, max_context_len, sm_cap, workspace,
-                  error_word, stream, (_dtype(q),), window, sinks)
-
-
-def _rows(t, dev: int, name: str, dtype, shape):
-    """Address and row stride of [T, V] rows, dense within a row."""
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}; all tensors must live on one CUDA device")
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, "
-                         f"not {t.dtype} {tuple(t.shape)}")
-    by_row, by_element = t.stride()
-    if shape[1] > 1 and by_element != 1:
-        raise ValueError(f"{name}: rows must be dense")
-    return t.data_ptr(), by_row if shape[0] > 1 else shape[1]
+                  error_word, stream, (_dtype(q),))
 
 
 def verify_drafts(accepted, next_tokens, target_probs, draft_probs, tokens, query_start, accept_u,
@@ -866,18 +807,6 @@ def verify_drafts(accepted, next_tokens, target_probs, draft_probs, tokens, quer
     and the token after them (``next_tokens`` [B]), by speculative sampling from the given
     uniforms. Row r of ``target_probs`` [T, V] (of ``draft_probs``, which may be None for certain
     drafts) is the target's (the draft model's) distribution of the token behind row r's."""
-    _require(target_probs.dim() == 2 and accepted.dim() == 1,
-             "target_probs must be [T, V] and accepted [B]")
-    T, V = target_probs.shape
-    B = accepted.shape[0]
-    dev, dt, i32, f32 = _cuda_index(target_probs), target_probs.dtype, torch.int32, torch.float32
-    p, p_stride = _rows(target_probs, dev, "target_probs", dt, (T, V))
-    q, q_stride = ((None, 0) if draft_probs is None else
-                   _rows(draft_probs, dev, "draft_probs", dt, (T, V)))
-    _call(load().pda_verify_drafts, "pda_verify_drafts", dev, stream,
-          _addr(accepted, dev, "accepted", i32), _addr(next_tokens, dev, "next_tokens", i32, (B,)),
-          p, q, p_stride, q_stride, _addr(tokens, dev, "tokens", i32, (T,)),
-          _addr(query_start, dev, "query_start", i32, (B + 1,)),
-          _addr(accept_u, dev, "accept_u", f32, (T,)), _addr(sample_u, dev, "sample_u", f32, (B,)),
-          T, B, V, _dtype(target_probs), _addr(error_word, dev, "error_word"))
+    _marshalled("verify_drafts", target_probs.get_device(), stream, accepted, next_tokens,
+                target_probs, draft_probs, tokens, query_start, accept_u, sample_u, error_word)
     return accepted, next_tokens

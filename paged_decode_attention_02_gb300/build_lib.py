@@ -1,7 +1,9 @@
 """Builds ``libpda.so`` in-tree from ``csrc/*.cu`` with nvcc for sm_103a.
 
 Each translation unit is compiled in parallel to ``_build/`` and linked with
-``nvcc -shared`` (static CUDA runtime, so the library needs no LD_LIBRARY_PATH). Run as
+``nvcc -shared`` (static CUDA runtime, so the library needs no LD_LIBRARY_PATH). Beside them the
+host compiler builds ``_marshal``, the extension module that hands tensors to the library's short
+calls. Run as
 ``python -m paged_decode_attention_02_gb300.build_lib`` or call ``build()``.
 """
 from __future__ import annotations
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libpda.so")
+MARSHAL_SRC = os.path.join(PKG, "marshal", "marshal.cpp")
+MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 
@@ -42,14 +47,37 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "pda.h"), __file__]
+        os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "pda.h"), __file__, MARSHAL_SRC]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(MARSHAL_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MARSHAL_PATH))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _build_marshal():
+    """The extension module: torch's and Python's headers, no CUDA code."""
+    import torch
+
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no host C++ compiler")
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    lib = os.path.join(root, "lib")
+    tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + INCLUDE, "-isystem", cuda,
+           "-isystem", os.path.join(root, "include"), "-isystem",
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem",
+           sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", MARSHAL_SRC, "-o",
+           tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building {MARSHAL_PATH} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL_PATH)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -69,7 +97,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(compile_one, _sources()))
+        marshal.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -60,12 +60,13 @@ pda_status launch_chunk(void* out, const void* q, const void* k_cache, const voi
   if (static_cast<long long>(num_blocks) * block_size >= (1ll << 31) ||
       static_cast<long long>(B) * max_blocks_per_seq >= (1ll << 31))
     return PDA_ERR_UNSUPPORTED;
-  ChunkParams p{out,     q,      k_cache,   v_cache,
-                      block_tables, context_lens, query_start, error_word,
-                      scale * k_scale * 1.4426950408889634f,
-                      v_scale, B,      T,         H,
-                      H_kv,    H / H_kv, max_blocks_per_seq, max_context_len,
-                      block_size, num_blocks, 0, 0, 0};
+  ChunkParams p{out,          q,            k_cache,     v_cache,
+                block_tables, context_lens, query_start, error_word,
+                scale * k_scale * 1.4426950408889634f,
+                v_scale,      B,            T,           H,
+                H_kv,         H / H_kv,     max_blocks_per_seq, max_context_len,
+                block_size,   num_blocks,   0,           0,
+                0};
   // a window no shorter than any history is none
   if (window > 0 && window < std::min<long long>(max_context_len, static_cast<long long>(
                                                      max_blocks_per_seq) * block_size)) {
