@@ -294,8 +294,8 @@ pda_status launch(const ChunkParams& p, int dev, int sms, bool capped, float* pa
   static_assert(smem <= 232448, "227 KB a block");
   static std::atomic<bool> raised[64];
   if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(chunk_f32_kernel<D, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             smem) != cudaSuccess)
+    if (cudaFuncSetAttribute(chunk_f32_kernel<D, kWindow>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return PDA_ERR_CUDA;
     if (dev < 64) raised[dev].store(true, std::memory_order_release);
   }

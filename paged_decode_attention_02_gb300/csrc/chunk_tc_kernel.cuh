@@ -44,6 +44,17 @@
 // would reach the output. Warps 12 to 15 zero the rows behind the end, replace non-finite
 // values by zeros and note their rows, and the epilogue adds those values back to the rows
 // that do see them.
+//
+// With a sliding window (kWindow) an item's tiles are those of the first `sinks` tokens and, from
+// its first token's window on, the rest: `skip` key tiles between them are left out, and nothing
+// but the key a tile starts at (key_tile) knows of the gap. Tiles at the window's lower border
+// and the end of the first tokens are masked per row and cleaned as the diagonal's are, and their
+// blocks that no row of the item sees are not looked up: block 0 stands in, whose values are
+// masked and cleaned too. 4096 tokens over 4096 + 64 keys of 32/8 heads run at 1313 TFLOP/s of
+// visible pairs (213 us), ragged prompts over 513 keys take 162 us: item borders, with five of an
+// item's seven tiles masked (5 % of the time) and cleaned (5-8 %).
+#pragma once
+
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -169,7 +180,8 @@ struct Misc {
 template <int D, bool kFp8, bool kWindow>
 constexpr size_t smem_bytes() {
   using C = Cfg<D, kFp8>;
-  return 1024 + static_cast<size_t>(C::kK + C::kV + 2) * C::kTile + 2 * C::kRaw + sizeof(Misc<kWindow>);
+  return 1024 + static_cast<size_t>(C::kK + C::kV + 2) * C::kTile + 2 * C::kRaw +
+         sizeof(Misc<kWindow>);
 }
 template <bool kWindow>
 constexpr bool kFits =
