@@ -151,6 +151,15 @@ cudaStream_t stream_of(PyObject* o) {
   return reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(o)));
 }
 
+// Makes the C call without the interpreter's lock (a launch may wait for room in its queue).
+template <typename F, typename... Args>
+int released(F f, Args... args) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int status = f(args...);
+  PyEval_RestoreThread(state);
+  return status;
+}
+
 // ---------------------------------------------------------------- the calls
 int rope_append(PyObject* const* a) {
   const int dev = static_cast<int>(whole(a[0], "device"));
@@ -170,8 +179,9 @@ int rope_append(PyObject* const* a) {
   apart(out, qr, true, "q");
   apart(out, kr, false, "k");
   apart(out, vr, false, "v");
-  return rope_append_fn(
-      out.at, qr.at, kr.at, vr.at, qr.stride, kr.stride, vr.stride, dense(a[6], dev, "k_cache"),
+  return released(
+      rope_append_fn, out.at, qr.at, kr.at, vr.at, qr.stride, kr.stride, vr.stride,
+      dense(a[6], dev, "k_cache"),
       dense(a[7], dev, "v_cache", kc.scalar_type(), {NB, bs, H_kv, D}),
       ints(a[8], dev, "slot_mapping", {T}), ints(a[9], dev, "positions", {T}),
       static_cast<const uint64_t*>(dense(a[10], dev, "freqs", ScalarType::Long, {freqs.size(0)})),
@@ -199,8 +209,8 @@ int rope(PyObject* const* a) {
   apart(ko, qr, false, "q");
   apart(ko, kr, true, "k");
   apart(qo, ko, false, "the other output");
-  return rope_fn(
-      qo.at, ko.at, qr.at, kr.at, qr.stride, kr.stride, ints(a[6], dev, "positions", {T}),
+  return released(
+      rope_fn, qo.at, ko.at, qr.at, kr.at, qr.stride, kr.stride, ints(a[6], dev, "positions", {T}),
       static_cast<const uint64_t*>(dense(a[7], dev, "freqs", ScalarType::Long, {freqs.size(0)})),
       2 * size(freqs, 0), PyObject_IsTrue(a[11]), number(a[12], "attention_factor"),
       dense(a[8], dev, "q_weight", type, {D}), dense(a[9], dev, "k_weight", type, {D}),
@@ -236,8 +246,8 @@ int window(PyObject* const* a) {
     k_bs = dense(a[6], dev, "k_block_scales", type, {NB, H_kv, bs, D / 16});
     v_bs = dense(a[7], dev, "v_block_scales", type, {NB, H_kv, bs, D / 16});
   }
-  return window_fn(
-      dense(a[2], dev, "out", out.scalar_type(), {B, H, D}), dense(a[3], dev, "q"),
+  return released(
+      window_fn, dense(a[2], dev, "out", out.scalar_type(), {B, H, D}), dense(a[3], dev, "q"),
       dense(a[4], dev, "k_cache"),
       dense(a[5], dev, "v_cache", kc.scalar_type(), {NB, bs, H_kv, kc.size(3)}), k_bs, v_bs,
       ints(a[8], dev, "block_tables", {B, tables.size(1)}), size(tables, 1),
@@ -264,8 +274,8 @@ int window_chunk(PyObject* const* a) {
   if ((kv == PDA_FP8_E4M3) != codes)
     refuse(codes ? "the caches must hold FP8 E4M3 codes"
                  : "an FP8 cache needs its scales: the _fp8 call");
-  return window_chunk_fn(
-      dense(a[2], dev, "out", q.scalar_type(), {T, H, D}), dense(a[3], dev, "q"),
+  return released(
+      window_chunk_fn, dense(a[2], dev, "out", q.scalar_type(), {T, H, D}), dense(a[3], dev, "q"),
       dense(a[4], dev, "k_cache"), dense(a[5], dev, "v_cache", kc.scalar_type(), {NB, bs, H_kv, D}),
       ints(a[6], dev, "block_tables", {B, tables.size(1)}), size(tables, 1),
       ints(a[7], dev, "context_lens", {B}), ints(a[8], dev, "query_start", {B + 1}),
@@ -285,12 +295,13 @@ int verify(PyObject* const* a) {
   const Rows target = rows(a[4], dev, "target_probs", type, {T, V});
   Rows draft{};
   if (a[5] != Py_None) draft = rows(a[5], dev, "draft_probs", type, {T, V});
-  return verify_fn(ints(a[2], dev, "accepted", {B}), ints(a[3], dev, "next_tokens", {B}),
-                   target.at, draft.at, target.stride, draft.stride,
-                   ints(a[6], dev, "tokens", {T}), ints(a[7], dev, "query_start", {B + 1}),
-                   static_cast<float*>(dense(a[8], dev, "accept_u", ScalarType::Float, {T})),
-                   static_cast<float*>(dense(a[9], dev, "sample_u", ScalarType::Float, {B})), T, B,
-                   V, dtype(p, "target_probs"), error_word(a[10], dev), stream_of(a[1]));
+  return released(
+      verify_fn, ints(a[2], dev, "accepted", {B}), ints(a[3], dev, "next_tokens", {B}), target.at,
+      draft.at, target.stride, draft.stride, ints(a[6], dev, "tokens", {T}),
+      ints(a[7], dev, "query_start", {B + 1}),
+      static_cast<float*>(dense(a[8], dev, "accept_u", ScalarType::Float, {T})),
+      static_cast<float*>(dense(a[9], dev, "sample_u", ScalarType::Float, {B})), T, B, V,
+      dtype(p, "target_probs"), error_word(a[10], dev), stream_of(a[1]));
 }
 
 // ---------------------------------------------------------------- the module
