@@ -6,13 +6,16 @@
  * query token over its whole cached history, and the gather of one request's scattered
  * KV blocks into a contiguous buffer for transfer. For the step that comes before it, the
  * new tokens of prompts, prompt chunks or drafts, it holds the attention of a chunk over the
- * same cache and the block tables and slots built on the GPU from the requests' lengths.
+ * same cache and the block tables and slots built on the GPU from the requests' lengths; for
+ * windowed models and drafted tokens, the same attention with a sliding window, the norm and
+ * rotation of queries and keys on their way into the cache, and the verification of drafts.
  *
  * Conventions shared by every entry point:
  *  - Every pointer argument is a DEVICE pointer unless its comment says "host". The caller
  *    owns all memory; the library allocates nothing. Apart from the fixed scratch array of
  *    pda_paged_decode_attention_noalloc it keeps no state between calls.
- *  - Tensors are dense and row-major with exactly the shapes given; no strides.
+ *  - Tensors are dense and row-major with exactly the shapes given; strides only where a call
+ *    takes them.
  *  - KV caches are [num_blocks, block_size, H_kv, D]: physical block p holds block_size
  *    consecutive tokens, token row r of block p is at ((p * block_size + r) * H_kv) * D.
  *    (Page "From PagedAttention to Prefill-Decode disaggregation", sec. 2.2 step 1: the

@@ -113,11 +113,8 @@ class Step:
 def test_vocabularies(kv, drafted, V):
     n = [1, 2, 5, 9, 3, 1, 4]
     s = Step(n, V, kv, drafted, seed=V)
-    assert s.got(check=V > 7) == s.want if V > 7 else True
-    if V <= 7:  # rows may be all zero there
-        got = s.got(check=False)
-        assert got == s.want
-        s.err.zero_()
+    assert s.got(check=V > 7) == s.want  # rows of a few tokens may be all zero: an error, and -1
+    s.err.zero_()
 
 
 @pytest.mark.parametrize("V,gap", [(1000, 8), (1000, 3), (999, 1), (131072, 0), (150001, 0)])

@@ -146,8 +146,8 @@ def test_two_streams_and_replays_with_their_own_workspaces():
         g.replay()
         eager = a.decode(check=False, workspace=ws[1])
         torch.cuda.synchronize()
-        assert torch.equal(oa[cut == 0 and slice(0) or slice(None)].isnan(),
-                           eager[cut == 0 and slice(0) or slice(None)].isnan())
+        # (a cut row may see blocks that have been given back: NaN)
+        assert torch.equal(oa.isnan(), eager.isnan())
         ok = ~eager.isnan()
         assert torch.equal(oa[ok], eager[ok])
     a.err.zero_()
