@@ -518,7 +518,7 @@ __device__ __forceinline__ unsigned arrive_add(unsigned long long* counter,
 
 // Claims the next pool chunk and returns its index (NW k or more once the pool is used up).
 // The tag mix leaves the low 16 bits alone, so the count adds without unmixing; a call makes
-// at most NW k + NW claims, below 2^16.
+// NW k + NW claims, below 2^16, and its last one resets the counter.
 __device__ __forceinline__ unsigned claim_chunk(unsigned long long* c) {
   return static_cast<unsigned>(atomicAdd(c, 1ull) & 0xffffull);
 }
@@ -1186,6 +1186,11 @@ __global__ void __launch_bounds__(warps_for_mode(G, MODE, std::is_same<KV, nvfp4
       c = __shfl_sync(kFullMask, c, 0);
     }
   }
+  // Every warp ends with one claim past the pool, so NW k + NW claims are made, as many as there
+  // are units, and whoever makes the last leaves the counter with nothing claimed: a captured call
+  // keeps its number, and its next replay would find the pool used up.
+  if (pool && lane == 0 && static_cast<int>(c) + 1 == un.units())
+    atomicExch(p.ws_claim, arrival_reset(p.call));
 }
 
 // ------------------------------------------------------------------ the launch's choice of kernel
