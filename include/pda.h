@@ -268,7 +268,8 @@ pda_status pda_paged_decode_attention_nvfp4(void* out, const void* q, const void
  * The pages describe no windowed model; this is what its layers need beside
  * pda_paged_decode_attention (page "Disaggregated LLM Serving", sec. 1), of which everything else
  * holds. Blocks that hold no visible token are not looked up or read: their table entries may be
- * anything, and their memory another request's. What blocks hold in rows that are not visible does
+ * anything (pda_kv_assign_blocks wants them negative once their blocks are given back), and their
+ * memory another request's. What blocks hold in rows that are not visible does
  * not reach the output.
  *
  *  window         >= 1; sinks >= 0. A window as long as the history is none.
@@ -499,7 +500,8 @@ pda_status pda_kv_unpack_block_scales_batched(const void* const* ins,
  * free_list[0 .. free_count) holds the ids of the free blocks, the last one on top. With
  * need_b = ceil(context_lens[b] / block_size):
  *  - a row that holds more than it needs gives back entries [need_b, blocks_held[b]) of its
- *    table; all rows' entries are pushed in order of b, then of the entry;
+ *    table; all rows' entries are pushed in order of b, then of the entry. A negative entry holds
+ *    no block and is passed over;
  *  - after that, a row that holds fewer gets entries [blocks_held[b], need_b), popped one at
  *    a time in the same order. The first row whose blocks are not all there, and every later
  *    row that grows, get none (PDA_DEVERR_NO_BLOCKS); their counts stay.
@@ -520,11 +522,16 @@ pda_status pda_kv_unpack_block_scales_batched(const void* const* ins,
  *                 write; its shared_blocks[b] falls to blocks_held[b], so that they are
  *                 given back. It is set anew, with the entries and blocks_held[b], when the
  *                 row takes its next request.
+ *  Blocks that the caller gives back itself out of a row's middle, as those that have left a
+ *  sliding window: it puts their ids on the stack, and makes their entries negative before the
+ *  next call. An entry that keeps such an id is given back a second time with its row, and two
+ *  rows then share the block, which this call cannot see.
  *  A row with context_lens < 0 or beyond max_blocks_per_seq * block_size, or with blocks_held
  *  outside [0, max_blocks_per_seq], is left as it is (PDA_DEVERR_CONTEXT_LEN). free_count
  *  outside [0, num_blocks] (PDA_DEVERR_NO_BLOCKS), or more blocks given back than the list
- *  holds (PDA_DEVERR_BLOCK_ID), leaves everything as it is. An id out of range that is moved
- *  sets PDA_DEVERR_BLOCK_ID. Buffers not named as shareable must not overlap.
+ *  holds (PDA_DEVERR_BLOCK_ID), leaves everything as it is. An entry of num_blocks or more that
+ *  would be given back is passed over, and an id out of range that is popped goes into the table;
+ *  both set PDA_DEVERR_BLOCK_ID. Buffers not named as shareable must not overlap.
  *  B <= 8192 and B * max_blocks_per_seq < 2^31, else PDA_ERR_UNSUPPORTED. B == 0 copies the
  *  count.
  */
