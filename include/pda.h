@@ -748,7 +748,7 @@ pda_status pda_paged_window_chunk_attention(
  *    if none of them is positive), or p_r at the request's last row, the first token t whose
  *    sum of weights up to t exceeds sample_u[b] times their sum.
  * So the request goes on with its first a drafts and next_tokens[b], and its length falls by
- * d - a.
+ * d - a. (A request without rows has no d: its length stays.)
  *
  *  accepted, next_tokens [B] int32, written.
  *  target_probs   [T, V] in dtype (PDA_F32, PDA_BF16, PDA_F16), rows target_stride elements apart
