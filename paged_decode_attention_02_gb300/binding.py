@@ -4,11 +4,12 @@ Argument marshalling only: shapes, dtypes and devices are read off torch tensors
 passed as plain pointers and sizes (by ``ctypes``, or for the calls whose kernels are shorter
 than that by the extension module ``_marshal``); every step of the computation runs in the
 library's CUDA kernels. Both must be built (``build_lib.build()``); if one is missing or
-fails to load, every call raises, and nothing falls back to another implementation.
+fails to load, every call that needs it raises, and nothing falls back to another implementation.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -59,7 +60,7 @@ def lib_path() -> str:
 
 def load():
     """Load libpda.so and declare its C signatures. Raises if the library is not built."""
-    global _lib, _marshal
+    global _lib
     if _lib is not None:
         return _lib
     with _lock:
@@ -68,9 +69,6 @@ def load():
         path = lib_path()
         if not os.path.exists(path):
             raise RuntimeError(f"libpda.so is not built ({path}); run build_lib.build() first")
-        if not os.path.exists(build_lib.MARSHAL_PATH):
-            raise RuntimeError(f"the extension module is not built ({build_lib.MARSHAL_PATH}); "
-                               "run build_lib.build() first")
         lib = ctypes.CDLL(path)
         P, I, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
         lib.pda_status_string.argtypes = [I]
@@ -157,13 +155,29 @@ def load():
         # error_word, stream
         lib.pda_verify_drafts.argtypes = [P, P, P, P, LL, LL, P, P, P, P, I, I, I, I, P, P]
         lib.pda_verify_drafts.restype = I
-        from . import _marshal as marshal
-        marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.pda_qk_norm_rope_append, lib.pda_qk_norm_rope, lib.pda_paged_window_attention,
-            lib.pda_paged_window_chunk_attention, lib.pda_verify_drafts)))
-        _marshal = marshal
         _lib = lib
         return lib
+
+
+def _load_marshal():
+    """Load the extension module, which the calls through ``_marshalled`` need. Raises if it is not
+    built for this torch and Python."""
+    global _marshal
+    lib = load()
+    with _lock:
+        if _marshal is None:
+            path = build_lib.marshal_path()
+            if not os.path.exists(path):
+                raise RuntimeError(f"the extension module is not built ({path}); "
+                                   "run build_lib.build() first")
+            spec = importlib.util.spec_from_file_location(__package__ + "._marshal", path)
+            marshal = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(marshal)
+            marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.pda_qk_norm_rope_append, lib.pda_qk_norm_rope, lib.pda_paged_window_attention,
+                lib.pda_paged_window_chunk_attention, lib.pda_verify_drafts)))
+            _marshal = marshal
+        return _marshal
 
 
 def status_string(status: int) -> str:
@@ -272,9 +286,7 @@ def _marshalled(name: str, dev: int, stream, *args):
     """``_marshal``'s call ``name`` on device ``dev``, on ``stream`` or the device's current one."""
     if dev < 0:
         raise ValueError("tensors must live on a CUDA device")
-    if _marshal is None:
-        load()
-    fn = getattr(_marshal, name)
+    fn = getattr(_marshal or _load_marshal(), name)
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if dev == torch._C._cuda_getDevice():
         status = fn(dev, raw, *args)

@@ -1,9 +1,10 @@
 """Builds ``libpda.so`` in-tree from ``csrc/*.cu`` with nvcc for sm_103a.
 
 Each translation unit is compiled in parallel to ``_build/`` and linked with
-``nvcc -shared`` (static CUDA runtime, so the library needs no LD_LIBRARY_PATH). Beside them the
+``nvcc -shared`` (static CUDA runtime, so the library needs no LD_LIBRARY_PATH). Beside it the
 host compiler builds ``_marshal``, the extension module that hands tensors to the library's short
-calls. Run as
+calls; its file name says for which torch and Python, so that another of them asks for a file of
+its own. Run as
 ``python -m paged_decode_attention_02_gb300.build_lib`` or call ``build()``.
 """
 from __future__ import annotations
@@ -23,7 +24,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libpda.so")
 MARSHAL_SRC = os.path.join(PKG, "marshal", "marshal.cpp")
-MARSHAL_PATH = os.path.join(PKG, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 
@@ -47,27 +47,43 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "pda.h"), __file__, MARSHAL_SRC]
+        os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "pda.h"), __file__]
+
+
+def _newer(path, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path)
+                                        for d in deps)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(MARSHAL_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(MARSHAL_PATH))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _newer(LIB_PATH, _deps())
+
+
+def marshal_path() -> str:
+    """The extension module of the torch and Python that run now."""
+    import torch
+
+    abi = "" if torch._C._GLIBCXX_USE_CXX11_ABI else "-oldabi"
+    return os.path.join(PKG, f"_marshal-torch{torch.__version__}{abi}" +
+                        (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+
+
+def marshal_up_to_date() -> bool:
+    return _newer(marshal_path(), [MARSHAL_SRC, os.path.join(INCLUDE, "pda.h"), __file__])
 
 
 def _build_marshal():
     """The extension module: torch's and Python's headers, no CUDA code."""
     import torch
 
+    path = marshal_path()
     cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
     if cxx is None:
         raise RuntimeError("no host C++ compiler")
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     lib = os.path.join(root, "lib")
-    tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + INCLUDE, "-isystem", cuda,
            "-isystem", os.path.join(root, "include"), "-isystem",
            os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem",
@@ -76,13 +92,23 @@ def _build_marshal():
            tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"building {MARSHAL_PATH} failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MARSHAL_PATH)
+        raise RuntimeError(f"building {path} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB_PATH
+    """Builds what is not up to date and returns the library's path. Where only the extension module
+    cannot be built, the library is in place when this raises, and the calls through it work."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        marshal = None if not force and marshal_up_to_date() else ex.submit(_build_marshal)
+        if force or not up_to_date():
+            _build_library(verbose)
+        if marshal is not None:
+            marshal.result()
+    return LIB_PATH
+
+
+def _build_library(verbose: bool):
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
 
@@ -97,9 +123,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(compile_one, _sources()))
-        marshal.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
