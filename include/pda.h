@@ -573,7 +573,9 @@ pda_status pda_kv_build_slots(int32_t* slot_mapping, int32_t* query_start,
  * its request (what pda_qk_norm_rope_append turns its queries and keys by).
  *
  *  positions      [N] int32, written whole: 0 for rows behind the last token and for the tokens
- *                 of a request in error or padded. Everything else as pda_kv_build_slots.
+ *                 of a request whose length is in error or 0 (padded). A token whose block id is
+ *                 out of range has no slot, but its position all the same.
+ *                 Everything else as pda_kv_build_slots.
  */
 pda_status pda_kv_build_slots_positions(int32_t* slot_mapping, int32_t* positions,
                                         int32_t* query_start, const int32_t* query_lens,
