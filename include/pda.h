@@ -596,8 +596,9 @@ pda_status pda_kv_build_slots_positions(int32_t* slot_mapping, int32_t* position
  *  - the first R = rope_dim elements turn in pairs by the angle of the token's position p:
  *      (a, b) -> (a c - b s, b c + a s),  c, s = attention_factor * cos, sin (2 pi p F_i / 2^64),
  *    pair i < R / 2 being elements (i, i + R / 2), or (2 i, 2 i + 1) where `interleaved` is not 0.
- * v is copied. k and v of token t go to slot_mapping[t] as by pda_kv_append (< 0: not written;
- * too large: PDA_DEVERR_SLOT, not written); q_out is written for every token.
+ * v is copied (a 16-bit NaN as the type's usual one). k and v of token t go to slot_mapping[t] as
+ * by pda_kv_append (< 0: not written; too large: PDA_DEVERR_SLOT, not written; no slot twice);
+ * q_out is written for every token.
  *
  *  q_out          [T, H, D] in dtype, dense. May be q itself where q is dense.
  *  q, k, v        [T, H, D], [T, H_kv, D], [T, H_kv, D] in dtype; a token's heads are dense, and
