@@ -92,6 +92,14 @@ float number(PyObject* o, const char* name) {
   }
   return static_cast<float>(v);
 }
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be true or false");
+  }
+  return v != 0;
+}
 
 pda_dtype dtype(const at::Tensor& t, const char* name) {
   switch (t.scalar_type()) {
@@ -185,7 +193,7 @@ int rope_append(PyObject* const* a) {
       dense(a[7], dev, "v_cache", kc.scalar_type(), {NB, bs, H_kv, D}),
       ints(a[8], dev, "slot_mapping", {T}), ints(a[9], dev, "positions", {T}),
       static_cast<const uint64_t*>(dense(a[10], dev, "freqs", ScalarType::Long, {freqs.size(0)})),
-      2 * size(freqs, 0), PyObject_IsTrue(a[14]), number(a[15], "attention_factor"),
+      2 * size(freqs, 0), truth(a[14], "interleaved"), number(a[15], "attention_factor"),
       dense(a[11], dev, "q_weight", type, {D}), dense(a[12], dev, "k_weight", type, {D}),
       number(a[13], "eps"), T, H, H_kv, D, bs, NB, number(a[16], "k_scale"),
       number(a[17], "v_scale"), dtype(q, "q"), dtype(kc, "k_cache"), error_word(a[18], dev),
@@ -212,7 +220,7 @@ int rope(PyObject* const* a) {
   return released(
       rope_fn, qo.at, ko.at, qr.at, kr.at, qr.stride, kr.stride, ints(a[6], dev, "positions", {T}),
       static_cast<const uint64_t*>(dense(a[7], dev, "freqs", ScalarType::Long, {freqs.size(0)})),
-      2 * size(freqs, 0), PyObject_IsTrue(a[11]), number(a[12], "attention_factor"),
+      2 * size(freqs, 0), truth(a[11], "interleaved"), number(a[12], "attention_factor"),
       dense(a[8], dev, "q_weight", type, {D}), dense(a[9], dev, "k_weight", type, {D}),
       number(a[10], "eps"), T, H, H_kv, D, dtype(q, "q"), stream_of(a[1]));
 }
@@ -266,7 +274,7 @@ int window_chunk(PyObject* const* a) {
   ranked(q, 3, "q must be [T, H, D]");
   ranked(kc, 4, "the caches must be [NB, bs, H_kv, D]");
   ranked(tables, 2, "block_tables must be [B, max_blocks]");
-  const bool codes = PyObject_IsTrue(a[15]);
+  const bool codes = truth(a[15], "codes");
   const int T = size(q, 0), H = size(q, 1), D = size(q, 2), B = size(tables, 0);
   const int NB = size(kc, 0), bs = size(kc, 1), H_kv = size(kc, 2);
   if (kc.size(3) != D) refuse("q and the caches must agree in head size");
